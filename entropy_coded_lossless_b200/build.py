@@ -10,8 +10,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libshn.so")
-SOURCES = ["capi.cu", "histogram.cu", "build_tables.cu", "encode.cu", "decode.cu", "noalloc.cu", "offload.cu"]
+SOURCES = ["capi.cu", "histogram.cu", "build_tables.cu", "encode.cu", "decode.cu", "noalloc.cu", "offload.cu",
+           "kv_capi.cu", "kv_plan.cu", "kv_store.cu", "kv_attn.cu"]
 HEADERS = [os.path.join(CSRC, "shn_internal.cuh"), os.path.join(ROOT, "include", "shn.h")]
+# the paged KV cache's sources (kv_*.cu) alone include these
+KV_HEADERS = [os.path.join(CSRC, "kv_internal.cuh"), os.path.join(ROOT, "include", "shn_kv.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
@@ -26,14 +29,15 @@ def _stale(target, deps):
 
 def build(force: bool = False, verbose: bool = False) -> str:
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    if not force and not _stale(LIB, srcs + HEADERS):
+    if not force and not _stale(LIB, srcs + HEADERS + KV_HEADERS):
         return LIB
     obj_dir = os.path.join(HERE, "_build")
     os.makedirs(obj_dir, exist_ok=True)
     objs = []
     for src in srcs:
         obj = os.path.join(obj_dir, os.path.basename(src) + ".o")
-        if force or _stale(obj, [src] + HEADERS):
+        deps = [src] + HEADERS + (KV_HEADERS if os.path.basename(src).startswith("kv_") else [])
+        if force or _stale(obj, deps):
             cmd = [NVCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
             if verbose:
                 cmd.insert(1, "-Xptxas=-v")

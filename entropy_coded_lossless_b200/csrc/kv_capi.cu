@@ -1,0 +1,209 @@
+// kv_capi.cu — the extern "C" entry points of include/shn_kv.h: argument checks and launches.
+// No device allocation and no synchronisation.
+#include "kv_internal.cuh"
+
+using namespace shn;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool power_of_two(uint32_t x) { return x && (x & (x - 1)) == 0; }
+uint32_t log2_of(uint32_t x) {
+  uint32_t l = 0;
+  while ((1u << l) < x) ++l;
+  return l;
+}
+
+// Largest group of query heads per key head: 64 rows of one query fit every kernel's row tile.
+constexpr uint32_t kMaxGroup = 64;
+
+int check_cache(const shn_kv_cache* c) {
+  if (!c || !c->d_k || !c->d_v || !c->d_k_scale || !c->d_v_scale) return SHN_ERR_INVALID_ARG;
+  if (!aligned(c->d_k, 16) || !aligned(c->d_v, 16) || !aligned(c->d_k_scale, 4) || !aligned(c->d_v_scale, 4))
+    return SHN_ERR_INVALID_ARG;
+  if (c->n_pages == 0 || c->kv_heads == 0 || c->kv_heads > 1024) return SHN_ERR_INVALID_ARG;
+  if (!power_of_two(c->page_tokens) || c->page_tokens < 16 || c->page_tokens > 1024) return SHN_ERR_INVALID_ARG;
+  if ((uint64_t)c->n_pages * c->page_tokens >= (1ull << 31)) return SHN_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return SHN_ERR_UNSUPPORTED;
+  return SHN_OK;
+}
+
+KvPages pages_of(const shn_kv_cache* c) {
+  return KvPages{c->d_k, c->d_v, c->d_k_scale, c->d_v_scale, c->n_pages, c->kv_heads, log2_of(c->page_tokens)};
+}
+
+// The workspace's status word, cleared on the stream. Null on failure (err set).
+DeviceStatus* clear_status(void* d_work, cudaStream_t s) {
+  DeviceStatus* st = static_cast<DeviceStatus*>(d_work);
+  return cudaMemsetAsync(st, 0, sizeof(DeviceStatus), s) == cudaSuccess ? st : nullptr;
+}
+
+int check_work(const void* d_work, size_t have, size_t need) {
+  if (!d_work || !aligned(d_work, 256)) return SHN_ERR_INVALID_ARG;
+  return have < need ? SHN_ERR_WORKSPACE : SHN_OK;
+}
+
+// rows of activations: 16-byte aligned, token stride a multiple of 8 values that holds a token
+bool rows_ok(const void* p, uint64_t stride, uint64_t heads, uint32_t head_dim, uint64_t n_tokens) {
+  return p && aligned(p, 16) && stride % 8 == 0 && (n_tokens <= 1 || stride >= heads * head_dim);
+}
+
+int check_attn(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32_t q_heads, const shn_kv_cache* cache,
+               const int32_t* d_block_table, uint32_t max_blocks, const int32_t* d_kv_len, uint32_t n_reqs,
+               const uint16_t* d_out, uint64_t out_stride) {
+  const int e = check_cache(cache);
+  if (e != SHN_OK) return e;
+  if (q_heads == 0 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > kMaxGroup) return SHN_ERR_INVALID_ARG;
+  if (n_tokens >= (1u << 31) / q_heads || n_reqs >= (1u << 31) - 1) return SHN_ERR_INVALID_ARG;
+  if (n_reqs && (!d_kv_len || (max_blocks && !d_block_table))) return SHN_ERR_INVALID_ARG;
+  if ((uint64_t)max_blocks * cache->page_tokens >= (1ull << 31)) return SHN_ERR_INVALID_ARG;
+  if (n_tokens && (!rows_ok(d_q, q_stride, q_heads, cache->head_dim, n_tokens) ||
+                   !rows_ok(d_out, out_stride, q_heads, cache->head_dim, n_tokens)))
+    return SHN_ERR_INVALID_ARG;
+  return SHN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int shn_kv_check_cache(const shn_kv_cache* c) { return check_cache(c); }
+
+int shn_kv_plan(const int32_t* d_ctx_len, const int32_t* d_new_len, uint32_t n_reqs, uint32_t page_tokens,
+                int32_t* d_block_table, uint32_t max_blocks, const int32_t* d_free_pages, uint32_t n_free,
+                const int32_t* d_free_head, int32_t* d_free_next, int32_t* d_cu_new, int32_t* d_kv_len,
+                int32_t* d_positions, int32_t* d_slots, uint32_t max_tokens, void* d_work, size_t work_bytes,
+                void* stream) {
+  if (!power_of_two(page_tokens) || page_tokens < 16 || page_tokens > 1024) return SHN_ERR_INVALID_ARG;
+  if (n_reqs >= (1u << 31) - 1 || max_tokens >= (1u << 31) || n_free >= (1u << 31) ||
+      (uint64_t)max_blocks * page_tokens >= (1ull << 31))
+    return SHN_ERR_INVALID_ARG;
+  if (!d_free_head || !d_free_next || !d_cu_new || (n_free && !d_free_pages)) return SHN_ERR_INVALID_ARG;
+  if (n_reqs && (!d_ctx_len || !d_new_len || !d_kv_len || (max_blocks && !d_block_table))) return SHN_ERR_INVALID_ARG;
+  if (max_tokens && (!d_positions || !d_slots)) return SHN_ERR_INVALID_ARG;
+  const int e = check_work(d_work, work_bytes, SHN_KV_WORKSPACE_BYTES);
+  if (e != SHN_OK) return e;
+  KvPlanArgs a;
+  a.ctx = d_ctx_len, a.fresh = d_new_len, a.n = n_reqs, a.log2_pt = log2_of(page_tokens);
+  a.max_blocks = max_blocks, a.n_free = n_free, a.max_tokens = max_tokens;
+  a.table = d_block_table, a.free_pages = d_free_pages, a.free_head = d_free_head, a.free_next = d_free_next;
+  a.cu = d_cu_new, a.kv_len = d_kv_len, a.positions = d_positions, a.slots = d_slots;
+  a.st = static_cast<DeviceStatus*>(d_work);  // the kernel sets it, without a launch to clear it
+  return launch_kv_plan(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
+}
+
+int shn_kv_store(const uint16_t* d_q, uint64_t q_stride, uint32_t q_heads, const uint16_t* d_k, uint64_t k_stride,
+                 const uint16_t* d_v, uint64_t v_stride, uint32_t n_tokens, const int32_t* d_positions,
+                 const int32_t* d_slots, const uint16_t* d_q_weight, const uint16_t* d_k_weight, float eps,
+                 const float* d_cos_sin, uint32_t n_positions, uint32_t rot_dim, uint32_t pairs,
+                 const shn_kv_cache* cache, uint16_t* d_q_out, uint64_t q_out_stride, void* d_work,
+                 size_t work_bytes, void* stream) {
+  int e = check_cache(cache);
+  if (e != SHN_OK) return e;
+  const uint32_t d = cache->head_dim;
+  if (n_tokens >= (1u << 31) || q_heads > 65536 || pairs > 1) return SHN_ERR_INVALID_ARG;
+  if (rot_dim > d || rot_dim % 16 || (rot_dim != 0) != (d_cos_sin != nullptr)) return SHN_ERR_INVALID_ARG;
+  if (!aligned(d_cos_sin, 16) || !aligned(d_q_weight, 16) || !aligned(d_k_weight, 16)) return SHN_ERR_INVALID_ARG;
+  if ((d_q_weight || d_k_weight) && !(eps >= 0.f)) return SHN_ERR_INVALID_ARG;
+  if ((d_q == nullptr) != (q_heads == 0) && n_tokens) return SHN_ERR_INVALID_ARG;
+  if (n_tokens) {
+    if (!rows_ok(d_k, k_stride, cache->kv_heads, d, n_tokens) || !rows_ok(d_v, v_stride, cache->kv_heads, d, n_tokens))
+      return SHN_ERR_INVALID_ARG;
+    if (q_heads && (!rows_ok(d_q, q_stride, q_heads, d, n_tokens) || !rows_ok(d_q_out, q_out_stride, q_heads, d, n_tokens)))
+      return SHN_ERR_INVALID_ARG;
+    if (d_q == d_q_out && q_stride != q_out_stride && n_tokens > 1) return SHN_ERR_INVALID_ARG;
+    if (!d_slots || (rot_dim && !d_positions)) return SHN_ERR_INVALID_ARG;
+  }
+  e = check_work(d_work, work_bytes, SHN_KV_WORKSPACE_BYTES);
+  if (e != SHN_OK) return e;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KvStoreArgs a;
+  a.q = d_q, a.k = d_k, a.v = d_v, a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.q_heads = q_heads, a.n_tokens = n_tokens, a.positions = d_positions, a.slots = d_slots;
+  a.q_weight = d_q_weight, a.k_weight = d_k_weight, a.eps = eps;
+  a.cos_sin = d_cos_sin, a.n_positions = n_positions, a.rot = rot_dim, a.pairs = pairs;
+  a.q_out = d_q_out, a.q_out_stride = q_out_stride;
+  a.st = clear_status(d_work, s);
+  if (!a.st) return SHN_ERR_CUDA;
+  if (n_tokens == 0) return SHN_OK;
+  return launch_kv_store(pages_of(cache), d, a, sm_count_for_launch(), s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
+}
+
+int shn_kv_load(const shn_kv_cache* cache, const int32_t* d_slots, uint32_t n_tokens, uint16_t* d_k_out,
+                uint64_t k_stride, uint16_t* d_v_out, uint64_t v_stride, void* d_work, size_t work_bytes,
+                void* stream) {
+  int e = check_cache(cache);
+  if (e != SHN_OK) return e;
+  if (n_tokens >= (1u << 31)) return SHN_ERR_INVALID_ARG;
+  if (n_tokens) {
+    if (!d_slots || (d_k_out && !rows_ok(d_k_out, k_stride, cache->kv_heads, cache->head_dim, n_tokens)) ||
+        (d_v_out && !rows_ok(d_v_out, v_stride, cache->kv_heads, cache->head_dim, n_tokens)))
+      return SHN_ERR_INVALID_ARG;
+  }
+  e = check_work(d_work, work_bytes, SHN_KV_WORKSPACE_BYTES);
+  if (e != SHN_OK) return e;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KvLoadArgs a;
+  a.slots = d_slots, a.n_tokens = n_tokens, a.k_out = d_k_out, a.v_out = d_v_out;
+  a.k_stride = k_stride, a.v_stride = v_stride;
+  a.st = clear_status(d_work, s);
+  if (!a.st) return SHN_ERR_CUDA;
+  if (n_tokens == 0 || (!d_k_out && !d_v_out)) return SHN_OK;
+  return launch_kv_load(pages_of(cache), cache->head_dim, a, sm_count_for_launch(), s) == cudaSuccess ? SHN_OK
+                                                                                                      : SHN_ERR_CUDA;
+}
+
+int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32_t q_heads,
+                       const shn_kv_cache* cache, const int32_t* d_block_table, uint32_t max_blocks,
+                       const int32_t* d_cu_q, const int32_t* d_kv_len, uint32_t n_reqs, float softmax_scale,
+                       uint16_t* d_out, uint64_t out_stride, void* d_work, size_t work_bytes, void* stream) {
+  int e = check_attn(d_q, q_stride, n_tokens, q_heads, cache, d_block_table, max_blocks, d_kv_len, n_reqs, d_out,
+                     out_stride);
+  if (e != SHN_OK) return e;
+  if (n_reqs && !d_cu_q) return SHN_ERR_INVALID_ARG;
+  e = check_work(d_work, work_bytes, SHN_KV_WORKSPACE_BYTES);
+  if (e != SHN_OK) return e;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KvAttnArgs a = {};
+  a.q = d_q, a.q_stride = q_stride, a.n_tokens = n_tokens, a.q_heads = q_heads;
+  a.table = d_block_table, a.max_blocks = max_blocks, a.cu_q = d_cu_q, a.kv_len = d_kv_len, a.n_reqs = n_reqs;
+  a.scale = softmax_scale, a.out = d_out, a.out_stride = out_stride;
+  a.st = clear_status(d_work, s);
+  if (!a.st) return SHN_ERR_CUDA;
+  if (n_tokens == 0 || n_reqs == 0) return SHN_OK;
+  return launch_kv_attn(pages_of(cache), cache->head_dim, a, s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
+}
+
+size_t shn_kv_attn_shared_workspace_bytes(const shn_kv_cache* cache, uint32_t n_reqs, uint32_t q_heads) {
+  if (check_cache(cache) != SHN_OK || q_heads == 0 || q_heads % cache->kv_heads ||
+      q_heads / cache->kv_heads > kMaxGroup || n_reqs >= (1u << 31) / q_heads)
+    return 0;
+  return SHN_KV_WORKSPACE_BYTES;
+}
+
+int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, uint32_t q_heads,
+                       const shn_kv_cache* cache, const int32_t* d_prefix_pages, uint32_t n_prefix_pages,
+                       const int32_t* d_prefix_len, const int32_t* d_block_table, uint32_t max_blocks,
+                       const int32_t* d_kv_len, float softmax_scale, uint16_t* d_out, uint64_t out_stride,
+                       void* d_work, size_t work_bytes, void* stream) {
+  int e = check_attn(d_q, q_stride, n_reqs, q_heads, cache, d_block_table, max_blocks, d_kv_len, n_reqs, d_out,
+                     out_stride);
+  if (e != SHN_OK) return e;
+  if (!d_prefix_len || (n_prefix_pages && !d_prefix_pages) ||
+      (uint64_t)n_prefix_pages * cache->page_tokens >= (1ull << 31))
+    return SHN_ERR_INVALID_ARG;
+  e = check_work(d_work, work_bytes, shn_kv_attn_shared_workspace_bytes(cache, n_reqs, q_heads));
+  if (e != SHN_OK) return e;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KvAttnArgs a = {};
+  a.q = d_q, a.q_stride = q_stride, a.n_tokens = n_reqs, a.q_heads = q_heads;
+  a.table = d_block_table, a.max_blocks = max_blocks, a.kv_len = d_kv_len, a.n_reqs = n_reqs;
+  a.prefix_pages = d_prefix_pages, a.n_prefix_pages = n_prefix_pages, a.prefix_len = d_prefix_len;
+  a.scale = softmax_scale, a.out = d_out, a.out_stride = out_stride;
+  a.st = clear_status(d_work, s);
+  if (!a.st) return SHN_ERR_CUDA;
+  if (n_reqs == 0) return SHN_OK;
+  return launch_kv_attn(pages_of(cache), cache->head_dim, a, s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,93 @@
+// kv_internal.cuh — what the kernels of the paged KV cache (include/shn_kv.h) share.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "../../include/shn_kv.h"
+#include "shn_internal.cuh"
+
+namespace shn {
+
+// The cache as kernels take it.
+struct KvPages {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  uint32_t n_pages;
+  uint32_t kv_heads;
+  uint32_t log2_pt;  // log2(page_tokens)
+};
+
+// Row (head h) of a slot, in rows of head_dim values: also the index of its scale. Slots stay below
+// 2^31, rows can pass 2^32.
+__device__ __forceinline__ uint64_t kv_row(const KvPages& c, uint32_t page, uint32_t h, uint32_t t_in_page) {
+  return (((uint64_t)page * c.kv_heads + h) << c.log2_pt) + t_in_page;
+}
+__device__ __forceinline__ uint64_t kv_row_of_slot(const KvPages& c, uint32_t slot, uint32_t h) {
+  return kv_row(c, slot >> c.log2_pt, h, slot & ((1u << c.log2_pt) - 1));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// (lo, hi) rounded to nearest even, packed
+__device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+struct KvPlanArgs {
+  const int32_t *ctx, *fresh;
+  uint32_t n, log2_pt, max_blocks, n_free, max_tokens;
+  int32_t* table;
+  const int32_t *free_pages, *free_head;
+  int32_t *free_next, *cu, *kv_len, *positions, *slots;
+  DeviceStatus* st;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t s);
+
+struct KvStoreArgs {
+  const uint16_t *q, *k, *v;
+  uint64_t q_stride, k_stride, v_stride;
+  uint32_t q_heads, n_tokens;
+  const int32_t *positions, *slots;
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  const float* cos_sin;
+  uint32_t n_positions, rot, pairs;
+  uint16_t* q_out;
+  uint64_t q_out_stride;
+  DeviceStatus* st;
+};
+cudaError_t launch_kv_store(const KvPages& c, uint32_t head_dim, const KvStoreArgs& a, int sm_count, cudaStream_t s);
+
+struct KvLoadArgs {
+  const int32_t* slots;
+  uint32_t n_tokens;
+  uint16_t *k_out, *v_out;
+  uint64_t k_stride, v_stride;
+  DeviceStatus* st;
+};
+cudaError_t launch_kv_load(const KvPages& c, uint32_t head_dim, const KvLoadArgs& a, int sm_count, cudaStream_t s);
+
+// Both attention calls. cu_q is null for single tokens (request r has query r).
+struct KvAttnArgs {
+  const uint16_t* q;
+  uint64_t q_stride;
+  uint32_t n_tokens, q_heads;
+  const int32_t* table;
+  uint32_t max_blocks;
+  const int32_t *cu_q, *kv_len;
+  uint32_t n_reqs;
+  const int32_t* prefix_pages;  // null: no prefix
+  uint32_t n_prefix_pages;
+  const int32_t* prefix_len;
+  float scale;
+  uint16_t* out;
+  uint64_t out_stride;
+  DeviceStatus* st;
+};
+cudaError_t launch_kv_attn(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, cudaStream_t s);
+
+}  // namespace shn

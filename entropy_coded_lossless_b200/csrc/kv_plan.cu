@@ -1,0 +1,169 @@
+// kv_plan.cu — block tables and slot maps of a step from the requests' lengths (shn_kv_plan).
+//
+// Two exclusive sums over the requests (new tokens; pages to take), then one independent item per new
+// token and per new page, each finding its request by a search in the sums. Little is read or written
+// (about 16 bytes per request and 8 per token), so the call is bound by latency: one launch, and one
+// cluster of up to 8 blocks so that a barrier can separate the reading of the free-list head from its
+// update. Every block forms the sums for itself, which costs less than handing them around.
+#include "kv_internal.cuh"
+
+namespace shn {
+namespace {
+
+constexpr int kThreads = 1024;
+
+struct Sum2 {
+  long long tokens, pages;
+};
+
+__device__ __forceinline__ long long pages_of(long long tokens, uint32_t log2_pt) {
+  return (tokens + (1ll << log2_pt) - 1) >> log2_pt;
+}
+
+__global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
+  __shared__ Sum2 before[kThreads + 1];  // sums in front of each thread's run of requests
+  __shared__ Sum2 warp_sum[32];
+  __shared__ uint32_t bad_code, bad_detail;
+  const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t rank = blockIdx.x, ranks = gridDim.x;  // one cluster: its blocks are the grid
+  const uint32_t run = (a.n + kThreads - 1) / kThreads;
+  const uint32_t r0 = min(a.n, t * run), r1 = min(a.n, r0 + run);
+  if (t == 0) bad_code = 0, bad_detail = 0xFFFFFFFFu;
+  const long long head = *a.free_head;
+  __syncthreads();
+
+  Sum2 own = {0, 0};
+  bool negative = false, wide = false;
+  uint32_t bad_r = 0xFFFFFFFFu;
+  for (uint32_t r = r0; r < r1; ++r) {
+    const long long c = a.ctx[r], f = a.fresh[r];
+    const long long p = pages_of(c + f, a.log2_pt);
+    const bool neg = c < 0 || f < 0 || c + f > 0x7FFFFFFFll, wd = p > (long long)a.max_blocks;
+    if ((neg || wd) && bad_r == 0xFFFFFFFFu) bad_r = r;
+    negative |= neg;
+    wide |= wd;
+    own.tokens += f;
+    own.pages += p - pages_of(c, a.log2_pt);
+  }
+  if (negative || wide) {
+    atomicMin(&bad_detail, bad_r);
+    atomicMax(&bad_code, negative ? 2u : 1u);
+  }
+  Sum2 inc = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(~0u, inc.tokens, d), y = __shfl_up_sync(~0u, inc.pages, d);
+    if (lane >= (uint32_t)d) inc.tokens += x, inc.pages += y;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    Sum2 w = warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(~0u, w.tokens, d), y = __shfl_up_sync(~0u, w.pages, d);
+      if (lane >= (uint32_t)d) w.tokens += x, w.pages += y;
+    }
+    warp_sum[lane] = w;
+  }
+  __syncthreads();
+  const Sum2 base = warp ? warp_sum[warp - 1] : Sum2{0, 0};
+  before[t] = {base.tokens + inc.tokens - own.tokens, base.pages + inc.pages - own.pages};
+  if (t == 0) before[kThreads] = warp_sum[31];
+  __syncthreads();
+  const Sum2 total = before[kThreads];
+
+  uint32_t code = bad_code == 2 ? SHN_ERR_INVALID_ARG : bad_code == 1 ? SHN_ERR_CAPACITY : SHN_OK;
+  uint32_t detail = code ? bad_detail : 0;
+  if (code == SHN_OK && (head < 0 || head > (long long)a.n_free)) code = SHN_ERR_INVALID_ARG;
+  if (code == SHN_OK && (total.tokens > (long long)a.max_tokens || head + total.pages > (long long)a.n_free))
+    code = SHN_ERR_CAPACITY;
+  const bool ok = code == SHN_OK;
+  if (rank == 0 && t == 0) a.st->status = code, a.st->detail = detail;
+  // every block has read the head (and the first has set the status) before anything is written
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  if (rank == 0 && t == 0) {
+    *a.free_next = (int32_t)(ok ? head + total.pages : head);
+    a.cu[a.n] = (int32_t)(ok ? total.tokens : 0);
+  }
+  if (t % ranks == rank) {
+    long long tok = before[t].tokens;
+    for (uint32_t r = r0; r < r1; ++r) {
+      a.cu[r] = (int32_t)(ok ? tok : 0);
+      a.kv_len[r] = ok ? a.ctx[r] + a.fresh[r] : 0;
+      tok += a.fresh[r];
+    }
+  }
+  const int32_t page_limit = (int32_t)(0x7FFFFFFFu >> a.log2_pt);
+  const uint32_t pt_mask = (1u << a.log2_pt) - 1;
+  // new pages into the table
+  if (ok) {
+    for (long long i = rank * kThreads + t; i < total.pages; i += (long long)ranks * kThreads) {
+      uint32_t lo = 0, hi = kThreads;
+      while (hi - lo > 1) {
+        const uint32_t m = (lo + hi) >> 1;
+        if (before[m].pages <= i) lo = m; else hi = m;
+      }
+      long long j = i - before[lo].pages;
+      for (uint32_t r = lo * run;; ++r) {
+        const long long have = pages_of(a.ctx[r], a.log2_pt);
+        const long long need = pages_of((long long)a.ctx[r] + a.fresh[r], a.log2_pt) - have;
+        if (j < need) {
+          const int32_t p = a.free_pages[head + i];
+          a.table[(uint64_t)r * a.max_blocks + have + j] = p;
+          if (p < 0 || p >= page_limit) report(a.st, SHN_ERR_INVALID_ARG, r);
+          break;
+        }
+        j -= need;
+      }
+    }
+  }
+  for (uint32_t i = rank * kThreads + t; i < a.max_tokens; i += ranks * kThreads) {
+    int32_t pos = 0, slot = -1;
+    if (ok && i < total.tokens) {
+      uint32_t lo = 0, hi = kThreads;
+      while (hi - lo > 1) {
+        const uint32_t m = (lo + hi) >> 1;
+        if (before[m].tokens <= i) lo = m; else hi = m;
+      }
+      long long j = i - before[lo].tokens, pages = before[lo].pages;
+      for (uint32_t r = lo * run;; ++r) {
+        const long long c = a.ctx[r], f = a.fresh[r], have = pages_of(c, a.log2_pt);
+        if (j < f) {
+          pos = (int32_t)(c + j);
+          const long long b = pos >> a.log2_pt;
+          const int32_t p = b < have ? a.table[(uint64_t)r * a.max_blocks + b] : a.free_pages[head + pages + b - have];
+          if (p >= 0 && p < page_limit) slot = (int32_t)(((uint32_t)p << a.log2_pt) + (pos & pt_mask));
+          else report(a.st, SHN_ERR_INVALID_ARG, r);
+          break;
+        }
+        j -= f;
+        pages += pages_of(c + f, a.log2_pt) - have;
+      }
+    }
+    a.positions[i] = pos;
+    a.slots[i] = slot;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t s) {
+  // a block per 4096 tokens (4 per thread) until the cluster's 8: below that a second block's start costs more
+  // than the tokens it takes over
+  uint32_t ranks = 1;
+  while (ranks < 8 && ranks * 4096ull < a.max_tokens) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ranks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_plan_kernel, a);
+}
+
+}  // namespace shn

@@ -31,6 +31,9 @@ EXPORTED = [
     "shn_encode_workspace_bytes", "shn_encode_workspace_bytes_min", "shn_decode_workspace_bytes", "shn_histogram", "shn_build_tables",
     "shn_encode", "shn_decode", "shn_decode_bf16", "shn_decode_from_host", "shn_offload_workspace_bytes",
     "shn_offload", "shn_get_device_status", "shn_encode_static_max_chunks", "shn_encode_static",
+    # include/shn_kv.h, bound in kv.py
+    "shn_kv_check_cache", "shn_kv_plan", "shn_kv_store", "shn_kv_load", "shn_kv_attn_prompt",
+    "shn_kv_attn_shared_workspace_bytes", "shn_kv_attn_shared",
 ]
 
 
