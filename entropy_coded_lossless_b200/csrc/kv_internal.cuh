@@ -88,6 +88,7 @@ struct KvAttnArgs {
   uint64_t out_stride;
   DeviceStatus* st;
 };
+cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t launch_kv_attn(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, cudaStream_t s);
 
 }  // namespace shn
