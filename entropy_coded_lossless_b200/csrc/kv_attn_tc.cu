@@ -14,11 +14,14 @@
 // than 8, i.e. a weight may reach 2^8 before the sums are scaled down: that is exact in float32 and bf16 alike
 // (a power-of-two range, no rounding) and spares almost every rescaling of O after a row's first tiles.
 //
-// Roles (512 threads): warps 0-3 and 4-7 the softmax of the two row tiles, warps 8-11 fetch the tiles and turn INT8 into
-// bf16 operands in shared memory, warp 12 issues the products. While the softmax of one row tile works, the
+// Roles (896 threads): warps 0-7 and 8-15 the softmax of the two row tiles (16 rows to a warp, so that each scheduler
+// has four of them to hide their latencies), warps 16-23 fetch the tiles and turn INT8 into bf16 operands in shared memory,
+// warp 24 issues the products. While the softmax of one row tile works, the
 // products of the other run. Two K and two V buffers; the next tile's bytes are on their way in registers while the present
 // one is converted.
 // TMEM (512 columns): S0, S1 (128 each; P in their first 64), O0, O1 (D each).
+#include <type_traits>
+
 #include "kv_tc.cuh"
 
 namespace shn {
@@ -26,7 +29,10 @@ namespace {
 
 using namespace tc;
 
-constexpr uint32_t kThreads = 512;
+constexpr uint32_t kSoftWarps = 16, kConvertWarps = 8;
+constexpr uint32_t kSoftThreads = 32 * kSoftWarps, kConvertThreads = 32 * kConvertWarps;
+constexpr uint32_t kIssueWarp = kSoftWarps + kConvertWarps;  // in a warpgroup of its own
+constexpr uint32_t kThreads = 32 * (kIssueWarp + 4);
 constexpr uint32_t kTile = 128;      // tokens of a tile
 constexpr uint32_t kRows = 256;      // query rows of a block
 constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows of 64 bf16
@@ -35,7 +41,7 @@ template <int D>
 struct Layout {
   static constexpr uint32_t kOperand = 128 * D * 2;  // one 128 x D bf16 operand
   static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, k_scale = 6 * kOperand, v_scale = k_scale + 4 * 512,
-                            bars = v_scale + 4 * 512, misc = bars + 256, scan = misc + 64, total = scan + 192;
+                            row_sum = v_scale + 4 * 512, bars = row_sum + 4 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
 };
 // barriers
 enum : uint32_t { kQFull = 0, kKFull = 8, kKEmpty = 24, kVFull = 40, kVEmpty = 56, kScaleFull = 72, kSFull = 104, kPFull = 120, kOFull = 136, kDrain = 152 };
@@ -66,7 +72,7 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
     if (lane >= (uint32_t)d) inc += x;
   }
   if (lane == 31) scan[warp] = inc;
-  if (t == 0) scan[17] = 0xFFFFFFFFu;
+  if (t == 0) scan[30] = 0xFFFFFFFFu;
   __syncthreads();
   uint32_t before = 0, total = 0;
 #pragma unroll
@@ -85,17 +91,17 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
       if (b < 0 || e < b || (uint32_t)e > a.n_tokens) continue;
       const uint32_t n = ((uint32_t)(e - b) * group + kRows - 1) / kRows;
       if (left < n) {
-        scan[17] = r;
-        scan[18] = left;
+        scan[30] = r;
+        scan[31] = left;
         break;
       }
       left -= n;
     }
   }
   __syncthreads();
-  w.req = scan[17];
+  w.req = scan[30];
   if (w.req >= a.n_reqs) return false;
-  w.row0 = scan[18] * kRows;
+  w.row0 = scan[31] * kRows;
   w.q0 = a.cu_q[w.req];
   w.nq = a.cu_q[w.req + 1] - w.q0;
   w.rows = (uint32_t)w.nq * group;
@@ -128,35 +134,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   const uint32_t tiles = ((uint32_t)most + kTile - 1) / kTile;
 
   if (tid == 0) {
-    bar_init(bars + kQFull, 256);
+    bar_init(bars + kQFull, kSoftThreads);
     bar_init(bars + kDrain, 1);
     for (uint32_t i = 0; i < 2; ++i) {
-      bar_init(bars + kKFull + 8 * i, 128);
+      bar_init(bars + kKFull + 8 * i, kConvertThreads);
       bar_init(bars + kKEmpty + 8 * i, 1);
-      bar_init(bars + kVFull + 8 * i, 128);
+      bar_init(bars + kVFull + 8 * i, kConvertThreads);
       bar_init(bars + kVEmpty + 8 * i, 1);
       bar_init(bars + kSFull + 8 * i, 1);
-      bar_init(bars + kPFull + 8 * i, 128);
+      bar_init(bars + kPFull + 8 * i, kSoftThreads / 2);
       bar_init(bars + kOFull + 8 * i, 1);
     }
-    for (uint32_t i = 0; i < 4; ++i) bar_init(bars + kScaleFull + 8 * i, 128);
+    for (uint32_t i = 0; i < 4; ++i) bar_init(bars + kScaleFull + 8 * i, kConvertThreads);
     sts32(stop, 0);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(stop + 4) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = lds32(stop + 4);
+  // all 512 columns are this block's, so its addresses begin at 0 (nothing that follows has to carry the base)
+  const uint32_t tmem = 0;
+  if (lds32(stop + 4) != 0) sts32(stop, 1);
 
-  if (warp < 8) {
-    // ---- softmax: thread = row -----------------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+  if (warp < kSoftWarps) {
+    // ---- softmax -------------------------------------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     // the queries of the block as an operand, zeros behind the last row
-    for (uint32_t i = tid; i < kRows * (D / 8); i += 256) {
+    for (uint32_t i = tid; i < kRows * (D / 8); i += kSoftThreads) {
       const uint32_t row = i / (D / 8), piece = i % (D / 8);
       uint4 x = make_uint4(0, 0, 0, 0);
       if (row < rows_here) {
@@ -168,104 +176,160 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     fence_smem();
     bar_arrive(bars + kQFull);
 
-    const uint32_t half = warp >> 2;  // which 128 rows
-    const uint32_t row = half * 128 + (warp & 3) * 32 + lane;
-    const uint32_t at = tmem + (((warp & 3) * 32) << 16);  // the warp's lanes of TMEM
-    const uint32_t s_col = at + half * 128, o_col = at + 256 + half * D;
-    const uint32_t g = w.row0 + row;
-    const int32_t seen = row < rows_here ? max(0, min(w.len, shift + (int32_t)(g / group))) : 0;
-    float m = -INFINITY, l = 0.f;
+    // A warp has 16 rows (TMEM lanes); a thread has two of them, `quad` and quad + 8, and of each 8 columns two: a column's
+    // scales, read from shared memory, serve two rows, and a row's maximum is two shuffles away.
+    const uint32_t half = warp >> 3;  // which 128 rows
+    const uint32_t lanes = (warp & 3) * 32 + (warp & 4) * 4, quad = lane >> 2, col = 2 * (lane & 3);
+    const uint32_t at = tmem + (lanes << 16);
+    const uint32_t s_at = at + half * 128, o_at = at + 256 + half * D;
+    auto seen_by = [&](uint32_t row) -> int32_t {
+      return row < rows_here ? max(0, min(w.len, shift + (int32_t)((w.row0 + row) / group))) : 0;
+    };
+    int32_t seen[2];
+    float m[2], l[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) seen[r] = seen_by(half * 128 + lanes + quad + 8 * r), m[r] = -INFINITY, l[r] = 0.f;
     bool ok = true;
     for (uint32_t j = 0; j < tiles; ++j) {
       ok = bar_wait(bars + kScaleFull + 8 * (j & 3), (j >> 2) & 1, stop) && bar_wait(bars + kSFull + 8 * half, j & 1, stop);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) ld32(s_col + 32 * q, s + 32 * q);
+      // s[4n + 2r + e]: row quad + 8r, column 8n + col + e
+      uint32_t s[64];
+      ld_quad32(s_at, s);
+      ld_quad32(s_at + 64, s + 32);
       wait_ld();
-      const uint32_t ks = base + L::k_scale + (j & 3) * 512, vs = base + L::v_scale + (j & 3) * 512;
-      float top = -INFINITY;
-      const bool edge = __any_sync(~0u, (int32_t)((j + 1) * kTile) > seen);
+      const uint32_t ks = base + L::k_scale + (j & 3) * 512 + 4 * col, vs = base + L::v_scale + (j & 3) * 512 + 4 * col;
+      float top[2] = {-INFINITY, -INFINITY};
+      const int32_t first = (int32_t)(j * kTile + col);
+      const bool edge = __any_sync(~0u, (int32_t)((j + 1) * kTile) > min(seen[0], seen[1]));
+      // two versions each: only tiles at the end of what a row sees look at the columns' places
+      auto scale_and_max = [&](auto edge_tag) {
+        constexpr bool kEdge = decltype(edge_tag)::value;
 #pragma unroll
-      for (int q = 0; q < 32; ++q) {
-        const uint4 f = lds128(ks + 16 * q);
-        float x[4];
-        unpack2(mul2(pack2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), pack2(__uint_as_float(f.x), __uint_as_float(f.y))), x[0], x[1]);
-        unpack2(mul2(pack2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), pack2(__uint_as_float(f.z), __uint_as_float(f.w))), x[2], x[3]);
-        if (edge) {
+        for (int n = 0; n < 16; ++n) {
+          const uint2 f = lds64(ks + 32 * n);
+          const uint64_t f2 = pack2(__uint_as_float(f.x), __uint_as_float(f.y));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = (int32_t)(j * kTile + 4 * q + e) < seen ? x[e] : -INFINITY;
+          for (int r = 0; r < 2; ++r) {
+            uint32_t* v = &s[4 * n + 2 * r];
+            float x, y;
+            unpack2(mul2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), f2), x, y);
+            if constexpr (kEdge) {
+              x = first + 8 * n < seen[r] ? x : -INFINITY;
+              y = first + 8 * n + 1 < seen[r] ? y : -INFINITY;
+            }
+            top[r] = fmaxf(top[r], fmaxf(x, y));
+            v[0] = __float_as_uint(x);
+            v[1] = __float_as_uint(y);
+          }
         }
-        top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+      };
+      if (edge) scale_and_max(std::true_type{});
+      else scale_and_max(std::false_type{});
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * q + e] = __float_as_uint(x[e]);
+      for (int r = 0; r < 2; ++r) {
+        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
       }
       if (j == 0) {
-        m = top;
-      } else if (__any_sync(~0u, top > m + 8.f)) {
-        const float next = top > m + 8.f ? top : m;
-        const float keep = next == m ? 1.f : exp2_approx(m - next);
-        m = next;
-        l *= keep;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) m[r] = top[r];
+      } else if (__any_sync(~0u, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+        float keep[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float next = top[r] > m[r] + 8.f ? top[r] : m[r];
+          keep[r] = next == m[r] ? 1.f : exp2_approx(m[r] - next);
+          m[r] = next;
+          l[r] *= keep[r];
+        }
         ok = __all_sync(~0u, bar_wait(bars + kOFull + 8 * half, (j - 1) & 1, stop));
         if (!ok) break;
         fence_after();
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          ld32(o_col + 32 * q, o);
+#pragma unroll 1
+        for (uint32_t o_q = o_at; o_q < o_at + D; o_q += 16) {  // few registers a time: the scores stay in theirs meanwhile
+          uint32_t o[8];
+          ld_quad8(o_q, o);
           wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-          st32(o_col + 32 * q, o);
+          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep[(e >> 1) & 1]);
+          st_quad8(o_q, o);
         }
       }
-      const float neg = m == -INFINITY ? 0.f : -m;
-      const uint64_t neg2 = pack2(neg, neg);
-      uint64_t sum2[2] = {0, 0};
+      uint64_t neg[2], sum[2];
 #pragma unroll
-      for (int q = 0; q < 32; ++q) {
-        const uint4 f = lds128(vs + 16 * q);
-        float x[4];
-        unpack2(add2(pack2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), neg2), x[0], x[1]);
-        unpack2(add2(pack2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), neg2), x[2], x[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = exp2_approx(x[e]);
-        const uint64_t p01 = pack2(x[0], x[1]), p23 = pack2(x[2], x[3]);
-        sum2[0] = add2(sum2[0], p01);
-        sum2[1] = add2(sum2[1], p23);
-        unpack2(mul2(p01, pack2(__uint_as_float(f.x), __uint_as_float(f.y))), x[0], x[1]);
-        unpack2(mul2(p23, pack2(__uint_as_float(f.z), __uint_as_float(f.w))), x[2], x[3]);
-        if (edge) {  // a scale behind the row's end may be anything: 0 * infinity
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = (int32_t)(j * kTile + 4 * q + e) < seen ? x[e] : 0.f;
-        }
-        s[2 * q] = bf16_pack(x[0], x[1]);  // (columns 2q and 2q+1 are behind us)
-        s[2 * q + 1] = bf16_pack(x[2], x[3]);
+      for (int r = 0; r < 2; ++r) {
+        const float x = m[r] == -INFINITY ? 0.f : -m[r];
+        neg[r] = pack2(x, x);
+        sum[r] = pack2(l[r], 0.f);
       }
-      st32(s_col, s);
-      st32(s_col + 32, s + 32);
-      float e0, e1, e2, e3;
-      unpack2(sum2[0], e0, e1);
-      unpack2(sum2[1], e2, e3);
-      l += (e0 + e1) + (e2 + e3);
+      auto weights = [&](auto edge_tag) {
+        constexpr bool kEdge = decltype(edge_tag)::value;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {  // 32 columns: 16 of packed pairs
+          uint32_t p[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = 4 * b + i;
+            const uint2 f = lds64(vs + 32 * n);
+            const uint64_t f2 = pack2(__uint_as_float(f.x), __uint_as_float(f.y));
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t* v = &s[4 * n + 2 * r];
+              float x, y;
+              unpack2(add2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), neg[r]), x, y);
+              const uint64_t e2 = pack2(exp2_approx(x), exp2_approx(y));
+              sum[r] = add2(sum[r], e2);
+              unpack2(mul2(e2, f2), x, y);
+              if constexpr (kEdge) {  // a scale behind the row's end may be anything: 0 * infinity
+                x = first + 8 * n < seen[r] ? x : 0.f;
+                y = first + 8 * n + 1 < seen[r] ? y : 0.f;
+              }
+              p[2 * i + r] = bf16_pack(x, y);
+            }
+          }
+          st_pairs8(s_at + 16 * b, p);
+        }
+      };
+      if (edge) weights(std::true_type{});
+      else weights(std::false_type{});
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float x, y;
+        unpack2(sum[r], x, y);
+        l[r] = x + y;
+      }
       wait_st();
       fence_before();
       bar_arrive(bars + kPFull + 8 * half);
     }
+    // the rows' sums, through shared memory to the threads that write the rows: warps of the same 32 rows take half of the
+    // columns each (the barrier comes first: no warp may miss it)
+    const uint32_t rows32 = (warp & 3) * 32;
+    const uint32_t sums = base + L::row_sum + 4 * (half * 128);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
+      if ((lane & 3) == 0) sts32(sums + 4 * (lanes + quad + 8 * r), __float_as_uint(l[r]));
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(kSoftThreads / 2) : "memory");
     if (ok && tiles) ok = __all_sync(~0u, bar_wait(bars + kOFull + 8 * half, (tiles - 1) & 1, stop));
     if (ok) {
       fence_after();
+      const uint32_t row = half * 128 + rows32 + lane, g = w.row0 + row;
+      const bool any = seen_by(row) > 0;
       // no token seen: zeros. (A sum that is not positive although tokens were seen is a NaN's or an infinity's.)
-      const float inv = seen > 0 ? 1.f / l : 0.f;
-      uint16_t* dst = a.out + (uint64_t)(w.q0 + g / group) * a.out_stride + (uint64_t)(hk * group + g % group) * D;
+      const float inv = any ? 1.f / __uint_as_float(lds32(sums + 4 * (rows32 + lane))) : 0.f;
+      const uint32_t first = (warp >> 2 & 1) * (D / 2);
+      uint16_t* dst = a.out + (uint64_t)(w.q0 + g / group) * a.out_stride + (uint64_t)(hk * group + g % group) * D + first;
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
+      for (int q = 0; q < D / 64; ++q) {
         uint32_t o[32];
         if (tiles) {
-          ld32(o_col + 32 * q, o);
+          ld32(tmem + (rows32 << 16) + 256 + half * D + first + 32 * q, o);
           wait_ld();
         }
         if (row < rows_here) {
@@ -274,22 +338,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
             uint32_t y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              y[i] = seen > 0 ? bf16_pack(__uint_as_float(o[8 * e + 2 * i]) * inv, __uint_as_float(o[8 * e + 2 * i + 1]) * inv) : 0u;
+              y[i] = any ? bf16_pack(__uint_as_float(o[8 * e + 2 * i]) * inv, __uint_as_float(o[8 * e + 2 * i + 1]) * inv) : 0u;
             *reinterpret_cast<uint4*>(dst + 32 * q + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
       }
       fence_before();
     }
-  } else if (warp < 12) {
+  } else if (warp < kIssueWarp) {
     // ---- fetch and convert ---------------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    constexpr int kLoads = D / 16;  // 16-byte loads of a thread per operand
-    const uint32_t t = tid - 256, cw = t >> 5;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    constexpr int kLoads = D / 32;  // 16-byte loads of a thread per operand
+    const uint32_t t = tid - kSoftThreads, cw = t >> 5;
     // A warp's load: 4 lanes on 64 values of a row, 8 rows. For D = 128 even warps take the rows' first 64 values.
-    const uint32_t part = D == 128 ? (cw & 1) : 0, first = D == 128 ? (cw >> 1) * 64 : cw * 32;
+    const uint32_t part = D == 128 ? (cw & 1) : 0, first = (cw >> (D == 128 ? 1 : 0)) * kLoads * 8;
     const uint32_t chunk = lane & 3, sub = lane >> 2;
-    const float k_mul = a.scale * 1.44269504088896340736f;  // log2(e)
     const int32_t* table = a.table + (uint64_t)w.req * a.max_blocks;
     const uint32_t pt_mask = (1u << c.log2_pt) - 1;
 
@@ -306,117 +369,118 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       }
       return p;
     };
-    auto fetch = [&](const int8_t* src, uint32_t j, int32_t pages, uint4* raw) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const uint32_t row = first + i * 8 + sub, tok = j * kTile + row;
-        const int32_t p = __shfl_sync(~0u, pages, (first + i * 8) >> 4);
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (p >= 0 && (int32_t)tok < most)
-          raw[i] = *reinterpret_cast<const uint4*>(src + kv_row(c, (uint32_t)p, hk, tok & pt_mask) * D + part * 64 + chunk * 16);
-      }
+    auto fetch = [&](const int8_t* src, uint32_t j, int32_t pages, int i) -> uint4 {
+      const uint32_t row = first + i * 8 + sub, tok = j * kTile + row;
+      const int32_t p = __shfl_sync(~0u, pages, (first + i * 8) >> 4);
+      if (p < 0 || (int32_t)tok >= most) return make_uint4(0, 0, 0, 0);
+      return *reinterpret_cast<const uint4*>(src + kv_row(c, (uint32_t)p, hk, tok & pt_mask) * D + part * 64 + chunk * 16);
     };
-    auto convert = [&](const uint4* raw, uint32_t dst) {
+    // Converts the thread's pieces of an operand, and as each one's registers are read asks for the same piece of the
+    // operand after it: one operand's worth of loads is always on its way and no more registers hold it.
+    uint4 raw[kLoads];
+    auto turn = [&](uint32_t dst, const int8_t* src, uint32_t j, int32_t pages) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const uint32_t row = first + i * 8 + sub;
         const uint2 x = bf16x4_of_int8(raw[i].x), y = bf16x4_of_int8(raw[i].y), z = bf16x4_of_int8(raw[i].z), u = bf16x4_of_int8(raw[i].w);
+        raw[i] = fetch(src, j, pages, i);
         sts128(dst + part * kHalf + swizzled(row, 2 * chunk), make_uint4(x.x, x.y, y.x, y.y));
         sts128(dst + part * kHalf + swizzled(row, 2 * chunk + 1), make_uint4(z.x, z.y, u.x, u.y));
       }
       fence_smem();
     };
-    uint4 kr[kLoads], vr[kLoads];
-    float ksc = 0.f, vsc = 0.f;
-    // scales of token t of the tile
-    auto fetch_scales = [&](uint32_t j, int32_t pages) {
-      const int32_t p = __shfl_sync(~0u, pages, t >> 4);
-      const uint32_t tok = j * kTile + t;
-      ksc = vsc = 0.f;
-      if (p >= 0 && (int32_t)tok < most) {
-        const uint64_t at = kv_row(c, (uint32_t)p, hk, tok & pt_mask);
-        ksc = c.k_scale[at];
-        vsc = c.v_scale[at];
-      }
+    // the thread's scale of the tile: a key's in the first half of the threads, a value's in the second
+    const bool is_v = t >= kTile;
+    const float* scales = is_v ? c.v_scale : c.k_scale;
+    const float factor = is_v ? 1.f : a.scale * 1.44269504088896340736f;  // log2(e)
+    const uint32_t scale_at = base + (is_v ? L::v_scale : L::k_scale) + 4 * (t % kTile);
+    auto fetch_scale = [&](uint32_t j, int32_t pages) -> float {
+      const int32_t p = __shfl_sync(~0u, pages, (t % kTile) >> 4);
+      const uint32_t tok = j * kTile + t % kTile;
+      if (p < 0 || (int32_t)tok >= most) return 0.f;
+      return scales[kv_row(c, (uint32_t)p, hk, tok & pt_mask)] * factor;
     };
+    float scale = 0.f;
     int32_t pages = pages_of(0);
     if (tiles) {
-      fetch(c.k, 0, pages, kr);
-      fetch_scales(0, pages);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) raw[i] = fetch(c.k, 0, pages, i);
+      scale = fetch_scale(0, pages);
     }
     for (uint32_t j = 0; j < tiles; ++j) {
       const uint32_t buf = j & 1, use = j >> 1;
-      fetch(c.v, j, pages, vr);
-      const int32_t next = pages_of(j + 1);
+      const int32_t next = pages_of(j + 1);  // -1 behind the last tile: nothing is fetched for it
       if (!__all_sync(~0u, bar_wait(bars + kKEmpty + 8 * buf, (use & 1) ^ 1, stop))) break;
       // The scales have four places: those of tile j - 4 were read before the products of tile j - 3 could begin, and
       // this K buffer is free since those of tile j - 2 are done.
-      sts32(base + L::k_scale + (j & 3) * 512 + 4 * t, __float_as_uint(ksc * k_mul));
-      sts32(base + L::v_scale + (j & 3) * 512 + 4 * t, __float_as_uint(vsc));
+      sts32(scale_at + (j & 3) * 512, __float_as_uint(scale));
       bar_arrive(bars + kScaleFull + 8 * (j & 3));
-      convert(kr, base + L::k + buf * L::kOperand);
+      turn(base + L::k + buf * L::kOperand, c.v, j, pages);
       bar_arrive(bars + kKFull + 8 * buf);
       pages = next;
-      if (j + 1 < tiles) {
-        fetch(c.k, j + 1, pages, kr);
-        fetch_scales(j + 1, pages);
-      }
+      scale = fetch_scale(j + 1, pages);
       if (!__all_sync(~0u, bar_wait(bars + kVEmpty + 8 * buf, (use & 1) ^ 1, stop))) break;
-      convert(vr, base + L::v + buf * L::kOperand);
+      turn(base + L::v + buf * L::kOperand, c.k, j + 1, pages);
       bar_arrive(bars + kVFull + 8 * buf);
     }
   } else {
-    // ---- products: one thread issues -----------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (tid == 12 * 32 && tiles) {
+    // ---- products: the warp runs the loop as one, an elected thread issues ------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == kIssueWarp && tiles) {
       constexpr uint32_t kS = instr_desc(128, 128, false), kO = instr_desc(128, D, true);
-      auto scores = [&](uint32_t i, uint32_t j) {
+      const bool lead = elect_one();
+      auto scores = [&](uint32_t i, uint32_t buf) {
+        const uint64_t q = smem_desc(base + L::q + i * L::kOperand, 16), k = smem_desc(base + L::k + buf * L::kOperand, 16);
+        if (lead) {
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) {
-          const uint32_t off = (e / 4) * kHalf + (e % 4) * 32;
-          mma_ss(tmem + 128 * i, smem_desc(base + L::q + i * L::kOperand + off, 16), smem_desc(base + L::k + (j & 1) * L::kOperand + off, 16), kS, e > 0);
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t off = ((e / 4) * kHalf + (e % 4) * 32) >> 4;
+            mma_ss(tmem + 128 * i, q + off, k + off, kS, e > 0);
+          }
+          commit(bars + kSFull + 8 * i);
         }
-        commit(bars + kSFull + 8 * i);
       };
-      auto values = [&](uint32_t i, uint32_t j) {
+      auto values = [&](uint32_t i, uint32_t buf, bool add) {
+        const uint64_t v = smem_desc(base + L::v + buf * L::kOperand, kHalf);
+        if (lead) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          mma_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * e, smem_desc(base + L::v + (j & 1) * L::kOperand + e * 2048, kHalf), kO, j > 0 || e > 0);
-        commit(bars + kOFull + 8 * i);
+          for (int e = 0; e < 8; ++e) mma_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * e, v + e * (2048 >> 4), kO, add || e > 0);
+          commit(bars + kOFull + 8 * i);
+        }
       };
-      bool ok = bar_wait(bars + kQFull, 0, stop) && bar_wait(bars + kKFull, 0, stop);
+      auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(~0u, bar_wait(bars + bar, parity, stop)); };
+      bool ok = wait(kQFull, 0) && wait(kKFull, 0);
       if (ok) {
         fence_after();
         scores(0, 0);
         scores(1, 0);
-        commit(bars + kKEmpty);
+        if (lead) commit(bars + kKEmpty);
       }
       for (uint32_t j = 0; ok && j < tiles; ++j) {
         const uint32_t buf = j & 1, nbuf = buf ^ 1;
-        ok = bar_wait(bars + kVFull + 8 * buf, (j >> 1) & 1, stop) && bar_wait(bars + kPFull, j & 1, stop);
+        ok = wait(kVFull + 8 * buf, (j >> 1) & 1) && wait(kPFull, j & 1);
         if (!ok) break;
         fence_after();
-        values(0, j);
+        values(0, buf, j > 0);
         if (j + 1 < tiles) {
-          ok = bar_wait(bars + kKFull + 8 * nbuf, ((j + 1) >> 1) & 1, stop);
+          ok = wait(kKFull + 8 * nbuf, ((j + 1) >> 1) & 1);
           if (!ok) break;
           fence_after();
-          scores(0, j + 1);
+          scores(0, nbuf);
         }
-        ok = bar_wait(bars + kPFull + 8, j & 1, stop);
+        ok = wait(kPFull + 8, j & 1);
         if (!ok) break;
         fence_after();
-        values(1, j);
-        commit(bars + kVEmpty + 8 * buf);
+        values(1, buf, j > 0);
+        if (lead) commit(bars + kVEmpty + 8 * buf);
         if (j + 1 < tiles) {
-          scores(1, j + 1);
-          commit(bars + kKEmpty + 8 * nbuf);
+          scores(1, nbuf);
+          if (lead) commit(bars + kKEmpty + 8 * nbuf);
         }
       }
       if (!ok) {
         // gave up: let the products in flight end (again with a limit) before TMEM goes back
-        report(a.st, SHN_ERR_TIMEOUT, w.req);
-        commit(bars + kDrain);
+        if (lead) commit(bars + kDrain);
         for (uint32_t i = 0; i < kWaitTries && !bar_try(bars + kDrain, 0); ++i) {
         }
       }
@@ -425,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (warp == kIssueWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   if (tid == 0 && lds32(stop) != 0) report(a.st, SHN_ERR_TIMEOUT, w.req);
 }
 

@@ -44,6 +44,13 @@ __device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.s
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// true in one thread of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -84,18 +91,24 @@ __device__ __forceinline__ void ld32(uint32_t addr, uint32_t* v) {
       : SHN_R8(v, 0), SHN_R8(v, 8), SHN_R8(v, 16), SHN_R8(v, 24)
       : "r"(addr));
 }
-__device__ __forceinline__ void st32(uint32_t addr, const uint32_t* v) {
+// 16 lanes: thread t holds rows t/4 (registers 0, 1) and t/4 + 8 (registers 2, 3) of columns 2(t%4), 2(t%4) + 1 of
+// each 8 columns; 4 registers per 8 columns
+__device__ __forceinline__ void ld_quad32(uint32_t addr, uint32_t* v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      SHN_I8(v, 0), SHN_I8(v, 8), SHN_I8(v, 16), SHN_I8(v, 24)
-      : "memory");
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : SHN_R8(v, 0), SHN_R8(v, 8), SHN_R8(v, 16), SHN_R8(v, 24)
+      : "r"(addr));
 }
-__device__ __forceinline__ void st16(uint32_t addr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      SHN_I8(v, 0), SHN_I8(v, 8)
-      : "memory");
+__device__ __forceinline__ void ld_quad8(uint32_t addr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : SHN_R8(v, 0) : "r"(addr));
+}
+__device__ __forceinline__ void st_quad8(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), SHN_I8(v, 0) : "memory");
+}
+// 16 lanes, packed pairs: thread t holds rows t/4 and t/4 + 8 (registers 0, 1) of column t%4 of each 4 columns
+__device__ __forceinline__ void st_pairs8(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), SHN_I8(v, 0) : "memory");
 }
 
 // ---- arithmetic ----------------------------------------------------------------------------------
