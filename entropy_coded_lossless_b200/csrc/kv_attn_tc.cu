@@ -35,16 +35,16 @@ constexpr uint32_t kIssueWarp = kSoftWarps + kConvertWarps;  // in a warpgroup o
 constexpr uint32_t kThreads = 32 * (kIssueWarp + 4);
 constexpr uint32_t kTile = 128;      // tokens of a tile
 constexpr uint32_t kRows = 256;      // query rows of a block
+constexpr float kRise = 8.f;         // how far (log2) a weight may pass 1 before the reference is raised
 constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows of 64 bf16
 
 template <int D>
 struct Layout {
   static constexpr uint32_t kOperand = 128 * D * 2;  // one 128 x D bf16 operand
-  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, k_scale = 6 * kOperand, v_scale = k_scale + 4 * 512,
-                            row_sum = v_scale + 4 * 512, bars = row_sum + 4 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
+  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, row_sum = scale + 4 * 1024, bars = row_sum + 4 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
 };
 // barriers
-enum : uint32_t { kQFull = 0, kKFull = 8, kKEmpty = 24, kVFull = 40, kVEmpty = 56, kScaleFull = 72, kSFull = 104, kPFull = 120, kOFull = 136, kDrain = 152 };
+enum : uint32_t { kQFull = 0, kKFull = 8, kKEmpty = 24, kVFull = 40, kVEmpty = 56, kScaleFull = 72, kSFull = 104, kPFull = 120, kOFull = 152, kDrain = 184 };
 
 struct Work {
   uint32_t req, row0, rows;  // request, first row of the block within it, rows of the request
@@ -137,15 +137,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     bar_init(bars + kQFull, kSoftThreads);
     bar_init(bars + kDrain, 1);
     for (uint32_t i = 0; i < 2; ++i) {
-      bar_init(bars + kKFull + 8 * i, kConvertThreads);
+      bar_init(bars + kKFull + 8 * i, kConvertWarps);
       bar_init(bars + kKEmpty + 8 * i, 1);
-      bar_init(bars + kVFull + 8 * i, kConvertThreads);
+      bar_init(bars + kVFull + 8 * i, kConvertWarps);
       bar_init(bars + kVEmpty + 8 * i, 1);
       bar_init(bars + kSFull + 8 * i, 1);
-      bar_init(bars + kPFull + 8 * i, kSoftThreads / 2);
-      bar_init(bars + kOFull + 8 * i, 1);
+      bar_init(bars + kPFull + 16 * i, kSoftWarps / 2);
+      bar_init(bars + kPFull + 16 * i + 8, kSoftWarps / 2);
+      bar_init(bars + kOFull + 16 * i, 1);
+      bar_init(bars + kOFull + 16 * i + 8, 1);
     }
-    for (uint32_t i = 0; i < 4; ++i) bar_init(bars + kScaleFull + 8 * i, kConvertThreads);
+    for (uint32_t i = 0; i < 4; ++i) bar_init(bars + kScaleFull + 8 * i, kConvertWarps);
     sts32(stop, 0);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -187,123 +189,116 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     };
     int32_t seen[2];
     float m[2], l[2];
+    uint64_t neg[2];  // minus the reference, twice (0 while there is none)
+    float limit[2];   // how far a score may be above it
 #pragma unroll
-    for (int r = 0; r < 2; ++r) seen[r] = seen_by(half * 128 + lanes + quad + 8 * r), m[r] = -INFINITY, l[r] = 0.f;
+    for (int r = 0; r < 2; ++r) {
+      seen[r] = seen_by(half * 128 + lanes + quad + 8 * r);
+      m[r] = -INFINITY, l[r] = 0.f, neg[r] = 0, limit[r] = -INFINITY;
+    }
     bool ok = true;
-    for (uint32_t j = 0; j < tiles; ++j) {
+    for (uint32_t j = 0; j < tiles && ok; ++j) {
       ok = bar_wait(bars + kScaleFull + 8 * (j & 3), (j >> 2) & 1, stop) && bar_wait(bars + kSFull + 8 * half, j & 1, stop);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       fence_after();
-      // s[4n + 2r + e]: row quad + 8r, column 8n + col + e
-      uint32_t s[64];
-      ld_quad32(s_at, s);
-      ld_quad32(s_at + 64, s + 32);
-      wait_ld();
-      const uint32_t ks = base + L::k_scale + (j & 3) * 512 + 4 * col, vs = base + L::v_scale + (j & 3) * 512 + 4 * col;
-      float top[2] = {-INFINITY, -INFINITY};
-      const int32_t first = (int32_t)(j * kTile + col);
-      const bool edge = __any_sync(~0u, (int32_t)((j + 1) * kTile) > min(seen[0], seen[1]));
-      // two versions each: only tiles at the end of what a row sees look at the columns' places
-      auto scale_and_max = [&](auto edge_tag) {
-        constexpr bool kEdge = decltype(edge_tag)::value;
+      // half a tile (64 tokens) at a time: its part of P V can begin while the other half is worked on
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const uint2 f = lds64(ks + 32 * n);
-          const uint64_t f2 = pack2(__uint_as_float(f.x), __uint_as_float(f.y));
+      for (int h = 0; h < 2; ++h) {
+        // s[4n + 2r + e]: row quad + 8r, column 64h + 8n + col + e
+        uint32_t s[32];
+        ld_quad32(s_at + 64 * h, s);
+        wait_ld();
+        const uint32_t scales = base + L::scale + (j & 3) * 1024 + h * 512 + 8 * col;
+        const int32_t first = (int32_t)(j * kTile + 64 * h + col);
+        const bool edge = __any_sync(~0u, first - (int32_t)col + 64 > min(seen[0], seen[1]));
+        float top[2];
+        uint64_t sum[2];
+        // Weights against the reference that stands; scores relative to it are watched, not searched first: almost
+        // always none is above the limit and this one pass is all. (Two versions: only tiles at the end of what a row
+        // sees look at the columns' places.)
+        auto weights = [&](auto edge_tag) {
+          constexpr bool kEdge = decltype(edge_tag)::value;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) top[r] = -INFINITY, sum[r] = 0;
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {  // 32 columns: 16 of packed pairs
+            uint32_t p[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int n = 4 * b + i;
+              const uint4 f = lds128_free(scales + 64 * n);
+              const uint64_t ks = pack2(__uint_as_float(f.x), __uint_as_float(f.y)), vs = pack2(__uint_as_float(f.z), __uint_as_float(f.w));
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t* v = &s[4 * n + 2 * r];
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), ks, neg[r]), x, y);
+                if constexpr (kEdge) {
+                  x = first + 8 * n < seen[r] ? x : -INFINITY;
+                  y = first + 8 * n + 1 < seen[r] ? y : -INFINITY;
+                }
+                top[r] = max3(top[r], x, y);
+                const uint64_t e2 = pack2(exp2_approx(x), exp2_approx(y));
+                sum[r] = add2(sum[r], e2);
+                unpack2(mul2(e2, vs), x, y);
+                if constexpr (kEdge) {  // a scale behind the row's end may be anything: 0 * infinity
+                  x = first + 8 * n < seen[r] ? x : 0.f;
+                  y = first + 8 * n + 1 < seen[r] ? y : 0.f;
+                }
+                p[2 * i + r] = bf16_pack(x, y);
+              }
+            }
+            st_pairs8(s_at + 32 * h + 16 * b, p);
+          }
+        };
+        if (edge) weights(std::true_type{});
+        else weights(std::false_type{});
+        if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
+          // the reference rises: what is summed is scaled down, and the weights formed again
+          float keep[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            uint32_t* v = &s[4 * n + 2 * r];
-            float x, y;
-            unpack2(mul2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), f2), x, y);
-            if constexpr (kEdge) {
-              x = first + 8 * n < seen[r] ? x : -INFINITY;
-              y = first + 8 * n + 1 < seen[r] ? y : -INFINITY;
+            top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+            keep[r] = 1.f;
+            if (top[r] > limit[r]) {
+              const float next = m[r] == -INFINITY ? top[r] : m[r] + top[r];
+              keep[r] = exp2_approx(m[r] - next);
+              m[r] = next;
+              neg[r] = pack2(-next, -next);
+              limit[r] = kRise;
             }
-            top[r] = fmaxf(top[r], fmaxf(x, y));
-            v[0] = __float_as_uint(x);
-            v[1] = __float_as_uint(y);
+            l[r] *= keep[r];
           }
+          if (j > 0 || h > 0) {
+            ok = __all_sync(~0u, bar_wait(bars + kOFull + 16 * half + 8 * (h ^ 1), (j + h + 1) & 1, stop));  // the part before this one
+            if (!ok) break;
+            fence_after();
+#pragma unroll 1
+            for (uint32_t o_q = o_at; o_q < o_at + D; o_q += 16) {  // few registers a time
+              uint32_t o[8];
+              ld_quad8(o_q, o);
+              wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep[(e >> 1) & 1]);
+              st_quad8(o_q, o);
+            }
+          }
+          if (edge) weights(std::true_type{});
+          else weights(std::false_type{});
         }
-      };
-      if (edge) scale_and_max(std::true_type{});
-      else scale_and_max(std::false_type{});
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
-      }
-      if (j == 0) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) m[r] = top[r];
-      } else if (__any_sync(~0u, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
-        float keep[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float next = top[r] > m[r] + 8.f ? top[r] : m[r];
-          keep[r] = next == m[r] ? 1.f : exp2_approx(m[r] - next);
-          m[r] = next;
-          l[r] *= keep[r];
+          float x, y;
+          unpack2(sum[r], x, y);
+          l[r] += x + y;
         }
-        ok = __all_sync(~0u, bar_wait(bars + kOFull + 8 * half, (j - 1) & 1, stop));
-        if (!ok) break;
-        fence_after();
-#pragma unroll 1
-        for (uint32_t o_q = o_at; o_q < o_at + D; o_q += 16) {  // few registers a time: the scores stay in theirs meanwhile
-          uint32_t o[8];
-          ld_quad8(o_q, o);
-          wait_ld();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep[(e >> 1) & 1]);
-          st_quad8(o_q, o);
-        }
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bars + kPFull + 16 * half + 8 * h);
       }
-      uint64_t neg[2], sum[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float x = m[r] == -INFINITY ? 0.f : -m[r];
-        neg[r] = pack2(x, x);
-        sum[r] = pack2(l[r], 0.f);
-      }
-      auto weights = [&](auto edge_tag) {
-        constexpr bool kEdge = decltype(edge_tag)::value;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {  // 32 columns: 16 of packed pairs
-          uint32_t p[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = 4 * b + i;
-            const uint2 f = lds64(vs + 32 * n);
-            const uint64_t f2 = pack2(__uint_as_float(f.x), __uint_as_float(f.y));
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const uint32_t* v = &s[4 * n + 2 * r];
-              float x, y;
-              unpack2(add2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), neg[r]), x, y);
-              const uint64_t e2 = pack2(exp2_approx(x), exp2_approx(y));
-              sum[r] = add2(sum[r], e2);
-              unpack2(mul2(e2, f2), x, y);
-              if constexpr (kEdge) {  // a scale behind the row's end may be anything: 0 * infinity
-                x = first + 8 * n < seen[r] ? x : 0.f;
-                y = first + 8 * n + 1 < seen[r] ? y : 0.f;
-              }
-              p[2 * i + r] = bf16_pack(x, y);
-            }
-          }
-          st_pairs8(s_at + 16 * b, p);
-        }
-      };
-      if (edge) weights(std::true_type{});
-      else weights(std::false_type{});
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float x, y;
-        unpack2(sum[r], x, y);
-        l[r] = x + y;
-      }
-      wait_st();
-      fence_before();
-      bar_arrive(bars + kPFull + 8 * half);
     }
     // the rows' sums, through shared memory to the threads that write the rows: warps of the same 32 rows take half of the
     // columns each (the barrier comes first: no warp may miss it)
@@ -316,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if ((lane & 3) == 0) sts32(sums + 4 * (lanes + quad + 8 * r), __float_as_uint(l[r]));
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(kSoftThreads / 2) : "memory");
-    if (ok && tiles) ok = __all_sync(~0u, bar_wait(bars + kOFull + 8 * half, (tiles - 1) & 1, stop));
+    if (ok && tiles) ok = __all_sync(~0u, bar_wait(bars + kOFull + 16 * half + 8, (tiles - 1) & 1, stop));
     if (ok) {
       fence_after();
       const uint32_t row = half * 128 + rows32 + lane, g = w.row0 + row;
@@ -369,31 +364,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       }
       return p;
     };
-    auto fetch = [&](const int8_t* src, uint32_t j, int32_t pages, int i) -> uint4 {
-      const uint32_t row = first + i * 8 + sub, tok = j * kTile + row;
-      const int32_t p = __shfl_sync(~0u, pages, (first + i * 8) >> 4);
-      if (p < 0 || (int32_t)tok >= most) return make_uint4(0, 0, 0, 0);
-      return *reinterpret_cast<const uint4*>(src + kv_row(c, (uint32_t)p, hk, tok & pt_mask) * D + part * 64 + chunk * 16);
+    // Where the warp's rows of a tile lie: their 16-token groups' offsets in the cache, for keys and values alike (-1: nothing
+    // there; the bytes behind a sequence's end in its last group are read and masked).
+    constexpr int kGroups = kLoads / 2;
+    const uint32_t lane_at = sub * D + part * 64 + chunk * 16;
+    auto offsets = [&](uint32_t j, int32_t pages, int64_t* off) {
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        const uint32_t group16 = (first >> 4) + i;
+        const int32_t p = __shfl_sync(~0u, pages, group16);
+        off[i] = p < 0 ? -1 : (int64_t)(kv_row(c, (uint32_t)p, hk, (j * kTile + group16 * 16) & pt_mask) * D + lane_at);
+      }
     };
     // Converts the thread's pieces of an operand, and as each one's registers are read asks for the same piece of the
     // operand after it: one operand's worth of loads is always on its way and no more registers hold it.
     uint4 raw[kLoads];
-    auto turn = [&](uint32_t dst, const int8_t* src, uint32_t j, int32_t pages) {
+    auto fetch = [&](const int8_t* src, const int64_t* off, int i) {
+      return off[i / 2] < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + off[i / 2] + (i % 2) * 8 * D);
+    };
+    const uint32_t write_at = part * kHalf + (first + sub) * 128 + (((2 * chunk) ^ sub) << 4);
+    auto turn = [&](uint32_t dst, const int8_t* src, const int64_t* off) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const uint32_t row = first + i * 8 + sub;
         const uint2 x = bf16x4_of_int8(raw[i].x), y = bf16x4_of_int8(raw[i].y), z = bf16x4_of_int8(raw[i].z), u = bf16x4_of_int8(raw[i].w);
-        raw[i] = fetch(src, j, pages, i);
-        sts128(dst + part * kHalf + swizzled(row, 2 * chunk), make_uint4(x.x, x.y, y.x, y.y));
-        sts128(dst + part * kHalf + swizzled(row, 2 * chunk + 1), make_uint4(z.x, z.y, u.x, u.y));
+        raw[i] = fetch(src, off, i);
+        sts128(dst + write_at + i * 1024, make_uint4(x.x, x.y, y.x, y.y));  // row mod 8 is sub: swizzled(row, 2 * chunk)
+        sts128((dst + write_at + i * 1024) ^ 16u, make_uint4(z.x, z.y, u.x, u.y));
       }
       fence_smem();
+      __syncwarp();
     };
     // the thread's scale of the tile: a key's in the first half of the threads, a value's in the second
     const bool is_v = t >= kTile;
     const float* scales = is_v ? c.v_scale : c.k_scale;
     const float factor = is_v ? 1.f : a.scale * 1.44269504088896340736f;  // log2(e)
-    const uint32_t scale_at = base + (is_v ? L::v_scale : L::k_scale) + 4 * (t % kTile);
+    const uint32_t scale_at = base + L::scale + (t % kTile / 2) * 16 + (t & 1) * 4 + (is_v ? 8 : 0);  // pairs: (k, k, v, v)
     auto fetch_scale = [&](uint32_t j, int32_t pages) -> float {
       const int32_t p = __shfl_sync(~0u, pages, (t % kTile) >> 4);
       const uint32_t tok = j * kTile + t % kTile;
@@ -402,26 +407,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     };
     float scale = 0.f;
     int32_t pages = pages_of(0);
+    int64_t off[kGroups];
+    offsets(0, pages, off);
     if (tiles) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) raw[i] = fetch(c.k, 0, pages, i);
+      for (int i = 0; i < kLoads; ++i) raw[i] = fetch(c.k, off, i);
       scale = fetch_scale(0, pages);
     }
     for (uint32_t j = 0; j < tiles; ++j) {
       const uint32_t buf = j & 1, use = j >> 1;
-      const int32_t next = pages_of(j + 1);  // -1 behind the last tile: nothing is fetched for it
+      pages = pages_of(j + 1);  // -1 behind the last tile: nothing is fetched for it
       if (!__all_sync(~0u, bar_wait(bars + kKEmpty + 8 * buf, (use & 1) ^ 1, stop))) break;
       // The scales have four places: those of tile j - 4 were read before the products of tile j - 3 could begin, and
       // this K buffer is free since those of tile j - 2 are done.
-      sts32(scale_at + (j & 3) * 512, __float_as_uint(scale));
-      bar_arrive(bars + kScaleFull + 8 * (j & 3));
-      turn(base + L::k + buf * L::kOperand, c.v, j, pages);
-      bar_arrive(bars + kKFull + 8 * buf);
-      pages = next;
+      sts32(scale_at + (j & 3) * 1024, __float_as_uint(scale));
+      turn(base + L::k + buf * L::kOperand, c.v, off);
+      if (lane == 0) {
+        bar_arrive(bars + kScaleFull + 8 * (j & 3));
+        bar_arrive(bars + kKFull + 8 * buf);
+      }
+      offsets(j + 1, pages, off);
       scale = fetch_scale(j + 1, pages);
       if (!__all_sync(~0u, bar_wait(bars + kVEmpty + 8 * buf, (use & 1) ^ 1, stop))) break;
-      turn(base + L::v + buf * L::kOperand, c.k, j + 1, pages);
-      bar_arrive(bars + kVFull + 8 * buf);
+      turn(base + L::v + buf * L::kOperand, c.k, off);
+      if (lane == 0) bar_arrive(bars + kVFull + 8 * buf);
     }
   } else {
     // ---- products: the warp runs the loop as one, an elected thread issues ------------------------
@@ -440,12 +449,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
           commit(bars + kSFull + 8 * i);
         }
       };
-      auto values = [&](uint32_t i, uint32_t buf, bool add) {
-        const uint64_t v = smem_desc(base + L::v + buf * L::kOperand, kHalf);
+      // tokens 64 h .. 64 h + 63 of the tile
+      auto values = [&](uint32_t i, uint32_t buf, uint32_t h, bool add) {
+        const uint64_t v = smem_desc(base + L::v + buf * L::kOperand, kHalf) + h * (4 * 2048 >> 4);
+        const uint32_t p = tmem + 128 * i + 32 * h;
         if (lead) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mma_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * e, v + e * (2048 >> 4), kO, add || e > 0);
-          commit(bars + kOFull + 8 * i);
+          for (int e = 0; e < 4; ++e) mma_ts(tmem + 256 + D * i, p + 8 * e, v + e * (2048 >> 4), kO, add || e > 0);
+          commit(bars + kOFull + 16 * i + 8 * h);
         }
       };
       auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(~0u, bar_wait(bars + bar, parity, stop)); };
@@ -458,24 +469,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       }
       for (uint32_t j = 0; ok && j < tiles; ++j) {
         const uint32_t buf = j & 1, nbuf = buf ^ 1;
-        ok = wait(kVFull + 8 * buf, (j >> 1) & 1) && wait(kPFull, j & 1);
-        if (!ok) break;
-        fence_after();
-        values(0, buf, j > 0);
-        if (j + 1 < tiles) {
-          ok = wait(kKFull + 8 * nbuf, ((j + 1) >> 1) & 1);
+        ok = wait(kVFull + 8 * buf, (j >> 1) & 1);
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i) {
+#pragma unroll
+          for (uint32_t h = 0; h < 2; ++h) {
+            ok = ok && wait(kPFull + 16 * i + 8 * h, j & 1);
+            if (!ok) break;
+            fence_after();
+            values(i, buf, h, j > 0 || h > 0);
+          }
           if (!ok) break;
-          fence_after();
-          scores(0, nbuf);
-        }
-        ok = wait(kPFull + 8, j & 1);
-        if (!ok) break;
-        fence_after();
-        values(1, buf, j > 0);
-        if (lead) commit(bars + kVEmpty + 8 * buf);
-        if (j + 1 < tiles) {
-          scores(1, nbuf);
-          if (lead) commit(bars + kKEmpty + 8 * nbuf);
+          if (i == 1 && lead) commit(bars + kVEmpty + 8 * buf);
+          if (j + 1 < tiles) {
+            if (i == 0) ok = wait(kKFull + 8 * nbuf, ((j + 1) >> 1) & 1);
+            if (!ok) break;
+            fence_after();
+            scores(i, nbuf);
+            if (i == 1 && lead) commit(bars + kKEmpty + 8 * nbuf);
+          }
         }
       }
       if (!ok) {
