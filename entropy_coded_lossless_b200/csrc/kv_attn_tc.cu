@@ -4,11 +4,14 @@
 // A block takes 256 rows of one key head: row = (query, head of the group), so every key and value it reads serves all
 // heads of the group, whatever their number. It walks the sequence in tiles of 128 tokens:
 //   S = Q K^T      tcgen05.mma, bf16, M = 128 rows, N = 128 tokens, two of them (rows 0-127, rows 128-255), into TMEM
-//   s = S * k_scale_j * softmax_scale * log2(e);  p = 2^(s - m);  l += p;  P = bf16(p * v_scale_j)   one thread per row
-//   O += P V       tcgen05.mma with P read from TMEM (it takes the place of S), V as the integers
-// K and V enter as the integers, which bf16 holds exactly, so nothing is rounded on the way in; their scales are
-// applied to the float32 scores and weights. The one rounding inside is P's to bf16: the tensor cores multiply
-// 16-bit operands, and bf16 (8 bits, float32's range) needs no care for the scales' size where fp16 would.
+//   s = S * k_scale_j * softmax_scale * log2(e);  p = 2^(s - m);  l += p;  P = fp16(p)
+//   O += P V       tcgen05.mma, fp16, P read from TMEM (it takes the place of S)
+// Keys enter as the integers, which bf16 holds exactly, and their scales are applied to the float32 scores: scores have
+// float32's error. Values enter as fp16(int8 * v_scale * 2^-e), e the exponent of the tile's largest value scale, the
+// product formed to more than fp16's 11 bits and rounded once; the weights are rounded to fp16 (2^-11 each, where bf16 operands
+// would cost 2^-8 twice). The power of two goes into the weights: P = p 2^(e - E), with E the exponent O is held in, raised
+// like the softmax's reference when a tile's values are more than 2^7 larger. A weight smaller than 2^-24 of that range is
+// lost, so O is exact to 2^-24 of the largest value of the sequence, or 2^-11 of what is summed.
 //
 // Softmax in one pass: m is a running maximum in units of log2. It is only raised when a row's maximum grows by more
 // than 8, i.e. a weight may reach 2^8 before the sums are scaled down: that is exact in float32 and bf16 alike
@@ -30,18 +33,20 @@ namespace {
 using namespace tc;
 
 constexpr uint32_t kSoftWarps = 16, kConvertWarps = 8;
-constexpr uint32_t kSoftThreads = 32 * kSoftWarps, kConvertThreads = 32 * kConvertWarps;
+constexpr uint32_t kSoftThreads = 32 * kSoftWarps;
 constexpr uint32_t kIssueWarp = kSoftWarps + kConvertWarps;  // in a warpgroup of its own
 constexpr uint32_t kThreads = 32 * (kIssueWarp + 4);
 constexpr uint32_t kTile = 128;      // tokens of a tile
 constexpr uint32_t kRows = 256;      // query rows of a block
-constexpr float kRise = 8.f;         // how far (log2) a weight may pass 1 before the reference is raised
+constexpr float kRise = 8.f;         // how far (log2) a weight may pass 1 before the reference is raised,
+constexpr float kValueRise = 7.f;    // and a tile's values the range O is held in: 2^15 together, within fp16
+constexpr float kValueFall = -60.f;  // a tile this far below adds nothing to O in fp16
 constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows of 64 bf16
 
 template <int D>
 struct Layout {
   static constexpr uint32_t kOperand = 128 * D * 2;  // one 128 x D bf16 operand
-  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, row_sum = scale + 4 * 1024, bars = row_sum + 4 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
+  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, info = scale + 4 * 512, row_sum = info + 64, bars = row_sum + 4 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
 };
 // barriers
 enum : uint32_t { kQFull = 0, kKFull = 8, kKEmpty = 24, kVFull = 40, kVEmpty = 56, kScaleFull = 72, kSFull = 104, kPFull = 120, kOFull = 152, kDrain = 184 };
@@ -164,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
 
   if (warp < kSoftWarps) {
     // ---- softmax -------------------------------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // the queries of the block as an operand, zeros behind the last row
     for (uint32_t i = tid; i < kRows * (D / 8); i += kSoftThreads) {
       const uint32_t row = i / (D / 8), piece = i % (D / 8);
@@ -189,12 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     };
     int32_t seen[2];
     float m[2], l[2];
-    uint64_t neg[2];  // minus the reference, twice (0 while there is none)
-    float limit[2];   // how far a score may be above it
+    float neg[2];    // minus the reference (0 while there is none)
+    float limit[2];  // how far a score may be above it
+    float held = 0.f;  // E: O is in units of 2^held
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       seen[r] = seen_by(half * 128 + lanes + quad + 8 * r);
-      m[r] = -INFINITY, l[r] = 0.f, neg[r] = 0, limit[r] = -INFINITY;
+      m[r] = -INFINITY, l[r] = 0.f, neg[r] = 0.f, limit[r] = -INFINITY;
     }
     bool ok = true;
     for (uint32_t j = 0; j < tiles && ok; ++j) {
@@ -202,6 +208,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       fence_after();
+      const float e_v = __uint_as_float(lds32(base + L::info + (j & 3) * 4));
+      const bool larger = j > 0 && e_v > held + kValueRise;
+      const float lower = larger ? pow2(fmaxf(held - e_v, -126.f)) : 1.f;  // what O is scaled by then
+      if (j == 0 || larger) held = e_v;
+      const float by = fmaxf(e_v - held, kValueFall), unby = pow2(-by);
       // half a tile (64 tokens) at a time: its part of P V can begin while the other half is worked on
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -209,44 +220,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         uint32_t s[32];
         ld_quad32(s_at + 64 * h, s);
         wait_ld();
-        const uint32_t scales = base + L::scale + (j & 3) * 1024 + h * 512 + 8 * col;
+        const uint32_t scales = after_here(base + L::scale + (j & 3) * 512 + h * 256 + 4 * col);
         const int32_t first = (int32_t)(j * kTile + 64 * h + col);
         const bool edge = __any_sync(~0u, first - (int32_t)col + 64 > min(seen[0], seen[1]));
         float top[2];
-        uint64_t sum[2];
+        uint64_t sum[2], ref[2];
         // Weights against the reference that stands; scores relative to it are watched, not searched first: almost
         // always none is above the limit and this one pass is all. (Two versions: only tiles at the end of what a row
         // sees look at the columns' places.)
         auto weights = [&](auto edge_tag) {
           constexpr bool kEdge = decltype(edge_tag)::value;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) top[r] = -INFINITY, sum[r] = 0;
+          for (int r = 0; r < 2; ++r) top[r] = -INFINITY, sum[r] = 0, ref[r] = pack2(neg[r] + by, neg[r] + by);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {  // 32 columns: 16 of packed pairs
             uint32_t p[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int n = 4 * b + i;
-              const uint4 f = lds128_free(scales + 64 * n);
-              const uint64_t ks = pack2(__uint_as_float(f.x), __uint_as_float(f.y)), vs = pack2(__uint_as_float(f.z), __uint_as_float(f.w));
+              const uint64_t ks = lds64_free(scales + 32 * n);
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
                 const uint32_t* v = &s[4 * n + 2 * r];
                 float x, y;
-                unpack2(fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), ks, neg[r]), x, y);
+                unpack2(fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), ks, ref[r]), x, y);
                 if constexpr (kEdge) {
                   x = first + 8 * n < seen[r] ? x : -INFINITY;
                   y = first + 8 * n + 1 < seen[r] ? y : -INFINITY;
                 }
                 top[r] = max3(top[r], x, y);
-                const uint64_t e2 = pack2(exp2_approx(x), exp2_approx(y));
-                sum[r] = add2(sum[r], e2);
-                unpack2(mul2(e2, vs), x, y);
-                if constexpr (kEdge) {  // a scale behind the row's end may be anything: 0 * infinity
-                  x = first + 8 * n < seen[r] ? x : 0.f;
-                  y = first + 8 * n + 1 < seen[r] ? y : 0.f;
-                }
-                p[2 * i + r] = bf16_pack(x, y);
+                x = exp2_approx(x), y = exp2_approx(y);
+                sum[r] = add2(sum[r], pack2(x, y));
+                p[2 * i + r] = fp16_pack(x, y);
               }
             }
             st_pairs8(s_at + 32 * h + 16 * b, p);
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         };
         if (edge) weights(std::true_type{});
         else weights(std::false_type{});
-        if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
+        if (__any_sync(~0u, top[0] > limit[0] + by || top[1] > limit[1] + by) || (larger && h == 0)) {
           // the reference rises: what is summed is scaled down, and the weights formed again
           float keep[2];
 #pragma unroll
@@ -262,14 +267,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
             top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
             top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
             keep[r] = 1.f;
-            if (top[r] > limit[r]) {
-              const float next = m[r] == -INFINITY ? top[r] : m[r] + top[r];
+            if (top[r] > limit[r] + by) {
+              const float next = (m[r] == -INFINITY ? 0.f : m[r]) + (top[r] - by);
               keep[r] = exp2_approx(m[r] - next);
               m[r] = next;
-              neg[r] = pack2(-next, -next);
+              neg[r] = -next;
               limit[r] = kRise;
             }
             l[r] *= keep[r];
+            if (h == 0) keep[r] *= lower;
           }
           if (j > 0 || h > 0) {
             ok = __all_sync(~0u, bar_wait(bars + kOFull + 16 * half + 8 * (h ^ 1), (j + h + 1) & 1, stop));  // the part before this one
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         for (int r = 0; r < 2; ++r) {
           float x, y;
           unpack2(sum[r], x, y);
-          l[r] += x + y;
+          l[r] = fmaf(x + y, unby, l[r]);
         }
         wait_st();
         fence_before();
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       const uint32_t row = half * 128 + rows32 + lane, g = w.row0 + row;
       const bool any = seen_by(row) > 0;
       // no token seen: zeros. (A sum that is not positive although tokens were seen is a NaN's or an infinity's.)
-      const float inv = any ? 1.f / __uint_as_float(lds32(sums + 4 * (rows32 + lane))) : 0.f;
+      const float inv = any ? pow2(held) / __uint_as_float(lds32(sums + 4 * (rows32 + lane))) : 0.f;
       const uint32_t first = (warp >> 2 & 1) * (D / 2);
       uint16_t* dst = a.out + (uint64_t)(w.q0 + g / group) * a.out_stride + (uint64_t)(hk * group + g % group) * D + first;
 #pragma unroll
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     }
   } else if (warp < kIssueWarp) {
     // ---- fetch and convert ---------------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     constexpr int kLoads = D / 32;  // 16-byte loads of a thread per operand
     const uint32_t t = tid - kSoftThreads, cw = t >> 5;
     // A warp's load: 4 lanes on 64 values of a row, 8 rows. For D = 128 even warps take the rows' first 64 values.
@@ -383,10 +389,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       return off[i / 2] < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + off[i / 2] + (i % 2) * 8 * D);
     };
     const uint32_t write_at = part * kHalf + (first + sub) * 128 + (((2 * chunk) ^ sub) << 4);
-    auto turn = [&](uint32_t dst, const int8_t* src, const int64_t* off) {
+    auto turn = [&](auto value_tag, uint32_t row_scale, uint32_t dst, const int8_t* src, const int64_t* off) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const uint2 x = bf16x4_of_int8(raw[i].x), y = bf16x4_of_int8(raw[i].y), z = bf16x4_of_int8(raw[i].z), u = bf16x4_of_int8(raw[i].w);
+        uint2 x, y, z, u;
+        if constexpr (decltype(value_tag)::value) {
+          const uint32_t f = __shfl_sync(~0u, row_scale, (first + i * 8 + sub) & 31);
+          const uint32_t hi = __byte_perm(f, 0, 0x1010), lo = __byte_perm(f, 0, 0x3232);
+          x = fp16x4_of_int8(raw[i].x, hi, lo), y = fp16x4_of_int8(raw[i].y, hi, lo);
+          z = fp16x4_of_int8(raw[i].z, hi, lo), u = fp16x4_of_int8(raw[i].w, hi, lo);
+        } else {
+          x = bf16x4_of_int8(raw[i].x), y = bf16x4_of_int8(raw[i].y), z = bf16x4_of_int8(raw[i].z), u = bf16x4_of_int8(raw[i].w);
+        }
         raw[i] = fetch(src, off, i);
         sts128(dst + write_at + i * 1024, make_uint4(x.x, x.y, y.x, y.y));  // row mod 8 is sub: swizzled(row, 2 * chunk)
         sts128((dst + write_at + i * 1024) ^ 16u, make_uint4(z.x, z.y, u.x, u.y));
@@ -394,25 +408,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       fence_smem();
       __syncwarp();
     };
-    // the thread's scale of the tile: a key's in the first half of the threads, a value's in the second
-    const bool is_v = t >= kTile;
-    const float* scales = is_v ? c.v_scale : c.k_scale;
-    const float factor = is_v ? 1.f : a.scale * 1.44269504088896340736f;  // log2(e)
-    const uint32_t scale_at = base + L::scale + (t % kTile / 2) * 16 + (t & 1) * 4 + (is_v ? 8 : 0);  // pairs: (k, k, v, v)
-    auto fetch_scale = [&](uint32_t j, int32_t pages) -> float {
-      const int32_t p = __shfl_sync(~0u, pages, (t % kTile) >> 4);
-      const uint32_t tok = j * kTile + t % kTile;
-      if (p < 0 || (int32_t)tok >= most) return 0.f;
-      return scales[kv_row(c, (uint32_t)p, hk, tok & pt_mask)] * factor;
+    // Scales: a lane holds the value scales of tokens lane, lane + 32, +64, +96 of the tile (every warp, so that each finds the
+    // tile's largest by itself), and in the first four warps the key scale of token t.
+    const float factor = a.scale * 1.44269504088896340736f;  // log2(e)
+    float k_scale = 0.f, v_scale[4];
+    auto fetch_scales = [&](uint32_t j, int32_t pages) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t p = __shfl_sync(~0u, pages, 2 * i + (lane >> 4));
+        const uint32_t tok = j * kTile + 32 * i + lane;
+        const bool is = p >= 0 && (int32_t)tok < most;
+        const uint64_t at = kv_row(c, (uint32_t)p, hk, tok & pt_mask);
+        v_scale[i] = is ? c.v_scale[at] : 0.f;
+        if (cw == (uint32_t)i) k_scale = is ? c.k_scale[at] * factor : 0.f;
+      }
     };
-    float scale = 0.f;
     int32_t pages = pages_of(0);
     int64_t off[kGroups];
     offsets(0, pages, off);
     if (tiles) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) raw[i] = fetch(c.k, off, i);
-      scale = fetch_scale(0, pages);
+      fetch_scales(0, pages);
     }
     for (uint32_t j = 0; j < tiles; ++j) {
       const uint32_t buf = j & 1, use = j >> 1;
@@ -420,23 +437,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if (!__all_sync(~0u, bar_wait(bars + kKEmpty + 8 * buf, (use & 1) ^ 1, stop))) break;
       // The scales have four places: those of tile j - 4 were read before the products of tile j - 3 could begin, and
       // this K buffer is free since those of tile j - 2 are done.
-      sts32(scale_at + (j & 3) * 1024, __float_as_uint(scale));
-      turn(base + L::k + buf * L::kOperand, c.v, off);
+      // A value scale that is not finite (or so large that its values would not be) makes the token's key scale NaN, and its values
+      // zeros: whoever sees the token gets NaN, and a masked weight of 0 meets no infinity.
+      uint32_t top = 0;
+      float mine = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool bad = !(fabsf(v_scale[i]) < 1e36f);
+        if (bad) v_scale[i] = 0.f;
+        if (cw == (uint32_t)i) sts32(base + L::scale + (j & 3) * 512 + 4 * t, bad ? 0x7FC00000u : __float_as_uint(k_scale));
+        top = max(top, __float_as_uint(fabsf(v_scale[i])));
+        if ((first >> 5) == (uint32_t)i) mine = v_scale[i];
+      }
+      top = __reduce_max_sync(~0u, top) >> 23;  // 2^(top - 127) <= the largest scale < 2^(top - 126)
+      const uint32_t e_v = max(top, 1u);
+      if (t == 0) sts32(base + L::info + (j & 3) * 4, __float_as_uint((float)(int32_t)(e_v - 127)));
+      // the scale of row first + lane (mod 32) in [0, 2) as fp16 and what that leaves over, packed
+      const uint32_t row_scale = split_fp16(mine * __uint_as_float((254u - e_v) << 23));
+      turn(std::false_type{}, 0u, base + L::k + buf * L::kOperand, c.v, off);
       if (lane == 0) {
         bar_arrive(bars + kScaleFull + 8 * (j & 3));
         bar_arrive(bars + kKFull + 8 * buf);
       }
       offsets(j + 1, pages, off);
-      scale = fetch_scale(j + 1, pages);
+      fetch_scales(j + 1, pages);
       if (!__all_sync(~0u, bar_wait(bars + kVEmpty + 8 * buf, (use & 1) ^ 1, stop))) break;
-      turn(base + L::v + buf * L::kOperand, c.k, off);
+      turn(std::true_type{}, row_scale, base + L::v + buf * L::kOperand, c.k, off);
       if (lane == 0) bar_arrive(bars + kVFull + 8 * buf);
     }
   } else {
     // ---- products: the warp runs the loop as one, an elected thread issues ------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == kIssueWarp && tiles) {
-      constexpr uint32_t kS = instr_desc(128, 128, false), kO = instr_desc(128, D, true);
+      constexpr uint32_t kS = instr_desc(128, 128, true, false), kO = instr_desc(128, D, false, true);
       const bool lead = elect_one();
       auto scores = [&](uint32_t i, uint32_t buf) {
         const uint64_t q = smem_desc(base + L::q + i * L::kOperand, 16), k = smem_desc(base + L::k + buf * L::kOperand, 16);

@@ -2,6 +2,8 @@
 // exact INT8 -> bf16 step in front of them.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "kv_internal.cuh"
 
 namespace shn {
@@ -62,9 +64,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// kind::f16 instruction descriptor: f32 accumulator, bf16 operands, M x N; b_rows_along_k: B is MN-major.
-__host__ __device__ constexpr uint32_t instr_desc(uint32_t m, uint32_t n, bool b_rows_along_k) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_rows_along_k ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+// kind::f16 instruction descriptor: f32 accumulator, bf16 or fp16 operands, M x N; b_rows_along_k: B is MN-major.
+__host__ __device__ constexpr uint32_t instr_desc(uint32_t m, uint32_t n, bool bf16, bool b_rows_along_k) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_rows_along_k ? 1u : 0u) << 16) | ((n >> 3) << 17) |
+         ((m >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -141,10 +144,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// 16 bytes of shared memory that nothing writes while they are read (no ordering asked for)
-__device__ __forceinline__ uint4 lds128_free(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+// 8 bytes of shared memory that nothing writes while they are read. The compiler may place the load freely after what
+// the address depends on; `after_here` makes an address depend on a place in the program (behind a wait).
+__device__ __forceinline__ uint32_t after_here(uint32_t a) {
+  asm volatile("" : "+r"(a)::"memory");
+  return a;
+}
+__device__ __forceinline__ uint64_t lds64_free(uint32_t a) {
+  uint64_t v;
+  asm("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -152,6 +160,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
+// 2^n, exactly, for a whole number n in [-126, 127]
+__device__ __forceinline__ float pow2(float n) { return __int_as_float(((int)n + 127) << 23); }
 
 // INT8 -> bf16, exactly. bf16 has 8 significant bits, so from 128 to 255 its step is 1: 0x4300 | m is 128 + m for a
 // 7-bit m, and 0x4380 is 256. With a byte x = m - 128 s (m its low 7 bits, s its sign bit), x = (128 + m) - (s ? 256 : 128)
@@ -167,6 +178,33 @@ __device__ __forceinline__ uint32_t bf16x2_of_int8(uint32_t w, uint32_t sel) {
 // the 4 bytes of w in order, as 2 x bf16x2
 __device__ __forceinline__ uint2 bf16x4_of_int8(uint32_t w) {
   return make_uint2(bf16x2_of_int8(w, 0x4140), bf16x2_of_int8(w, 0x4342));
+}
+
+// (lo, hi) rounded to fp16, packed
+__device__ __forceinline__ uint32_t fp16_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// x as fp16 (low half) and what that leaves over, in fp16 (high half): x to about 22 bits where it is near 1
+__device__ __forceinline__ uint32_t split_fp16(float x) {
+  const __half hi = __float2half_rn(x);
+  const __half lo = __float2half_rn(x - __half2float(hi));
+  return (uint32_t)__half_as_ushort(hi) | (uint32_t)__half_as_ushort(lo) << 16;
+}
+// Two bytes times a scale hi + lo (each twice), rounded to fp16. 0x6400 | u is 1024 + u in fp16, u = x + 128: minus
+// 1152 that is x, exactly. x * lo is rounded far below fp16's last bit of x * hi, and the sum once.
+__device__ __forceinline__ uint32_t fp16x2_of_int8(uint32_t w, uint32_t sel, uint32_t hi, uint32_t lo) {
+  const uint32_t t = __byte_perm(w, 0x64646464u, sel);
+  uint32_t x, y, r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(t), "r"(0x64806480u));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(lo));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(hi), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint2 fp16x4_of_int8(uint32_t w, uint32_t hi, uint32_t lo) {
+  w ^= 0x80808080u;
+  return make_uint2(fp16x2_of_int8(w, 0x4140, hi, lo), fp16x2_of_int8(w, 0x4342, hi, lo));
 }
 
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {

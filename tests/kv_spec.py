@@ -54,13 +54,18 @@ def token_slots(pages, pt, n):
 
 def attention(q, k, v, seen, scale):
     """q [rows, dim], k and v [tokens, dim] float64; row i sees the first seen[i] tokens. Returns (out, bound): the
-    result and, for each value, how far float32 arithmetic with the weights rounded once to bfloat16 and
-    the result once to bfloat16 may be from it.
+    result and, for each value, how far it may be off with float32 scores and sums, weights and values rounded once to
+    fp16 or bfloat16 and the result once to bfloat16.
 
-    The bound: a weight is rounded by at most eps/2 = 2^-8 of itself; a score is a float32 sum of dim products
-    (error at most (dim + 8) 2^-24 times the sum of their magnitudes, the scalings included), which
-    changes a weight's share by at most 2 max(error); the sums over n tokens add at most (2 n + 64) 2^-24, which covers
-    the exponential's 2^-22; the result is rounded by 2^-8 of itself."""
+    The bound: a weight and a value are rounded by at most 2^-8 of themselves together (bfloat16 weights: eps/2 = 2^-8; fp16
+    weights and values: 2^-11 each). fp16 has a floor besides, half its smallest step, 2^-25: a weight p <= 2^8 enters as
+    p 2^(e - E), where 2^e is the size of its tile's value scales and 2^E that of the range the sum is held in, and its value as
+    v 2^-e, below 254. So one key's product is off by at most 2^-25 254 2^E, and 2^E is at most the largest value scale, which is
+    vmax / 127 with vmax the largest value an INT8 127 can stand for: 2^-24 vmax a key, against a sum of weights of at least 1. The
+    largest value of the tokens given stands for vmax; twice that covers a largest INT8 of only 64.
+    A score is a float32 sum of dim products (error at most (dim + 8) 2^-24 times the sum of their magnitudes, the scalings
+    included), which changes a weight's share by at most 2 max(error); the sums over n tokens add at most (2 n + 64) 2^-24,
+    which covers the exponential's 2^-22; the result is rounded by 2^-8 of itself."""
     s = q @ k.T * scale
     mask = torch.arange(k.shape[0], device=k.device)[None, :] >= seen[:, None]
     s = s.masked_fill(mask, -math.inf)
@@ -70,7 +75,8 @@ def attention(q, k, v, seen, scale):
     mass = w @ v.abs()
     size = (q.abs() @ k.abs().T * abs(scale)).masked_fill(mask, 0.0).amax(-1, keepdim=True) if k.shape[0] else q.new_zeros(q.shape[0], 1)
     err = 2 * (q.shape[1] + 8) * 2.0**-24 * size + (2 * k.shape[0] + 64) * 2.0**-24 + 2.0**-8
-    return out, err * mass + 2.0**-8 * out.abs() + 1e-30
+    floor = 2.0**-23 * (w > 0).sum(-1, keepdim=True) * v.abs().max() if k.shape[0] else 0.0
+    return out, err * mass + floor + 2.0**-8 * out.abs() + 1e-30
 
 
 def cache_attention(q, cache, pages_of, kv_len, cu, scale, prefix=None):
