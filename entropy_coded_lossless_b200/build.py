@@ -11,10 +11,11 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libshn.so")
 SOURCES = ["capi.cu", "histogram.cu", "build_tables.cu", "encode.cu", "decode.cu", "noalloc.cu", "offload.cu",
-           "kv_capi.cu", "kv_plan.cu", "kv_store.cu", "kv_attn.cu", "kv_attn_tc.cu"]
+           "kv_capi.cu", "kv_plan.cu", "kv_store.cu", "kv_attn_tc.cu", "kv_decode.cu"]
 HEADERS = [os.path.join(CSRC, "shn_internal.cuh"), os.path.join(ROOT, "include", "shn.h")]
 # the paged KV cache's sources (kv_*.cu) alone include these
-KV_HEADERS = [os.path.join(CSRC, "kv_internal.cuh"), os.path.join(CSRC, "kv_tc.cuh"), os.path.join(ROOT, "include", "shn_kv.h")]
+KV_HEADERS = [os.path.join(CSRC, "kv_internal.cuh"), os.path.join(CSRC, "kv_tc.cuh"),
+              os.path.join(CSRC, "kv_decode.cuh"), os.path.join(ROOT, "include", "shn_kv.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]

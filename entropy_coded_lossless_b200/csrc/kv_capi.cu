@@ -1,6 +1,6 @@
 // kv_capi.cu — the extern "C" entry points of include/shn_kv.h: argument checks and launches.
 // No device allocation and no synchronisation.
-#include "kv_internal.cuh"
+#include "kv_decode.cuh"
 
 using namespace shn;
 
@@ -61,6 +61,26 @@ int check_attn(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32
                    !rows_ok(d_out, out_stride, q_heads, cache->head_dim, n_tokens)))
     return SHN_ERR_INVALID_ARG;
   return SHN_OK;
+}
+
+// How shn_kv_attn_shared is cut up, and its workspace: [status 256][pieces' sums][pieces' (mt, ms, l)].
+struct SharedLayout {
+  DecodePlan pl;
+  size_t out_off, ml_off, total;
+};
+
+SharedLayout shared_layout(const shn_kv_cache* c, uint32_t n_reqs, uint32_t q_heads) {
+  SharedLayout x = {};
+  const uint32_t group = q_heads / c->kv_heads;
+  x.pl.rows = group <= 8 ? 8 : 16;  // the rows of one mma are 8; 16 share what is done for a token's bytes
+  x.pl.own_groups = (group + x.pl.rows - 1) / x.pl.rows;
+  x.pl.prefix_groups = (uint32_t)(((uint64_t)n_reqs * group + x.pl.rows - 1) / x.pl.rows);
+  const uint64_t segs = (uint64_t)c->kv_heads * (x.pl.prefix_groups + (uint64_t)n_reqs * x.pl.own_groups);
+  const uint64_t pieces = (kDecodeMaxWarps + segs) * x.pl.rows;
+  x.out_off = 256;
+  x.ml_off = x.out_off + round_up(pieces * c->head_dim * sizeof(float), 256);
+  x.total = x.ml_off + round_up(pieces * sizeof(float4), 256);
+  return x;
 }
 
 }  // namespace
@@ -178,7 +198,7 @@ size_t shn_kv_attn_shared_workspace_bytes(const shn_kv_cache* cache, uint32_t n_
   if (check_cache(cache) != SHN_OK || q_heads == 0 || q_heads % cache->kv_heads ||
       q_heads / cache->kv_heads > kMaxGroup || n_reqs >= (1u << 31) / q_heads)
     return 0;
-  return SHN_KV_WORKSPACE_BYTES;
+  return shared_layout(cache, n_reqs, q_heads).total;
 }
 
 int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, uint32_t q_heads,
@@ -192,7 +212,8 @@ int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, 
   if (!d_prefix_len || (n_prefix_pages && !d_prefix_pages) ||
       (uint64_t)n_prefix_pages * cache->page_tokens >= (1ull << 31))
     return SHN_ERR_INVALID_ARG;
-  e = check_work(d_work, work_bytes, shn_kv_attn_shared_workspace_bytes(cache, n_reqs, q_heads));
+  SharedLayout x = shared_layout(cache, n_reqs, q_heads);
+  e = check_work(d_work, work_bytes, x.total);
   if (e != SHN_OK) return e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   KvAttnArgs a = {};
@@ -203,7 +224,18 @@ int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, 
   a.st = clear_status(d_work, s);
   if (!a.st) return SHN_ERR_CUDA;
   if (n_reqs == 0) return SHN_OK;
-  return launch_kv_attn(pages_of(cache), cache->head_dim, a, s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
+  uint8_t* wb = static_cast<uint8_t*>(d_work);
+  x.pl.out = reinterpret_cast<float*>(wb + x.out_off);
+  x.pl.ml = reinterpret_cast<float4*>(wb + x.ml_off);
+  // warps: two blocks on each SM (one for 16 rows, which takes more registers), but no more than there can be units
+  const uint64_t units = (uint64_t)cache->kv_heads * x.pl.prefix_groups * (((uint64_t)n_prefix_pages * cache->page_tokens + kUnit - 1) / kUnit) +
+                         (uint64_t)n_reqs * cache->kv_heads * x.pl.own_groups * (((uint64_t)max_blocks * cache->page_tokens + kUnit - 1) / kUnit + 1);
+  const uint64_t per_block = kDecodeThreads / 32;
+  uint64_t blocks = (uint64_t)sm_count_for_launch() * (x.pl.rows == 8 ? 2 : 1);
+  if (blocks > (units + per_block - 1) / per_block) blocks = (units + per_block - 1) / per_block;
+  if (blocks > kDecodeMaxWarps / per_block) blocks = kDecodeMaxWarps / per_block;
+  x.pl.warps = (uint32_t)(blocks * per_block);
+  return launch_kv_decode(pages_of(cache), cache->head_dim, a, x.pl, s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,424 @@
+// kv_decode.cu — attention of single tokens over the paged INT8 cache, with a prefix that the requests share
+// (shn_kv_attn_shared).
+//
+// Bound by reading the cache: a token's keys and values of one key head are 2 (head_dim + 4) bytes, used by few rows. So
+// bytes go from global memory straight into the registers that feed mma.sync, no shared memory between: with the
+// order of the contracted dimension free (as long as both operands agree) a lane's 16 consecutive bytes are its
+// operands of several steps. Rows are the narrow side:
+//   S' = K Q'   m16 (tokens) n8 (query rows) k16, 16 tokens a step
+//   O' = V' P'  m16 (values of a head) n8 (query rows) k16 (the 16 tokens); P' is S' transposed by movmatrix
+// INT8 enters as fp16, exactly (1024 + u with u = x + 128 is a byte put into fp16's last bits; minus 1152 it is x). A query row
+// is scaled by a power of two into fp16, exactly but for parts 2^-25 of its largest. Scales meet the float32 scores: with
+// x = s k_scale softmax_scale log2(e),
+//   l += 2^(x - ms),   P = sign(v_scale) 2^(x + log2|v_scale| - mt)  rounded to fp16 (2^-11)
+// two exponentials a score, so that P lies in fp16's range whatever the value scales are. ms and mt are running references
+// raised only when a score passes them by 8 (log2), which spares a reduction across lanes almost always.
+#include "kv_decode.cuh"
+#include "kv_tc.cuh"
+
+namespace shn {
+namespace {
+
+using namespace tc;
+
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float log2_approx(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// two fp16 of 1024 + byte -> the signed bytes (their sign bits inverted before)
+__device__ __forceinline__ uint32_t minus1152(uint32_t t) {
+  uint32_t x;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(t), "r"(0x64806480u));
+  return x;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_kernel(KvPages c, KvAttnArgs a, DecodePlan pl) {
+  constexpr uint32_t kRows = 8 * NT;
+  constexpr int kKLoads = D / 64;  // 16-byte loads of a token's keys per lane
+  __shared__ UnitScan scan;
+  const uint32_t lane = threadIdx.x & 31, g = lane >> 2, cc = lane & 3;
+  const uint32_t w = blockIdx.x * (kDecodeThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t group = a.q_heads / c.kv_heads;
+  bool bad;
+  const int32_t prefix = decode_prefix(c, a, bad);
+  if (bad && blockIdx.x == 0 && threadIdx.x == 0) report(a.st, SHN_ERR_INVALID_ARG, 0);
+  scan_units(c, a, prefix, scan, blockIdx.x == 0);
+
+  const uint32_t prefix_units = pl.prefix_groups ? ((uint32_t)prefix + kUnit - 1) / kUnit : 0;
+  const uint32_t prefix_segs = c.kv_heads * pl.prefix_groups, seg_per_req = c.kv_heads * pl.own_groups;
+  const unsigned long long own0 = (unsigned long long)prefix_segs * prefix_units;
+  const unsigned long long units = own0 + scan.before[kDecodeThreads] * seg_per_req;
+  unsigned long long u = first_unit(w, units, pl.warps);
+  const unsigned long long u_end = first_unit(w + 1, units, pl.warps);
+
+  // the segment of unit u
+  uint32_t r = 0, sub = 0;              // request (own tokens) and segment within it; or the prefix segment
+  unsigned long long seg0 = 0;          // its first unit
+  bool own = false;
+  if (u < u_end) {
+    if (u < own0) {
+      sub = (uint32_t)(u / prefix_units);
+      seg0 = (unsigned long long)sub * prefix_units;
+    } else {
+      own = true;
+      const unsigned long long v = u - own0;
+      uint32_t lo = 0, hi = kDecodeThreads;
+      while (hi - lo > 1) {
+        const uint32_t m = (lo + hi) >> 1;
+        if (scan.before[m] * seg_per_req <= v) lo = m; else hi = m;
+      }
+      const uint32_t run = (a.n_reqs + kDecodeThreads - 1) / kDecodeThreads;
+      unsigned long long at = scan.before[lo] * seg_per_req;
+      for (r = lo * run;; ++r) {
+        const uint32_t n = own_units(prefix, decode_len(c, a, prefix, r, bad));
+        if (v < at + (unsigned long long)n * seg_per_req) {
+          sub = (uint32_t)((v - at) / n);
+          seg0 = own0 + at + (unsigned long long)sub * n;
+          break;
+        }
+        at += (unsigned long long)n * seg_per_req;
+      }
+    }
+  }
+  const float log2e_scale = a.scale * 1.44269504088896340736f;
+
+  while (u < u_end) {
+    // ---- a piece: units [u, piece_end) of one segment ----
+    const uint32_t groups = own ? pl.own_groups : pl.prefix_groups;
+    const uint32_t hk = sub / groups, row0 = sub % groups * kRows;
+    const int32_t len = own ? decode_len(c, a, prefix, r, bad) : prefix;
+    const uint32_t n_units = own ? own_units(prefix, len) : prefix_units;
+    const unsigned long long piece_end = min(u_end, seg0 + n_units);
+    const uint32_t origin = own ? own_start(prefix) : 0;
+    const uint32_t t_first = origin + (uint32_t)(u - seg0) * kUnit;
+    const uint32_t t_last = min((uint32_t)len, origin + (uint32_t)(piece_end - seg0) * kUnit);
+    const int32_t t_from = own ? prefix : 0;
+    const int32_t* pages = own ? a.table + (uint64_t)r * a.max_blocks : a.prefix_pages;
+
+    // queries: B operands. Lane (g, cc) holds row g's values 16 cc + 4 k + j (and 64 + ...) for step k
+    uint32_t qb[NT][D / 16][2];
+    float mul[NT][2];     // scale of query columns 2 cc, 2 cc + 1
+    int32_t limit_at[NT][2];  // tokens they see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t row = row0 + 8 * nt + g;
+      const bool real = own ? row < group : row < a.n_reqs * group;
+      const uint32_t req = own ? r : row / group, head = hk * group + (own ? row : row % group);
+      uint2 v[D / 16];
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        v[k] = real ? *reinterpret_cast<const uint2*>(a.q + (uint64_t)req * a.q_stride + (uint64_t)head * D + (k / 4) * 64 + cc * 16 + (k % 4) * 4)
+                    : make_uint2(0, 0);
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t x = v[k].x & 0x7FFF7FFFu, y = v[k].y & 0x7FFF7FFFu;
+        top = max(max(top, max(x & 0xFFFFu, x >> 16)), max(y & 0xFFFFu, y >> 16));
+      }
+      top = max(top, __shfl_xor_sync(~0u, top, 1));
+      top = max(top, __shfl_xor_sync(~0u, top, 2));
+      // exponent of the row's largest, kept where its power of two and the inverse are normal
+      const int32_t e = max(-100, min(126, (int32_t)(top >> 7) - 127));
+      const float by = pow2((float)-e);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qb[nt][k][0] = fp16_pack(bf16_lo(v[k].x) * by, bf16_hi(v[k].x) * by);
+        qb[nt][k][1] = fp16_pack(bf16_lo(v[k].y) * by, bf16_hi(v[k].y) * by);
+      }
+      int32_t sees = 0;
+      if (real) sees = own ? len : min(prefix, decode_len(c, a, prefix, req, bad));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int32_t src = (2 * cc + i) * 4;
+        mul[nt][i] = log2e_scale * pow2((float)__shfl_sync(~0u, e, src));
+        limit_at[nt][i] = __shfl_sync(~0u, sees, src);
+      }
+    }
+
+    float o[NT][D / 16][4], l[NT][2], ms[NT][2], mt[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) l[nt][i] = 0.f, ms[nt][i] = mt[nt][i] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][k][i] = 0.f;
+    }
+
+    // 16 tokens a step: row of their first one in the cache, or ~0 where the page is none
+    auto row_of = [&](uint32_t t) -> uint64_t {
+      if (t >= t_last) return ~0ull;
+      const int32_t p = pages[t >> c.log2_pt];
+      if (p < 0 || (uint32_t)p >= c.n_pages) {
+        if (lane == 0) report(a.st, SHN_ERR_INVALID_ARG, r);
+        return ~0ull;
+      }
+      return kv_row(c, (uint32_t)p, hk, t & ((1u << c.log2_pt) - 1));
+    };
+    uint4 kr[2][kKLoads];  // tokens g, g + 8
+    uint32_t vr[4][D / 32];  // tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9: D/8 bytes at g D/8
+    float ks[2], vs[2];
+    auto load_k = [&](uint64_t row) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int h = 0; h < kKLoads; ++h)
+          kr[i][h] = row == ~0ull ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(c.k + (row + g + 8 * i) * D + h * 64 + cc * 16));
+        ks[i] = row == ~0ull ? 0.f : __ldg(c.k_scale + row + g + 8 * i);
+        vs[i] = row == ~0ull ? 0.f : __ldg(c.v_scale + row + g + 8 * i);
+      }
+    };
+    auto load_v = [&](uint64_t row) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int8_t* src = c.v + (row + 2 * cc + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8);
+        if (row == ~0ull) {
+#pragma unroll
+          for (int h = 0; h < D / 32; ++h) vr[i][h] = 0;
+        } else if constexpr (D == 128) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+          vr[i][0] = x.x, vr[i][1] = x.y, vr[i][D / 32 - 2] = x.z, vr[i][D / 32 - 1] = x.w;
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+          vr[i][0] = x.x, vr[i][1] = x.y;
+        }
+      }
+    };
+    uint64_t row_now = row_of(t_first), row_next = row_of(t_first + 16);
+    load_k(row_now);
+    load_v(row_now);
+#pragma unroll 1
+    for (uint32_t t = t_first; t < t_last; t += 16) {
+      const uint64_t row_after = row_of(t + 32);
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      // keys of tokens g, g + 8 -> scores
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t af[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 x = kr[i][k / 4];
+          const uint32_t wd = ((k & 3) == 0 ? x.x : (k & 3) == 1 ? x.y : (k & 3) == 2 ? x.z : x.w) ^ 0x80808080u;
+          af[i] = minus1152(__byte_perm(wd, 0x64646464u, 0x4140));
+          af[i + 2] = minus1152(__byte_perm(wd, 0x64646464u, 0x4342));
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], af, qb[nt][k][0], qb[nt][k][1]);
+      }
+      const float ks_now[2] = {ks[0], ks[1]};
+      float lv[2], sg[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        lv[i] = log2_approx(fabsf(vs[i]));
+        sg[i] = vs[i];
+      }
+      load_k(row_next);
+      // scores -> weights: s[2 i + e] is token g + 8 i, query column 2 cc + e
+      uint32_t pb[NT][2];
+      bool rise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int32_t tok = (int32_t)(t + g + 8 * i);
+            float x = s[nt][2 * i + e] * (ks_now[i] * mul[nt][e]);
+            x = tok >= t_from && tok < limit_at[nt][e] && tok < (int32_t)t_last ? x : -INFINITY;
+            s[nt][2 * i + e] = x;
+            rise |= x > ms[nt][e] + 8.f || x + lv[i] > mt[nt][e] + 8.f;
+          }
+      if (__any_sync(~0u, rise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[nt][e], s[nt][2 + e]);
+            // (a masked score is -inf whatever its token's value scale; -inf + inf would be NaN, which fmaxf passes over)
+            float y = fmaxf(s[nt][e] + lv[0], s[nt][2 + e] + lv[1]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
+              y = fmaxf(y, __shfl_xor_sync(~0u, y, d));
+            }
+            if (x > ms[nt][e] + 8.f) {
+              l[nt][e] *= exp2_approx(ms[nt][e] - x);
+              ms[nt][e] = x;
+            }
+            if (y > mt[nt][e] + 8.f) {
+              const float keep = exp2_approx(mt[nt][e] - y);
+              mt[nt][e] = y;
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) o[nt][k][e] *= keep, o[nt][k][2 + e] *= keep;
+            }
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float p[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = s[nt][2 * i + e];
+            const bool sees = x != -INFINITY;
+            l[nt][e] += sees ? exp2_approx(x - ms[nt][e]) : 0.f;
+            p[e] = sees && lv[i] != -INFINITY ? copysignf(exp2_approx(x + lv[i] - mt[nt][e]), sg[i]) : 0.f;
+          }
+          pb[nt][i] = transposed8x8(fp16_pack(p[0], p[1]));
+        }
+      // values -> sums: a lane's bytes are values g D/8 + 2k, + 1 of step k, for tokens 2 cc, 2 cc + 1 (and + 8, + 9)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t af[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t x = vr[2 * i][k / 2], y = vr[2 * i + 1][k / 2];
+          const uint32_t b = 2 * (k & 1);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t v = __byte_perm(x, y, (b + e) | (b + e) << 4 | (4 + b + e) << 8 | (4 + b + e) << 12);
+            af[2 * i + e] = minus1152(((v & 0x00FF00FFu) ^ 0x00800080u) | 0x64006400u);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][k], af, pb[nt][0], pb[nt][1]);
+      }
+      load_v(row_next);
+      row_next = row_after;
+    }
+
+    // ---- the piece's result ----
+    const uint32_t seg = own ? prefix_segs + r * seg_per_req + sub : sub;
+    const uint64_t piece = (uint64_t)(w + seg) * kRows;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], d);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = l[nt][e];
+        const uint32_t row = 8 * nt + 2 * cc + e;
+        if (own ? row0 + row >= group : row0 + row >= a.n_reqs * group) continue;  // nobody's row
+        const uint64_t q = piece + row;
+        float* dst = pl.out + q * D + g * (D / 8);
+#pragma unroll
+        for (int k = 0; k < D / 16; k += 2)
+          *reinterpret_cast<float4*>(dst + 2 * k) = make_float4(o[nt][k][e], o[nt][k][2 + e], o[nt][k + 1][e], o[nt][k + 1][2 + e]);
+        if (g == 0) pl.ml[q] = make_float4(mt[nt][e], ms[nt][e], x, 0.f);
+      }
+
+    // ---- on to the next segment ----
+    u = piece_end;
+    if (u < u_end) {
+      seg0 = u;
+      if (!own) {
+        if (++sub == prefix_segs) own = true, r = 0, sub = 0;
+      } else if (++sub == seg_per_req) {
+        sub = 0, ++r;
+      }
+      if (own)
+        while (own_units(prefix, decode_len(c, a, prefix, r, bad)) == 0) ++r;  // ends: there are units left
+    }
+  }
+}
+
+// Joins the pieces of a row: a warp per (request, head), lanes across its values.
+template <int D>
+__global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAttnArgs a, DecodePlan pl) {
+  __shared__ UnitScan scan;
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t group = a.q_heads / c.kv_heads;
+  bool bad;
+  const int32_t prefix = decode_prefix(c, a, bad);
+  scan_units(c, a, prefix, scan, false);
+  const uint32_t item = blockIdx.x * (kDecodeThreads / 32) + (threadIdx.x >> 5);
+  if (item >= a.n_reqs * a.q_heads) return;
+  const uint32_t r = item / a.q_heads, head = item % a.q_heads, hk = head / group, g = head % group;
+  const int32_t len = decode_len(c, a, prefix, r, bad);
+  const uint32_t prefix_units = pl.prefix_groups ? ((uint32_t)prefix + kUnit - 1) / kUnit : 0;
+  const uint32_t prefix_segs = c.kv_heads * pl.prefix_groups, seg_per_req = c.kv_heads * pl.own_groups;
+  const unsigned long long own0 = (unsigned long long)prefix_segs * prefix_units;
+  const unsigned long long units = own0 + scan.before[kDecodeThreads] * seg_per_req;
+
+  constexpr int E = D / 32;
+  float o[E], l = 0.f, m = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  auto add = [&](const float* src, float4 x) {  // x: mt, ms, l
+    if (x.y == -INFINITY && x.z == 0.f) return;  // the piece saw nothing
+    if (x.y > m) {
+      const float keep = exp2_approx(m - x.y);
+      l *= keep;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= keep;
+      m = x.y;
+    }
+    l = fmaf(x.z, exp2_approx(x.y - m), l);
+    const float by = x.x == -INFINITY ? 0.f : exp2_approx(x.x - m);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(src[lane * E + e], by, o[e]);
+  };
+  auto pieces = [&](uint32_t seg, unsigned long long u0, uint32_t n, uint32_t row) {
+    if (n == 0) return;
+    const uint32_t w1 = warp_of(u0 + n - 1, units, pl.warps);
+    for (uint32_t w = warp_of(u0, units, pl.warps); w <= w1; ++w) {
+      if (first_unit(w, units, pl.warps) == first_unit(w + 1, units, pl.warps)) continue;  // a warp without units
+      const uint64_t q = (uint64_t)(w + seg) * pl.rows + row;
+      add(pl.out + q * D, pl.ml[q]);
+    }
+  };
+  if (pl.prefix_groups) {
+    const uint32_t row = r * group + g, sub = hk * pl.prefix_groups + row / pl.rows;
+    pieces(sub, (unsigned long long)sub * prefix_units, prefix_units, row % pl.rows);
+  }
+  for (uint32_t i = 0; i < pl.splits; ++i) {
+    const uint64_t q = (uint64_t)i * a.n_reqs * a.q_heads + item;
+    add(pl.split_out + q * D, pl.split_ml[q]);
+  }
+  const uint32_t n = own_units(prefix, len);
+  const uint32_t sub = hk * pl.own_groups + g / pl.rows;
+  pieces(prefix_segs + r * seg_per_req + sub, own0 + units_before(c, a, prefix, scan, r) * seg_per_req + (unsigned long long)sub * n, n, g % pl.rows);
+  uint16_t* dst = a.out + (uint64_t)r * a.out_stride + (uint64_t)head * D + lane * E;
+  const float inv = len > 0 ? 1.f / l : 0.f;  // (a sum of 0 although tokens were seen: every score was -infinity, the result is NaN)
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = len > 0 ? bf16_pack(o[e] * inv, o[e + 1] * inv) : 0u;
+}
+
+template <int D>
+cudaError_t launch(const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s) {
+  const uint32_t blocks = pl.warps / (kDecodeThreads / 32);
+  if (pl.rows == 8) kv_decode_kernel<D, 1><<<blocks, kDecodeThreads, 0, s>>>(c, a, pl);
+  else kv_decode_kernel<D, 2><<<blocks, kDecodeThreads, 0, s>>>(c, a, pl);
+  const uint32_t items = a.n_reqs * a.q_heads;
+  kv_join_kernel<D><<<(items + kDecodeThreads / 32 - 1) / (kDecodeThreads / 32), kDecodeThreads, 0, s>>>(c, a, pl);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_decode(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s) {
+  return head_dim == 128 ? launch<128>(c, a, pl, s) : launch<64>(c, a, pl, s);
+}
+
+}  // namespace shn

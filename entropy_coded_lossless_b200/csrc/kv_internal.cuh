@@ -89,6 +89,5 @@ struct KvAttnArgs {
   DeviceStatus* st;
 };
 cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, cudaStream_t s);
-cudaError_t launch_kv_attn(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, cudaStream_t s);
 
 }  // namespace shn

@@ -638,7 +638,7 @@ def test_two_streams_at_once_and_same_bits():
 
 def test_binding_refuses():
     cache = filled_cache(4, 2, 16, 128)
-    q, w = bf16(2, 4, 128), work(1 << 20)
+    q, w = bf16(2, 4, 128), work(kv.attn_shared_workspace_bytes(cache, 2, 4))
     t, one = ints([[0, 1], [2, 3]]), ints([16, 16])
     out = torch.empty_like(q)
     ok = dict(q=q, cache=cache, prefix_pages=None, prefix_len=ints([0]), block_table=t, kv_len=one, scale=0.1, out=out, work=w)
