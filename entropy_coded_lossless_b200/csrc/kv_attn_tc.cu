@@ -25,6 +25,7 @@
 // TMEM (512 columns): S0, S1 (128 each; P in their first 64), O0, O1 (D each).
 #include <type_traits>
 
+#include "kv_decode.cuh"
 #include "kv_tc.cuh"
 
 namespace shn {
@@ -46,7 +47,7 @@ constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows of 64 bf16
 template <int D>
 struct Layout {
   static constexpr uint32_t kOperand = 128 * D * 2;  // one 128 x D bf16 operand
-  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, info = scale + 4 * 512, row_sum = info + 64, bars = row_sum + 4 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
+  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, info = scale + 4 * 512, row_sum = info + 64, bars = row_sum + 8 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
 };
 // barriers
 enum : uint32_t { kQFull = 0, kKFull = 8, kKEmpty = 24, kVFull = 40, kVEmpty = 56, kScaleFull = 72, kSFull = 104, kPFull = 120, kOFull = 152, kDrain = 184 };
@@ -55,6 +56,7 @@ struct Work {
   uint32_t req, row0, rows;  // request, first row of the block within it, rows of the request
   int32_t q0;                // first query of the request
   int32_t len, nq;           // its tokens and queries
+  uint32_t t0;               // first token (in pages) of the block's part of the sequence
 };
 
 // Which request's rows a block takes: tiles of 256 rows, request after request, the last tile first (a
@@ -117,11 +119,26 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
     len = len < 0 ? 0 : (int32_t)holds;
   }
   w.len = len;
+  w.t0 = 0;
   return true;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAttnArgs a) {
+// The same for a part of a shared prefix: blockIdx = (key head, tile of 256 rows, split), rows = (request, head of the group),
+// tokens = the split's tiles of the prefix.
+__device__ __forceinline__ void find_part(const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, uint32_t group, Work& w) {
+  bool bad;
+  const int32_t prefix = decode_prefix(c, a, bad);
+  const uint32_t tiles = ((uint32_t)prefix + kTile - 1) / kTile;
+  const uint32_t rest = blockIdx.x / c.kv_heads, split = rest % pl.splits;
+  w.req = 0, w.q0 = 0, w.nq = (int32_t)a.n_reqs;
+  w.row0 = rest / pl.splits * kRows;
+  w.rows = a.n_reqs * group;
+  w.t0 = (uint32_t)((uint64_t)split * tiles / pl.splits) * kTile;
+  w.len = min(prefix, (int32_t)((uint64_t)(split + 1) * tiles / pl.splits * kTile)) - (int32_t)w.t0;
+}
+
+template <int D, bool kPart>
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAttnArgs a, DecodePlan pl) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using L = Layout<D>;
   const uint32_t base = smem_addr(smem), bars = base + L::bars, stop = base + L::misc;
@@ -131,11 +148,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   // after a wait that gave up the call has failed: the other blocks do not start on it
   if (__syncthreads_or(*reinterpret_cast<volatile uint32_t*>(&a.st->status) == SHN_ERR_TIMEOUT)) return;
   Work w;
-  if (!find_work(c, a, group, blockIdx.x / c.kv_heads, reinterpret_cast<uint32_t*>(smem + L::scan), w)) return;
+  if constexpr (kPart) find_part(c, a, pl, group, w);
+  else if (!find_work(c, a, group, blockIdx.x / c.kv_heads, reinterpret_cast<uint32_t*>(smem + L::scan), w)) return;
   const uint32_t rows_here = min(kRows, w.rows - w.row0);
   // tokens the block's last row sees; every row of the block sees at most as many
   const int32_t shift = w.len - w.nq + 1;  // query i sees shift + i tokens
-  const int32_t most = max(0, min(w.len, shift + (int32_t)((w.row0 + rows_here - 1) / group)));
+  const int32_t most = kPart ? max(0, w.len) : max(0, min(w.len, shift + (int32_t)((w.row0 + rows_here - 1) / group)));
   const uint32_t tiles = ((uint32_t)most + kTile - 1) / kTile;
 
   if (tid == 0) {
@@ -190,7 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     const uint32_t at = tmem + (lanes << 16);
     const uint32_t s_at = at + half * 128, o_at = at + 256 + half * D;
     auto seen_by = [&](uint32_t row) -> int32_t {
-      return row < rows_here ? max(0, min(w.len, shift + (int32_t)((w.row0 + row) / group))) : 0;
+      if (row >= rows_here) return 0;
+      const uint32_t q = (w.row0 + row) / group;
+      if constexpr (kPart) {
+        bool bad;
+        return max(0, min(w.len, decode_len(c, a, (int32_t)w.t0 + w.len, q, bad) - (int32_t)w.t0));
+      }
+      return max(0, min(w.len, shift + (int32_t)q));
     };
     int32_t seen[2];
     float m[2], l[2];
@@ -309,12 +333,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     // the rows' sums, through shared memory to the threads that write the rows: warps of the same 32 rows take half of the
     // columns each (the barrier comes first: no warp may miss it)
     const uint32_t rows32 = (warp & 3) * 32;
-    const uint32_t sums = base + L::row_sum + 4 * (half * 128);
+    const uint32_t sums = base + L::row_sum + 4 * (half * 128), refs = sums + 4 * kRows;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
       if ((lane & 3) == 0) sts32(sums + 4 * (lanes + quad + 8 * r), __float_as_uint(l[r]));
+      if (kPart && (lane & 3) == 0) sts32(refs + 4 * (lanes + quad + 8 * r), __float_as_uint(m[r]));
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(kSoftThreads / 2) : "memory");
     if (ok && tiles) ok = __all_sync(~0u, bar_wait(bars + kOFull + 16 * half + 8, (tiles - 1) & 1, stop));
@@ -323,9 +348,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       const uint32_t row = half * 128 + rows32 + lane, g = w.row0 + row;
       const bool any = seen_by(row) > 0;
       // no token seen: zeros. (A sum that is not positive although tokens were seen is a NaN's or an infinity's.)
-      const float inv = any ? pow2(held) / __uint_as_float(lds32(sums + 4 * (rows32 + lane))) : 0.f;
+      const float sum = __uint_as_float(lds32(sums + 4 * (rows32 + lane)));
+      const float inv = any ? pow2(held) / sum : 0.f;
       const uint32_t first = (warp >> 2 & 1) * (D / 2);
-      uint16_t* dst = a.out + (uint64_t)(w.q0 + g / group) * a.out_stride + (uint64_t)(hk * group + g % group) * D + first;
+      const uint64_t query = (uint64_t)(w.q0 + g / group), head = hk * group + g % group;
+      uint16_t* dst = a.out + query * a.out_stride + head * D + first;
+      float* part = nullptr;
+      if constexpr (kPart) {
+        const uint64_t at = ((uint64_t)(blockIdx.x / c.kv_heads % pl.splits) * a.n_reqs + query) * a.q_heads + head;
+        part = pl.split_out + at * D + first;
+        if (row < rows_here && first == 0) {
+          const float ref = __uint_as_float(lds32(refs + 4 * (rows32 + lane)));
+          pl.split_ml[at] = make_float4(tiles ? ref + held : -INFINITY, ref, tiles ? sum : 0.f, 0.f);
+        }
+      }
 #pragma unroll
       for (int q = 0; q < D / 64; ++q) {
         uint32_t o[32];
@@ -333,7 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
           ld32(tmem + (rows32 << 16) + 256 + half * D + first + 32 * q, o);
           wait_ld();
         }
-        if (row < rows_here) {
+        if constexpr (kPart) {
+          if (row < rows_here && tiles) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(part + 32 * q + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        } else if (row < rows_here) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t y[4];
@@ -354,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     // A warp's load: 4 lanes on 64 values of a row, 8 rows. For D = 128 even warps take the rows' first 64 values.
     const uint32_t part = D == 128 ? (cw & 1) : 0, first = (cw >> (D == 128 ? 1 : 0)) * kLoads * 8;
     const uint32_t chunk = lane & 3, sub = lane >> 2;
-    const int32_t* table = a.table + (uint64_t)w.req * a.max_blocks;
+    const int32_t* table = kPart ? a.prefix_pages + (w.t0 >> c.log2_pt) : a.table + (uint64_t)w.req * a.max_blocks;
+    const uint32_t skip = kPart ? w.t0 & ((1u << c.log2_pt) - 1) : 0;  // (pages longer than a tile: the part begins inside one)
     const uint32_t pt_mask = (1u << c.log2_pt) - 1;
 
     // page of the tile's 16-token group `lane` (lanes 0-7), -1 where there are no tokens
@@ -362,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       const int32_t tok = (int32_t)(j * kTile + (lane & 7) * 16);
       int32_t p = -1;
       if (j < tiles && tok < most) {
-        p = table[tok >> c.log2_pt];
+        p = table[(tok + skip) >> c.log2_pt];
         if (p < 0 || (uint32_t)p >= c.n_pages) {
           if (lane < 8) report(a.st, SHN_ERR_INVALID_ARG, w.req);
           p = -1;
@@ -379,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       for (int i = 0; i < kGroups; ++i) {
         const uint32_t group16 = (first >> 4) + i;
         const int32_t p = __shfl_sync(~0u, pages, group16);
-        off[i] = p < 0 ? -1 : (int64_t)(kv_row(c, (uint32_t)p, hk, (j * kTile + group16 * 16) & pt_mask) * D + lane_at);
+        off[i] = p < 0 ? -1 : (int64_t)(kv_row(c, (uint32_t)p, hk, (j * kTile + group16 * 16 + skip) & pt_mask) * D + lane_at);
       }
     };
     // Converts the thread's pieces of an operand, and as each one's registers are read asks for the same piece of the
@@ -418,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         const int32_t p = __shfl_sync(~0u, pages, 2 * i + (lane >> 4));
         const uint32_t tok = j * kTile + 32 * i + lane;
         const bool is = p >= 0 && (int32_t)tok < most;
-        const uint64_t at = kv_row(c, (uint32_t)p, hk, tok & pt_mask);
+        const uint64_t at = kv_row(c, (uint32_t)p, hk, (tok + skip) & pt_mask);
         v_scale[i] = is ? c.v_scale[at] : 0.f;
         if (cw == (uint32_t)i) k_scale = is ? c.k_scale[at] * factor : 0.f;
       }
@@ -538,24 +581,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   if (tid == 0 && lds32(stop) != 0) report(a.st, SHN_ERR_TIMEOUT, w.req);
 }
 
-template <int D>
-cudaError_t launch(const KvPages& c, const KvAttnArgs& a, cudaStream_t s) {
-  // more shared memory than the default 48 KB: an attribute of the kernel on each device, so it is set for the one that
-  // is current on every call
-  cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::total);
+// More shared memory than the default 48 KB: an attribute of the kernel on each device, so it is set for the one that is
+// current on every call.
+template <int D, bool kPart>
+cudaError_t launch(uint64_t blocks, const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s) {
+  if (blocks >= (1ull << 31)) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D, kPart>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::total);
   if (e != cudaSuccess) return e;
-  const uint64_t group = a.q_heads / c.kv_heads;
-  // at most so many tiles, however the queries are spread over the requests
-  const uint64_t tiles = (uint64_t)a.n_tokens * group / kRows + (a.n_reqs < a.n_tokens ? a.n_reqs : a.n_tokens);
-  if (tiles * c.kv_heads >= (1ull << 31)) return cudaErrorInvalidConfiguration;
-  kv_prompt_kernel<D><<<(uint32_t)(tiles * c.kv_heads), kThreads, Layout<D>::total, s>>>(c, a);
+  kv_prompt_kernel<D, kPart><<<(uint32_t)blocks, kThreads, Layout<D>::total, s>>>(c, a, pl);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, cudaStream_t s) {
-  return head_dim == 128 ? launch<128>(c, a, s) : launch<64>(c, a, s);
+  const uint64_t group = a.q_heads / c.kv_heads;
+  // at most so many tiles, however the queries are spread over the requests
+  const uint64_t blocks = ((uint64_t)a.n_tokens * group / kRows + (a.n_reqs < a.n_tokens ? a.n_reqs : a.n_tokens)) * c.kv_heads;
+  const DecodePlan none = {};
+  return head_dim == 128 ? launch<128, false>(blocks, c, a, none, s) : launch<64, false>(blocks, c, a, none, s);
+}
+
+cudaError_t launch_kv_prefix(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s) {
+  const uint64_t group = a.q_heads / c.kv_heads;
+  const uint64_t blocks = (a.n_reqs * group + kRows - 1) / kRows * c.kv_heads * pl.splits;
+  return head_dim == 128 ? launch<128, true>(blocks, c, a, pl, s) : launch<64, true>(blocks, c, a, pl, s);
 }
 
 }  // namespace shn

@@ -63,10 +63,14 @@ int check_attn(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32
   return SHN_OK;
 }
 
+// From this many query rows per key head on, the prefix goes to the tensor core kernel.
+constexpr uint64_t kPrefixRows = 32;
+constexpr uint64_t kSplitBlocks = 148;
+
 // How shn_kv_attn_shared is cut up, and its workspace: [status 256][pieces' sums][pieces' (mt, ms, l)].
 struct SharedLayout {
   DecodePlan pl;
-  size_t out_off, ml_off, total;
+  size_t out_off, ml_off, split_off, split_ml_off, total;
 };
 
 SharedLayout shared_layout(const shn_kv_cache* c, uint32_t n_reqs, uint32_t q_heads) {
@@ -74,12 +78,22 @@ SharedLayout shared_layout(const shn_kv_cache* c, uint32_t n_reqs, uint32_t q_he
   const uint32_t group = q_heads / c->kv_heads;
   x.pl.rows = group <= 8 ? 8 : 16;  // the rows of one mma are 8; 16 share what is done for a token's bytes
   x.pl.own_groups = (group + x.pl.rows - 1) / x.pl.rows;
-  x.pl.prefix_groups = (uint32_t)(((uint64_t)n_reqs * group + x.pl.rows - 1) / x.pl.rows);
+  const uint64_t rows = (uint64_t)n_reqs * group;
+  if (rows >= kPrefixRows) {
+    // as many parts as give every SM one block of the tensor core kernel
+    const uint64_t blocks = (rows + 255) / 256 * c->kv_heads;
+    x.pl.splits = blocks >= kSplitBlocks ? 1 : (uint32_t)(kSplitBlocks / blocks);
+  } else {
+    x.pl.prefix_groups = (uint32_t)((rows + x.pl.rows - 1) / x.pl.rows);
+  }
   const uint64_t segs = (uint64_t)c->kv_heads * (x.pl.prefix_groups + (uint64_t)n_reqs * x.pl.own_groups);
   const uint64_t pieces = (kDecodeMaxWarps + segs) * x.pl.rows;
+  const uint64_t parts = (uint64_t)x.pl.splits * n_reqs * q_heads;
   x.out_off = 256;
   x.ml_off = x.out_off + round_up(pieces * c->head_dim * sizeof(float), 256);
-  x.total = x.ml_off + round_up(pieces * sizeof(float4), 256);
+  x.split_off = x.ml_off + round_up(pieces * sizeof(float4), 256);
+  x.split_ml_off = x.split_off + round_up(parts * c->head_dim * sizeof(float), 256);
+  x.total = x.split_ml_off + round_up(parts * sizeof(float4), 256);
   return x;
 }
 
@@ -227,6 +241,11 @@ int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, 
   uint8_t* wb = static_cast<uint8_t*>(d_work);
   x.pl.out = reinterpret_cast<float*>(wb + x.out_off);
   x.pl.ml = reinterpret_cast<float4*>(wb + x.ml_off);
+  x.pl.split_out = reinterpret_cast<float*>(wb + x.split_off);
+  x.pl.split_ml = reinterpret_cast<float4*>(wb + x.split_ml_off);
+  // no more parts than the prefix can have tiles of 128 tokens
+  const uint64_t tiles = ((uint64_t)n_prefix_pages * cache->page_tokens + 127) / 128;
+  if (x.pl.splits > tiles) x.pl.splits = (uint32_t)tiles;
   // warps: two blocks on each SM (one for 16 rows, which takes more registers), but no more than there can be units
   const uint64_t units = (uint64_t)cache->kv_heads * x.pl.prefix_groups * (((uint64_t)n_prefix_pages * cache->page_tokens + kUnit - 1) / kUnit) +
                          (uint64_t)n_reqs * cache->kv_heads * x.pl.own_groups * (((uint64_t)max_blocks * cache->page_tokens + kUnit - 1) / kUnit + 1);
@@ -235,6 +254,7 @@ int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, 
   if (blocks > (units + per_block - 1) / per_block) blocks = (units + per_block - 1) / per_block;
   if (blocks > kDecodeMaxWarps / per_block) blocks = kDecodeMaxWarps / per_block;
   x.pl.warps = (uint32_t)(blocks * per_block);
+  if (x.pl.splits && launch_kv_prefix(pages_of(cache), cache->head_dim, a, x.pl, s) != cudaSuccess) return SHN_ERR_CUDA;
   return launch_kv_decode(pages_of(cache), cache->head_dim, a, x.pl, s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
 }
 

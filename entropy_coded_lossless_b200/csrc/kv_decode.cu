@@ -360,44 +360,74 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
   const unsigned long long own0 = (unsigned long long)prefix_segs * prefix_units;
   const unsigned long long units = own0 + scan.before[kDecodeThreads] * seg_per_req;
 
+  // the row's results, in this order: pieces of the prefix's segment, parts of the prefix, pieces of its own tokens' segment
+  const uint32_t prow = r * group + g, psub = pl.prefix_groups ? hk * pl.prefix_groups + prow / pl.rows : 0;
+  const uint32_t osub = hk * pl.own_groups + g / pl.rows;
+  const uint32_t n = own_units(prefix, len);
+  uint32_t pw = 0, pn = 0, ow = 0, on = 0;  // first warp and number of pieces
+  if (prefix_units) {
+    const unsigned long long u0 = (unsigned long long)psub * prefix_units;
+    pw = warp_of(u0, units, pl.warps);
+    pn = warp_of(u0 + prefix_units - 1, units, pl.warps) - pw + 1;
+  }
+  if (n) {
+    const unsigned long long u0 = own0 + units_before(c, a, prefix, scan, r) * seg_per_req + (unsigned long long)osub * n;
+    ow = warp_of(u0, units, pl.warps);
+    on = warp_of(u0 + n - 1, units, pl.warps) - ow + 1;
+  }
+  const uint32_t all = pn + pl.splits + on;
   constexpr int E = D / 32;
   float o[E], l = 0.f, m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  auto add = [&](const float* src, float4 x) {  // x: mt, ms, l
-    if (x.y == -INFINITY && x.z == 0.f) return;  // the piece saw nothing
-    if (x.y > m) {
-      const float keep = exp2_approx(m - x.y);
+  // 32 results at a time: a lane finds one's place and reads its (mt, ms, l); then all lanes add them up one after another
+  for (uint32_t k0 = 0; k0 < all; k0 += 32) {
+    const uint32_t k = k0 + lane;
+    const float* src = nullptr;
+    float4 x = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+    if (k < all) {
+      const bool part = k >= pn && k < pn + pl.splits;
+      if (part) {
+        const uint64_t q = (uint64_t)(k - pn) * a.n_reqs * a.q_heads + item;
+        src = pl.split_out + q * D;
+        x = pl.split_ml[q];
+      } else {
+        const bool mine = k >= pn;
+        const uint32_t w = mine ? ow + (k - pn - pl.splits) : pw + k;
+        if (first_unit(w, units, pl.warps) != first_unit(w + 1, units, pl.warps)) {  // (there are warps without units)
+          const uint64_t q = (uint64_t)(w + (mine ? prefix_segs + r * seg_per_req + osub : psub)) * pl.rows + (mine ? g : prow) % pl.rows;
+          src = pl.out + q * D;
+          x = pl.ml[q];
+        }
+      }
+      if (x.y == -INFINITY && x.z == 0.f) src = nullptr;  // it saw nothing
+    }
+    float top = src ? x.y : -INFINITY;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    if (top > m) {
+      const float keep = exp2_approx(m - top);
       l *= keep;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] *= keep;
-      m = x.y;
+      m = top;
     }
-    l = fmaf(x.z, exp2_approx(x.y - m), l);
-    const float by = x.x == -INFINITY ? 0.f : exp2_approx(x.x - m);
+    float share = src ? x.z * exp2_approx(x.y - m) : 0.f;
+    const float by = src && x.x != -INFINITY ? exp2_approx(x.x - m) : 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(src[lane * E + e], by, o[e]);
-  };
-  auto pieces = [&](uint32_t seg, unsigned long long u0, uint32_t n, uint32_t row) {
-    if (n == 0) return;
-    const uint32_t w1 = warp_of(u0 + n - 1, units, pl.warps);
-    for (uint32_t w = warp_of(u0, units, pl.warps); w <= w1; ++w) {
-      if (first_unit(w, units, pl.warps) == first_unit(w + 1, units, pl.warps)) continue;  // a warp without units
-      const uint64_t q = (uint64_t)(w + seg) * pl.rows + row;
-      add(pl.out + q * D, pl.ml[q]);
+    for (int d = 16; d; d >>= 1) share += __shfl_xor_sync(~0u, share, d);
+    l += share;
+    const uint32_t have = __ballot_sync(~0u, src != nullptr);
+    const uint32_t last = min(32u, all - k0);
+#pragma unroll 4
+    for (uint32_t i = 0; i < last; ++i) {
+      const float* from = reinterpret_cast<const float*>(__shfl_sync(~0u, (unsigned long long)src, i));
+      const float f = __shfl_sync(~0u, by, i);
+      if (!(have >> i & 1)) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(from[lane * E + e], f, o[e]);
     }
-  };
-  if (pl.prefix_groups) {
-    const uint32_t row = r * group + g, sub = hk * pl.prefix_groups + row / pl.rows;
-    pieces(sub, (unsigned long long)sub * prefix_units, prefix_units, row % pl.rows);
   }
-  for (uint32_t i = 0; i < pl.splits; ++i) {
-    const uint64_t q = (uint64_t)i * a.n_reqs * a.q_heads + item;
-    add(pl.split_out + q * D, pl.split_ml[q]);
-  }
-  const uint32_t n = own_units(prefix, len);
-  const uint32_t sub = hk * pl.own_groups + g / pl.rows;
-  pieces(prefix_segs + r * seg_per_req + sub, own0 + units_before(c, a, prefix, scan, r) * seg_per_req + (unsigned long long)sub * n, n, g % pl.rows);
   uint16_t* dst = a.out + (uint64_t)r * a.out_stride + (uint64_t)head * D + lane * E;
   const float inv = len > 0 ? 1.f / l : 0.f;  // (a sum of 0 although tokens were seen: every score was -infinity, the result is NaN)
 #pragma unroll

@@ -95,6 +95,8 @@ __device__ __forceinline__ uint32_t warp_of(unsigned long long u, unsigned long 
   return (uint32_t)(((u + 1) * warps - 1) / units);
 }
 
+// The prefix in pl.splits parts (kv_attn_tc.cu): parts' sums into pl.split_out, pl.split_ml.
+cudaError_t launch_kv_prefix(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s);
 cudaError_t launch_kv_decode(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s);
 
 }  // namespace shn
