@@ -10,9 +10,12 @@
 // INT8 enters as fp16, exactly (1024 + u with u = x + 128 is a byte put into fp16's last bits; minus 1152 it is x). A query row
 // is scaled by a power of two into fp16, exactly but for parts 2^-25 of its largest. Scales meet the float32 scores: with
 // x = s k_scale softmax_scale log2(e),
-//   l += 2^(x - ms),   P = sign(v_scale) 2^(x + log2|v_scale| - mt)  rounded to fp16 (2^-11)
-// two exponentials a score, so that P lies in fp16's range whatever the value scales are. ms and mt are running references
-// raised only when a score passes them by 8 (log2), which spares a reduction across lanes almost always.
+//   p = 2^(x - m),   l += p,   P = fp16(p v_scale 2^-E)   (2^-11, the one rounding before the sums)
+// The reference m is raised only when a score passes it by 8, and E, the exponent the sums are held in, when a value scale
+// is more than 2^7 above it (2^15 together, within fp16): almost every step does without a reduction across lanes. A
+// weight below 2^-25 of that range is lost, so the sums are exact to 2^-24 of the sequence's largest value.
+#include <type_traits>
+
 #include "kv_decode.cuh"
 #include "kv_tc.cuh"
 
@@ -29,11 +32,6 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
 __device__ __forceinline__ uint32_t transposed8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-__device__ __forceinline__ float log2_approx(float x) {
-  float r;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 // two fp16 of 1024 + byte -> the signed bytes (their sign bits inverted before)
@@ -93,6 +91,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
     }
   }
   const float log2e_scale = a.scale * 1.44269504088896340736f;
+  const uint32_t lane_k = g * D + cc * 16, lane_v = 2 * cc * D + g * (D / 8);
 
   while (u < u_end) {
     // ---- a piece: units [u, piece_end) of one segment ----
@@ -106,6 +105,67 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
     const uint32_t t_last = min((uint32_t)len, origin + (uint32_t)(piece_end - seg0) * kUnit);
     const int32_t t_from = own ? prefix : 0;
     const int32_t* pages = own ? a.table + (uint64_t)r * a.max_blocks : a.prefix_pages;
+
+    // 16 tokens a step: where their keys and values lie, and whether there is a page (warp-uniform)
+    auto row_of = [&](uint32_t t, uint64_t& row) -> bool {
+      if (t >= t_last) return false;
+      const int32_t p = __ldg(pages + (t >> c.log2_pt));
+      if (p < 0 || (uint32_t)p >= c.n_pages) {
+        if (lane == 0) report(a.st, SHN_ERR_INVALID_ARG, r);
+        return false;
+      }
+      row = kv_row(c, (uint32_t)p, hk, t & ((1u << c.log2_pt) - 1));
+      return true;
+    };
+    uint4 kr[2][kKLoads];    // tokens g, g + 8
+    uint32_t vr[4][D / 32];  // tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9: D/8 bytes at g D/8
+    float ks[2], vs[2];
+    auto load_k = [&](bool is, uint64_t row) {
+      if (is) {
+        const int8_t* src = c.k + row * D + lane_k;
+        const float *k_scale = c.k_scale + row + g, *v_scale = c.v_scale + row + g;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int h = 0; h < kKLoads; ++h) kr[i][h] = __ldg(reinterpret_cast<const uint4*>(src + 8 * i * D + h * 64));
+          ks[i] = __ldg(k_scale + 8 * i);
+          vs[i] = __ldg(v_scale + 8 * i);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int h = 0; h < kKLoads; ++h) kr[i][h] = make_uint4(0, 0, 0, 0);
+          ks[i] = vs[i] = 0.f;
+        }
+      }
+    };
+    auto load_v = [&](bool is, uint64_t row) {
+      if (is) {
+        const int8_t* src = c.v + row * D + lane_v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int8_t* at = src + ((i & 1) + 8 * (i >> 1)) * D;
+          if constexpr (D == 128) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+            vr[i][0] = x.x, vr[i][1] = x.y, vr[i][D / 32 - 2] = x.z, vr[i][D / 32 - 1] = x.w;
+          } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
+            vr[i][0] = x.x, vr[i][1] = x.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int h = 0; h < D / 32; ++h) vr[i][h] = 0;
+      }
+    };
+    uint64_t row_now = 0, row_next = 0;
+    const bool is_now = row_of(t_first, row_now);
+    bool is_next = row_of(t_first + 16, row_next);
+    load_k(is_now, row_now);
+    load_v(is_now, row_now);
 
     // queries: B operands. Lane (g, cc) holds row g's values 16 cc + 4 k + j (and 64 + ...) for step k
     uint32_t qb[NT][D / 16][2];
@@ -137,7 +197,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
         qb[nt][k][0] = fp16_pack(bf16_lo(v[k].x) * by, bf16_hi(v[k].x) * by);
         qb[nt][k][1] = fp16_pack(bf16_lo(v[k].y) * by, bf16_hi(v[k].y) * by);
       }
-      int32_t sees = 0;
+      int32_t sees = 0x7FFFFFFF;  // (nobody's rows hold no step back)
       if (real) sees = own ? len : min(prefix, decode_len(c, a, prefix, req, bad));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -147,62 +207,30 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
       }
     }
 
-    float o[NT][D / 16][4], l[NT][2], ms[NT][2], mt[NT][2];
+    // steps from full_from on and below full_to need no mask
+    int32_t least = limit_at[0][0];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) least = min(least, limit_at[nt][i]);
+    const int32_t full_to = min((int32_t)t_last, __reduce_min_sync(~0u, least));
+
+    float o[NT][D / 16][4], l[NT][2], m[NT][2], above[NT][2];  // above: m + 8
+    float held = -200.f, ceiling = 0.f, unit = 0.f;            // E, 2^(E + 7), 2^-E
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) l[nt][i] = 0.f, ms[nt][i] = mt[nt][i] = -INFINITY;
+      for (int i = 0; i < 2; ++i) l[nt][i] = m[nt][i] = 0.f, above[nt][i] = -INFINITY;  // (a reference of 0 until there is one)
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[nt][k][i] = 0.f;
     }
 
-    // 16 tokens a step: row of their first one in the cache, or ~0 where the page is none
-    auto row_of = [&](uint32_t t) -> uint64_t {
-      if (t >= t_last) return ~0ull;
-      const int32_t p = pages[t >> c.log2_pt];
-      if (p < 0 || (uint32_t)p >= c.n_pages) {
-        if (lane == 0) report(a.st, SHN_ERR_INVALID_ARG, r);
-        return ~0ull;
-      }
-      return kv_row(c, (uint32_t)p, hk, t & ((1u << c.log2_pt) - 1));
-    };
-    uint4 kr[2][kKLoads];  // tokens g, g + 8
-    uint32_t vr[4][D / 32];  // tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9: D/8 bytes at g D/8
-    float ks[2], vs[2];
-    auto load_k = [&](uint64_t row) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int h = 0; h < kKLoads; ++h)
-          kr[i][h] = row == ~0ull ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(c.k + (row + g + 8 * i) * D + h * 64 + cc * 16));
-        ks[i] = row == ~0ull ? 0.f : __ldg(c.k_scale + row + g + 8 * i);
-        vs[i] = row == ~0ull ? 0.f : __ldg(c.v_scale + row + g + 8 * i);
-      }
-    };
-    auto load_v = [&](uint64_t row) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int8_t* src = c.v + (row + 2 * cc + (i & 1) + 8 * (i >> 1)) * D + g * (D / 8);
-        if (row == ~0ull) {
-#pragma unroll
-          for (int h = 0; h < D / 32; ++h) vr[i][h] = 0;
-        } else if constexpr (D == 128) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
-          vr[i][0] = x.x, vr[i][1] = x.y, vr[i][D / 32 - 2] = x.z, vr[i][D / 32 - 1] = x.w;
-        } else {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-          vr[i][0] = x.x, vr[i][1] = x.y;
-        }
-      }
-    };
-    uint64_t row_now = row_of(t_first), row_next = row_of(t_first + 16);
-    load_k(row_now);
-    load_v(row_now);
 #pragma unroll 1
     for (uint32_t t = t_first; t < t_last; t += 16) {
-      const uint64_t row_after = row_of(t + 32);
+      uint64_t row_after = 0;
+      const bool is_after = row_of(t + 32, row_after);
       float s[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
@@ -220,68 +248,88 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], af, qb[nt][k][0], qb[nt][k][1]);
       }
-      const float ks_now[2] = {ks[0], ks[1]};
-      float lv[2], sg[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        lv[i] = log2_approx(fabsf(vs[i]));
-        sg[i] = vs[i];
-      }
-      load_k(row_next);
-      // scores -> weights: s[2 i + e] is token g + 8 i, query column 2 cc + e
-      uint32_t pb[NT][2];
-      bool rise = false;
+      float vs_now[2] = {vs[0], vs[1]};
+      // scores -> x: s[2 i + e] is token g + 8 i, query column 2 cc + e
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i) s[nt][i] *= ks[i >> 1] * mul[nt][i & 1];
+      load_k(is_next, row_next);
+      const bool edge = (int32_t)t < t_from || (int32_t)t + 16 > full_to;
+      if (edge) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int32_t tok = (int32_t)(t + g + 8 * i);
-            float x = s[nt][2 * i + e] * (ks_now[i] * mul[nt][e]);
-            x = tok >= t_from && tok < limit_at[nt][e] && tok < (int32_t)t_last ? x : -INFINITY;
-            s[nt][2 * i + e] = x;
-            rise |= x > ms[nt][e] + 8.f || x + lv[i] > mt[nt][e] + 8.f;
-          }
+        for (int i = 0; i < 2; ++i) {
+          const int32_t tok = (int32_t)(t + g + 8 * i);
+          const bool in = tok >= t_from && tok < (int32_t)t_last;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!in || tok >= limit_at[nt][e]) s[nt][2 * i + e] = -INFINITY;
+          if (!in) vs_now[i] = 0.f;  // what stands there is nobody's
+        }
+      }
+      bool rise = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) rise |= fabsf(vs_now[i]) > ceiling && fabsf(vs_now[i]) < INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) rise |= fmaxf(s[nt][e], s[nt][2 + e]) > above[nt][e];
       if (__any_sync(~0u, rise)) {
+        uint32_t big = 0;  // the largest finite value scale of the step
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (fabsf(vs_now[i]) < INFINITY) big = max(big, __float_as_uint(fabsf(vs_now[i])));
+        big = __reduce_max_sync(~0u, big);
+        float lower = 1.f;
+        if (__uint_as_float(big) > ceiling) {
+          const float to = (float)max(-126, min(119, (int32_t)(big >> 23) - 127));
+          lower = held < -150.f ? 0.f : pow2(fmaxf(held - to, -126.f));
+          held = to;
+          ceiling = pow2(held + 7.f);
+          unit = pow2(-held);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float x = fmaxf(s[nt][e], s[nt][2 + e]);
-            // (a masked score is -inf whatever its token's value scale; -inf + inf would be NaN, which fmaxf passes over)
-            float y = fmaxf(s[nt][e] + lv[0], s[nt][2 + e] + lv[1]);
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
-              y = fmaxf(y, __shfl_xor_sync(~0u, y, d));
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
+            float keep = 1.f;
+            if (x > above[nt][e]) {
+              keep = above[nt][e] == -INFINITY ? 0.f : exp2_approx(m[nt][e] - x);
+              m[nt][e] = x;
+              above[nt][e] = x + 8.f;
             }
-            if (x > ms[nt][e] + 8.f) {
-              l[nt][e] *= exp2_approx(ms[nt][e] - x);
-              ms[nt][e] = x;
-            }
-            if (y > mt[nt][e] + 8.f) {
-              const float keep = exp2_approx(mt[nt][e] - y);
-              mt[nt][e] = y;
+            l[nt][e] *= keep;
+            keep *= lower;
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) o[nt][k][e] *= keep, o[nt][k][2 + e] *= keep;
-            }
+            for (int k = 0; k < D / 16; ++k) o[nt][k][e] *= keep, o[nt][k][2 + e] *= keep;
           }
       }
+      uint32_t pb[NT][2];
+      const float f[2] = {vs_now[0] * unit, vs_now[1] * unit};
+      auto weights = [&](auto edge_tag) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float p[2];
+          for (int i = 0; i < 2; ++i) {
+            float p[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = s[nt][2 * i + e];
-            const bool sees = x != -INFINITY;
-            l[nt][e] += sees ? exp2_approx(x - ms[nt][e]) : 0.f;
-            p[e] = sees && lv[i] != -INFINITY ? copysignf(exp2_approx(x + lv[i] - mt[nt][e]), sg[i]) : 0.f;
+            for (int e = 0; e < 2; ++e) {
+              const float x = s[nt][2 * i + e];
+              p[e] = exp2_approx(x - m[nt][e]);
+              l[nt][e] += p[e];
+              p[e] *= f[i];
+              if constexpr (decltype(edge_tag)::value) p[e] = x == -INFINITY ? 0.f : p[e];  // (a scale may be infinite)
+            }
+            pb[nt][i] = transposed8x8(fp16_pack(p[0], p[1]));
           }
-          pb[nt][i] = transposed8x8(fp16_pack(p[0], p[1]));
-        }
+      };
+      if (edge) weights(std::true_type{});
+      else weights(std::false_type{});
       // values -> sums: a lane's bytes are values g D/8 + 2k, + 1 of step k, for tokens 2 cc, 2 cc + 1 (and + 8, + 9)
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -293,14 +341,14 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t v = __byte_perm(x, y, (b + e) | (b + e) << 4 | (4 + b + e) << 8 | (4 + b + e) << 12);
-            af[2 * i + e] = minus1152(((v & 0x00FF00FFu) ^ 0x00800080u) | 0x64006400u);
+            af[2 * i + e] = minus1152((v & 0x00FF00FFu) ^ 0x64806480u);
           }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][k], af, pb[nt][0], pb[nt][1]);
       }
-      load_v(row_next);
-      row_next = row_after;
+      load_v(is_next, row_next);
+      row_next = row_after, is_next = is_after;
     }
 
     // ---- the piece's result ----
@@ -324,7 +372,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
 #pragma unroll
         for (int k = 0; k < D / 16; k += 2)
           *reinterpret_cast<float4*>(dst + 2 * k) = make_float4(o[nt][k][e], o[nt][k][2 + e], o[nt][k + 1][e], o[nt][k + 1][2 + e]);
-        if (g == 0) pl.ml[q] = make_float4(mt[nt][e], ms[nt][e], x, 0.f);
+        if (g == 0) pl.ml[q] = make_float4(held < -150.f ? -INFINITY : m[nt][e] + held, above[nt][e] == -INFINITY ? -INFINITY : m[nt][e], x, 0.f);
       }
 
     // ---- on to the next segment ----
@@ -342,17 +390,19 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
   }
 }
 
-// Joins the pieces of a row: a warp per (request, head), lanes across its values.
-template <int D>
+// Joins the pieces of a row (request, head): kTeam warps to a row, lanes across its values.
+template <int D, uint32_t kTeam>
 __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAttnArgs a, DecodePlan pl) {
+  constexpr uint32_t kWarps = kDecodeThreads / 32;
   __shared__ UnitScan scan;
-  const uint32_t lane = threadIdx.x & 31;
+  __shared__ float sum_o[kWarps][D], sum_m[kWarps], sum_l[kWarps];
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t group = a.q_heads / c.kv_heads;
   bool bad;
   const int32_t prefix = decode_prefix(c, a, bad);
   scan_units(c, a, prefix, scan, false);
-  const uint32_t item = blockIdx.x * (kDecodeThreads / 32) + (threadIdx.x >> 5);
-  if (item >= a.n_reqs * a.q_heads) return;
+  const uint32_t wanted = blockIdx.x * (kWarps / kTeam) + warp / kTeam, items = a.n_reqs * a.q_heads;
+  const uint32_t item = min(wanted, items - 1);  // (no warp leaves: there is a barrier ahead)
   const uint32_t r = item / a.q_heads, head = item % a.q_heads, hk = head / group, g = head % group;
   const int32_t len = decode_len(c, a, prefix, r, bad);
   const uint32_t prefix_units = pl.prefix_groups ? ((uint32_t)prefix + kUnit - 1) / kUnit : 0;
@@ -381,7 +431,7 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   // 32 results at a time: a lane finds one's place and reads its (mt, ms, l); then all lanes add them up one after another
-  for (uint32_t k0 = 0; k0 < all; k0 += 32) {
+  for (uint32_t k0 = 32 * (warp % kTeam); k0 < all; k0 += 32 * kTeam) {
     const uint32_t k = k0 + lane;
     const float* src = nullptr;
     float4 x = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
@@ -423,11 +473,43 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
     for (uint32_t i = 0; i < last; ++i) {
       const float* from = reinterpret_cast<const float*>(__shfl_sync(~0u, (unsigned long long)src, i));
       const float f = __shfl_sync(~0u, by, i);
-      if (!(have >> i & 1)) continue;
+      float v[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(from[lane * E + e], f, o[e]);
+      for (int e = 0; e < E; ++e) v[e] = 0.f;
+      if (have >> i & 1) {
+        if constexpr (E == 4) {
+          const float4 x4 = __ldg(reinterpret_cast<const float4*>(from) + lane);
+          v[0] = x4.x, v[1] = x4.y, v[E - 2] = x4.z, v[E - 1] = x4.w;
+        } else {
+          const float2 x2 = __ldg(reinterpret_cast<const float2*>(from) + lane);
+          v[0] = x2.x, v[1] = x2.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(v[e], f, o[e]);
     }
   }
+  if constexpr (kTeam > 1) {
+    if (lane == 0) sum_m[warp] = m, sum_l[warp] = l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum_o[warp][lane * E + e] = o[e];
+    __syncthreads();
+    if (warp % kTeam) return;
+#pragma unroll
+    for (uint32_t i = 1; i < kTeam; ++i) m = fmaxf(m, sum_m[warp + i]);
+    const float own = sum_m[warp] == -INFINITY ? 0.f : exp2_approx(sum_m[warp] - m);
+    l *= own;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= own;
+#pragma unroll
+    for (uint32_t i = 1; i < kTeam; ++i) {
+      const float f = sum_m[warp + i] == -INFINITY ? 0.f : exp2_approx(sum_m[warp + i] - m);
+      l = fmaf(sum_l[warp + i], f, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(sum_o[warp + i][lane * E + e], f, o[e]);
+    }
+  }
+  if (wanted >= items) return;
   uint16_t* dst = a.out + (uint64_t)r * a.out_stride + (uint64_t)head * D + lane * E;
   const float inv = len > 0 ? 1.f / l : 0.f;  // (a sum of 0 although tokens were seen: every score was -infinity, the result is NaN)
 #pragma unroll
@@ -440,8 +522,13 @@ cudaError_t launch(const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, 
   const uint32_t blocks = pl.warps / (kDecodeThreads / 32);
   if (pl.rows == 8) kv_decode_kernel<D, 1><<<blocks, kDecodeThreads, 0, s>>>(c, a, pl);
   else kv_decode_kernel<D, 2><<<blocks, kDecodeThreads, 0, s>>>(c, a, pl);
+  // few rows may have hundreds of pieces each: as many warps to a row as fill the warps that ran before, 8 at most
   const uint32_t items = a.n_reqs * a.q_heads;
-  kv_join_kernel<D><<<(items + kDecodeThreads / 32 - 1) / (kDecodeThreads / 32), kDecodeThreads, 0, s>>>(c, a, pl);
+  const uint64_t twice = 2ull * items;
+  if (twice > pl.warps) kv_join_kernel<D, 1><<<(items + 7) / 8, kDecodeThreads, 0, s>>>(c, a, pl);
+  else if (2 * twice > pl.warps) kv_join_kernel<D, 2><<<(items + 3) / 4, kDecodeThreads, 0, s>>>(c, a, pl);
+  else if (4 * twice > pl.warps) kv_join_kernel<D, 4><<<(items + 1) / 2, kDecodeThreads, 0, s>>>(c, a, pl);
+  else kv_join_kernel<D, 8><<<items, kDecodeThreads, 0, s>>>(c, a, pl);
   return cudaGetLastError();
 }
 
