@@ -145,6 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t group = a.q_heads / c.kv_heads, hk = blockIdx.x % c.kv_heads;
 
+  after_previous();
+  let_next();
   // after a wait that gave up the call has failed: the other blocks do not start on it
   if (__syncthreads_or(*reinterpret_cast<volatile uint32_t*>(&a.st->status) == SHN_ERR_TIMEOUT)) return;
   Work w;
@@ -189,14 +191,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     // ---- softmax -------------------------------------------------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // the queries of the block as an operand, zeros behind the last row
-    for (uint32_t i = tid; i < kRows * (D / 8); i += kSoftThreads) {
-      const uint32_t row = i / (D / 8), piece = i % (D / 8);
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (row < rows_here) {
-        const uint32_t g = w.row0 + row;
-        x = *reinterpret_cast<const uint4*>(a.q + (uint64_t)(w.q0 + g / group) * a.q_stride + (uint64_t)(hk * group + g % group) * D + piece * 8);
-      }
-      sts128(base + L::q + (row / 128) * L::kOperand + (piece / 8) * kHalf + swizzled(row % 128, piece % 8), x);
+    uint4 qx[kRows * D / 8 / kSoftThreads];  // all loads first: one wait for them
+#pragma unroll
+    for (uint32_t i = 0; i < kRows * D / 8 / kSoftThreads; ++i) {
+      const uint32_t at = tid + i * kSoftThreads, row = at / (D / 8), piece = at % (D / 8), g = w.row0 + row;
+      qx[i] = make_uint4(0, 0, 0, 0);
+      if (row < rows_here)
+        qx[i] = *reinterpret_cast<const uint4*>(a.q + (uint64_t)(w.q0 + g / group) * a.q_stride + (uint64_t)(hk * group + g % group) * D + piece * 8);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kRows * D / 8 / kSoftThreads; ++i) {
+      const uint32_t at = tid + i * kSoftThreads, row = at / (D / 8), piece = at % (D / 8);
+      sts128(base + L::q + (row / 128) * L::kOperand + (piece / 8) * kHalf + swizzled(row % 128, piece % 8), qx[i]);
     }
     fence_smem();
     bar_arrive(bars + kQFull);
@@ -588,8 +594,7 @@ cudaError_t launch(uint64_t blocks, const KvPages& c, const KvAttnArgs& a, const
   if (blocks >= (1ull << 31)) return cudaErrorInvalidConfiguration;
   const cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D, kPart>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::total);
   if (e != cudaSuccess) return e;
-  kv_prompt_kernel<D, kPart><<<(uint32_t)blocks, kThreads, Layout<D>::total, s>>>(c, a, pl);
-  return cudaGetLastError();
+  return launch_behind(kv_prompt_kernel<D, kPart>, dim3((uint32_t)blocks), kThreads, Layout<D>::total, s, c, a, pl);
 }
 
 }  // namespace

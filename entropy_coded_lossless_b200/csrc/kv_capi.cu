@@ -35,7 +35,7 @@ KvPages pages_of(const shn_kv_cache* c) {
 // The workspace's status word, cleared on the stream. Null on failure (err set).
 DeviceStatus* clear_status(void* d_work, cudaStream_t s) {
   DeviceStatus* st = static_cast<DeviceStatus*>(d_work);
-  return cudaMemsetAsync(st, 0, sizeof(DeviceStatus), s) == cudaSuccess ? st : nullptr;
+  return launch_kv_begin(st, s) == cudaSuccess ? st : nullptr;
 }
 
 int check_work(const void* d_work, size_t have, size_t need) {

@@ -49,6 +49,10 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
   const uint32_t lane = threadIdx.x & 31, g = lane >> 2, cc = lane & 3;
   const uint32_t w = blockIdx.x * (kDecodeThreads / 32) + (threadIdx.x >> 5);
   const uint32_t group = a.q_heads / c.kv_heads;
+  // Nothing here reads what the kernel before writes. Where that is the prefix's, the status word is cleared already, and only
+  // the end of this kernel has to come after it (the join is behind both); else the clearing comes first.
+  if (!pl.splits) after_previous();
+  let_next();
   bool bad;
   const int32_t prefix = decode_prefix(c, a, bad);
   if (bad && blockIdx.x == 0 && threadIdx.x == 0) report(a.st, SHN_ERR_INVALID_ARG, 0);
@@ -58,8 +62,9 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
   const uint32_t prefix_segs = c.kv_heads * pl.prefix_groups, seg_per_req = c.kv_heads * pl.own_groups;
   const unsigned long long own0 = (unsigned long long)prefix_segs * prefix_units;
   const unsigned long long units = own0 + scan.before[kDecodeThreads] * seg_per_req;
-  unsigned long long u = first_unit(w, units, pl.warps);
-  const unsigned long long u_end = first_unit(w + 1, units, pl.warps);
+  const Line line(units, pl.warps);
+  unsigned long long u = line.first(w);
+  const unsigned long long u_end = line.first(w + 1);
 
   // the segment of unit u
   uint32_t r = 0, sub = 0;              // request (own tokens) and segment within it; or the prefix segment
@@ -388,6 +393,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
         while (own_units(prefix, decode_len(c, a, prefix, r, bad)) == 0) ++r;  // ends: there are units left
     }
   }
+  if (pl.splits) after_previous();
 }
 
 // Joins the pieces of a row (request, head): kTeam warps to a row, lanes across its values.
@@ -410,6 +416,7 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
   const unsigned long long own0 = (unsigned long long)prefix_segs * prefix_units;
   const unsigned long long units = own0 + scan.before[kDecodeThreads] * seg_per_req;
 
+  const Line line(units, pl.warps);
   // the row's results, in this order: pieces of the prefix's segment, parts of the prefix, pieces of its own tokens' segment
   const uint32_t prow = r * group + g, psub = pl.prefix_groups ? hk * pl.prefix_groups + prow / pl.rows : 0;
   const uint32_t osub = hk * pl.own_groups + g / pl.rows;
@@ -417,19 +424,20 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
   uint32_t pw = 0, pn = 0, ow = 0, on = 0;  // first warp and number of pieces
   if (prefix_units) {
     const unsigned long long u0 = (unsigned long long)psub * prefix_units;
-    pw = warp_of(u0, units, pl.warps);
-    pn = warp_of(u0 + prefix_units - 1, units, pl.warps) - pw + 1;
+    pw = line.warp_of(u0);
+    pn = line.warp_of(u0 + prefix_units - 1) - pw + 1;
   }
   if (n) {
     const unsigned long long u0 = own0 + units_before(c, a, prefix, scan, r) * seg_per_req + (unsigned long long)osub * n;
-    ow = warp_of(u0, units, pl.warps);
-    on = warp_of(u0 + n - 1, units, pl.warps) - ow + 1;
+    ow = line.warp_of(u0);
+    on = line.warp_of(u0 + n - 1) - ow + 1;
   }
   const uint32_t all = pn + pl.splits + on;
   constexpr int E = D / 32;
   float o[E], l = 0.f, m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
+  after_previous();
   // 32 results at a time: a lane finds one's place and reads its (mt, ms, l); then all lanes add them up one after another
   for (uint32_t k0 = 32 * (warp % kTeam); k0 < all; k0 += 32 * kTeam) {
     const uint32_t k = k0 + lane;
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
       } else {
         const bool mine = k >= pn;
         const uint32_t w = mine ? ow + (k - pn - pl.splits) : pw + k;
-        if (first_unit(w, units, pl.warps) != first_unit(w + 1, units, pl.warps)) {  // (there are warps without units)
+        if (line.first(w) != line.first(w + 1)) {  // (there are warps without units)
           const uint64_t q = (uint64_t)(w + (mine ? prefix_segs + r * seg_per_req + osub : psub)) * pl.rows + (mine ? g : prow) % pl.rows;
           src = pl.out + q * D;
           x = pl.ml[q];
@@ -478,10 +486,10 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
       for (int e = 0; e < E; ++e) v[e] = 0.f;
       if (have >> i & 1) {
         if constexpr (E == 4) {
-          const float4 x4 = __ldg(reinterpret_cast<const float4*>(from) + lane);
+          const float4 x4 = reinterpret_cast<const float4*>(from)[lane];  // (written while this kernel may have run: no __ldg)
           v[0] = x4.x, v[1] = x4.y, v[E - 2] = x4.z, v[E - 1] = x4.w;
         } else {
-          const float2 x2 = __ldg(reinterpret_cast<const float2*>(from) + lane);
+          const float2 x2 = reinterpret_cast<const float2*>(from)[lane];
           v[0] = x2.x, v[1] = x2.y;
         }
       }
@@ -519,17 +527,17 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
 
 template <int D>
 cudaError_t launch(const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s) {
-  const uint32_t blocks = pl.warps / (kDecodeThreads / 32);
-  if (pl.rows == 8) kv_decode_kernel<D, 1><<<blocks, kDecodeThreads, 0, s>>>(c, a, pl);
-  else kv_decode_kernel<D, 2><<<blocks, kDecodeThreads, 0, s>>>(c, a, pl);
+  const dim3 blocks(pl.warps / (kDecodeThreads / 32));
+  const cudaError_t e = pl.rows == 8 ? launch_behind(kv_decode_kernel<D, 1>, blocks, kDecodeThreads, 0, s, c, a, pl)
+                                     : launch_behind(kv_decode_kernel<D, 2>, blocks, kDecodeThreads, 0, s, c, a, pl);
+  if (e != cudaSuccess) return e;
   // few rows may have hundreds of pieces each: as many warps to a row as fill the warps that ran before, 8 at most
   const uint32_t items = a.n_reqs * a.q_heads;
   const uint64_t twice = 2ull * items;
-  if (twice > pl.warps) kv_join_kernel<D, 1><<<(items + 7) / 8, kDecodeThreads, 0, s>>>(c, a, pl);
-  else if (2 * twice > pl.warps) kv_join_kernel<D, 2><<<(items + 3) / 4, kDecodeThreads, 0, s>>>(c, a, pl);
-  else if (4 * twice > pl.warps) kv_join_kernel<D, 4><<<(items + 1) / 2, kDecodeThreads, 0, s>>>(c, a, pl);
-  else kv_join_kernel<D, 8><<<items, kDecodeThreads, 0, s>>>(c, a, pl);
-  return cudaGetLastError();
+  if (twice > pl.warps) return launch_behind(kv_join_kernel<D, 1>, dim3((items + 7) / 8), kDecodeThreads, 0, s, c, a, pl);
+  if (2 * twice > pl.warps) return launch_behind(kv_join_kernel<D, 2>, dim3((items + 3) / 4), kDecodeThreads, 0, s, c, a, pl);
+  if (4 * twice > pl.warps) return launch_behind(kv_join_kernel<D, 4>, dim3((items + 1) / 2), kDecodeThreads, 0, s, c, a, pl);
+  return launch_behind(kv_join_kernel<D, 8>, dim3(items), kDecodeThreads, 0, s, c, a, pl);
 }
 
 }  // namespace

@@ -2,8 +2,8 @@
 //
 // A segment is a run of tokens with the query rows that read it: the tokens of one request that are its own (rows: the
 // heads of a group), or the shared prefix (rows: all requests' heads of a group). Its tokens are counted in units of
-// kUnit, all segments' units lie in one line, and warp w of W takes the units [w U / W, (w + 1) U / W): every warp the
-// same number, whatever the lengths. A warp's part of a segment is a piece; pieces are numbered w + segment, which is
+// kUnit, all segments' units lie in one line, and each of the W warps takes the same number in a row (or one more),
+// whatever the lengths. A warp's part of a segment is a piece; pieces are numbered w + segment, which is
 // unique because both only grow along the line. A piece's result for a row is (O, mt, ms, l):
 //   sum of weights = l 2^ms,  sum of weighted values = O 2^mt
 // and a last kernel joins a row's pieces in their order, so results do not depend on timing.
@@ -89,11 +89,25 @@ __device__ __forceinline__ unsigned long long units_before(const KvPages& c, con
   }
   return u;
 }
-__device__ __forceinline__ unsigned long long first_unit(uint32_t w, unsigned long long units, uint32_t warps) { return w * units / warps; }
-// The warp that takes unit u.
-__device__ __forceinline__ uint32_t warp_of(unsigned long long u, unsigned long long units, uint32_t warps) {
-  return (uint32_t)(((u + 1) * warps - 1) / units);
-}
+// The line of units and the warps' shares of it: the first `rest` warps take one unit more than the others.
+struct Line {
+  unsigned long long units, cut;  // cut: units of the first `rest` warps
+  unsigned long long each;
+  uint32_t rest;
+  __device__ __forceinline__ Line(unsigned long long n, uint32_t warps) : units(n) {
+    if (n >> 32) each = n / warps;
+    else each = (uint32_t)n / warps;  // (the 64-bit division is many times as long)
+    rest = (uint32_t)(n - each * warps);
+    cut = rest * (each + 1);
+  }
+  __device__ __forceinline__ unsigned long long first(uint32_t w) const { return w * each + min(w, rest); }
+  // The warp that takes unit u (u < units).
+  __device__ __forceinline__ uint32_t warp_of(unsigned long long u) const {
+    const bool in = u < cut;
+    const unsigned long long x = in ? u : u - cut, y = in ? each + 1 : each;
+    return (in ? 0 : rest) + (uint32_t)(units >> 32 ? x / y : (uint32_t)x / (uint32_t)y);
+  }
+};
 
 // The prefix in pl.splits parts (kv_attn_tc.cu): parts' sums into pl.split_out, pl.split_ml.
 cudaError_t launch_kv_prefix(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s);

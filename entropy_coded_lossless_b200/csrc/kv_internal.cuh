@@ -37,6 +37,28 @@ __device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
   return r;
 }
 
+// A call's first kernel clears the status word; the next ones are launched so that they start while the one before still
+// runs (programmatic dependent launch) and hide their start behind it. A kernel launched so reads nothing that the one
+// before writes, and reports nothing, until after_previous(); let_next() lets the one after it start.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, uint32_t threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+cudaError_t launch_kv_begin(DeviceStatus* st, cudaStream_t s);
+
 struct KvPlanArgs {
   const int32_t *ctx, *fresh;
   uint32_t n, log2_pt, max_blocks, n_free, max_tokens;

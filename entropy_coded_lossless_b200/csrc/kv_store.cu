@@ -5,6 +5,11 @@
 namespace shn {
 namespace {
 
+__global__ void kv_begin_kernel(DeviceStatus* st) {
+  let_next();
+  if (threadIdx.x == 0) st->status = 0, st->detail = 0;
+}
+
 // ---- shn_kv_store -------------------------------------------------------------------------------
 // HBM-bound: every value is read and written once and costs about ten operations. A head row of D values
 // is held by D/8 lanes, 8 values (16 bytes) each, so that a row's sum of squares and its largest
@@ -16,6 +21,7 @@ constexpr int kStoreThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(KvPages c, KvStoreArgs a) {
   constexpr uint32_t kLanes = D / 8, kGroups = kStoreThreads / kLanes;
+  after_previous();
   const uint32_t token = blockIdx.x, lane = threadIdx.x % kLanes;
   const uint32_t rows = a.q_heads + 2 * c.kv_heads;
   const uint32_t warp_lane = threadIdx.x & 31u;
@@ -139,6 +145,7 @@ __device__ __forceinline__ float int8_of(uint32_t w, int i) { return (float)(int
 template <int D>
 __global__ void __launch_bounds__(kLoadThreads) kv_load_kernel(KvPages c, KvLoadArgs a) {
   constexpr uint32_t kLanes = D / 16;
+  after_previous();
   const uint64_t step = (uint64_t)gridDim.x * kLoadThreads / kLanes;
   const uint32_t lane = threadIdx.x % kLanes;
   const uint64_t rows = (uint64_t)a.n_tokens * c.kv_heads;
@@ -171,24 +178,28 @@ __global__ void __launch_bounds__(kLoadThreads) kv_load_kernel(KvPages c, KvLoad
 
 }  // namespace
 
+cudaError_t launch_kv_begin(DeviceStatus* st, cudaStream_t s) {
+  kv_begin_kernel<<<1, 32, 0, s>>>(st);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_kv_store(const KvPages& c, uint32_t head_dim, const KvStoreArgs& a, int sm_count, cudaStream_t s) {
   const uint32_t groups = kStoreThreads * 8 / head_dim, rows = a.q_heads + 2 * c.kv_heads;
   // few tokens: their rows over several blocks, until the SMs have two blocks each or a block has one row per group
   uint32_t parts = 1;
   while ((uint64_t)parts * a.n_tokens < 2ull * sm_count && parts * groups < rows) ++parts;
   const dim3 grid(a.n_tokens, parts);
-  if (head_dim == 128) kv_store_kernel<128><<<grid, kStoreThreads, 0, s>>>(c, a);
-  else kv_store_kernel<64><<<grid, kStoreThreads, 0, s>>>(c, a);
-  return cudaGetLastError();
+  return head_dim == 128 ? launch_behind(kv_store_kernel<128>, grid, kStoreThreads, 0, s, c, a)
+                         : launch_behind(kv_store_kernel<64>, grid, kStoreThreads, 0, s, c, a);
 }
 
 cudaError_t launch_kv_load(const KvPages& c, uint32_t head_dim, const KvLoadArgs& a, int sm_count, cudaStream_t s) {
   const uint64_t threads = (uint64_t)a.n_tokens * c.kv_heads * (head_dim / 16);
   uint64_t blocks = (threads + kLoadThreads - 1) / kLoadThreads;
   if (blocks > 8ull * sm_count) blocks = 8ull * sm_count;
-  if (head_dim == 128) kv_load_kernel<128><<<(uint32_t)blocks, kLoadThreads, 0, s>>>(c, a);
-  else kv_load_kernel<64><<<(uint32_t)blocks, kLoadThreads, 0, s>>>(c, a);
-  return cudaGetLastError();
+  const dim3 grid((uint32_t)blocks);
+  return head_dim == 128 ? launch_behind(kv_load_kernel<128>, grid, kLoadThreads, 0, s, c, a)
+                         : launch_behind(kv_load_kernel<64>, grid, kLoadThreads, 0, s, c, a);
 }
 
 }  // namespace shn
