@@ -7,7 +7,7 @@
 //   s = S * k_scale_j * softmax_scale * log2(e);  p = 2^(s - m);  l += p;  P = fp16(p)
 //   O += P V       tcgen05.mma, fp16, P read from TMEM (it takes the place of S)
 // Keys enter as the integers, which bf16 holds exactly, and their scales are applied to the float32 scores: scores have
-// float32's error. Values enter as fp16(int8 * v_scale * 2^-e), e the exponent of the tile's largest value scale, the
+// float32's error. Values enter as fp16(int8 * v_scale * 2^-e), e the exponent of the largest value scale of 32 tokens, the
 // product formed to more than fp16's 11 bits and rounded once; the weights are rounded to fp16 (2^-11 each, where bf16 operands
 // would cost 2^-8 twice). The power of two goes into the weights: P = p 2^(e - E), with E the exponent O is held in, raised
 // like the softmax's reference when a tile's values are more than 2^7 larger. A weight smaller than 2^-24 of that range is
@@ -238,11 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       fence_after();
-      const float e_v = __uint_as_float(lds32(base + L::info + (j & 3) * 4));
-      const bool larger = j > 0 && e_v > held + kValueRise;
-      const float lower = larger ? pow2(fmaxf(held - e_v, -126.f)) : 1.f;  // what O is scaled by then
-      if (j == 0 || larger) held = e_v;
-      const float by = fmaxf(e_v - held, kValueFall), unby = pow2(-by);
+      // the size (log2) of the value scales, 32 tokens a time
+      const uint4 sizes = lds128(base + L::info + (j & 3) * 16);
+      const float size[4] = {__uint_as_float(sizes.x), __uint_as_float(sizes.y), __uint_as_float(sizes.z), __uint_as_float(sizes.w)};
+      const float largest = fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3]));
+      const bool larger = j > 0 && largest > held + kValueRise;
+      const float lower = larger ? pow2(fmaxf(held - largest, -126.f)) : 1.f;  // what O is scaled by then
+      if (j == 0 || larger) held = largest;
       // half a tile (64 tokens) at a time: its part of P V can begin while the other half is worked on
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -254,16 +256,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         const int32_t first = (int32_t)(j * kTile + 64 * h + col);
         const bool edge = __any_sync(~0u, first - (int32_t)col + 64 > min(seen[0], seen[1]));
         float top[2];
-        uint64_t sum[2], ref[2];
+        float sum[2];
         // Weights against the reference that stands; scores relative to it are watched, not searched first: almost
         // always none is above the limit and this one pass is all. (Two versions: only tiles at the end of what a row
         // sees look at the columns' places.)
         auto weights = [&](auto edge_tag) {
           constexpr bool kEdge = decltype(edge_tag)::value;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) top[r] = -INFINITY, sum[r] = 0, ref[r] = pack2(neg[r] + by, neg[r] + by);
+          for (int r = 0; r < 2; ++r) top[r] = -INFINITY, sum[r] = 0.f;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {  // 32 columns: 16 of packed pairs
+            const float by = fmaxf(size[2 * h + b] - held, kValueFall);  // their weights' power of two
+            uint64_t part[2] = {0, 0}, ref[2];
+            float high[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int r = 0; r < 2; ++r) ref[r] = pack2(neg[r] + by, neg[r] + by);
             uint32_t p[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -278,18 +285,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
                   x = first + 8 * n < seen[r] ? x : -INFINITY;
                   y = first + 8 * n + 1 < seen[r] ? y : -INFINITY;
                 }
-                top[r] = max3(top[r], x, y);
+                high[r] = max3(high[r], x, y);
                 x = exp2_approx(x), y = exp2_approx(y);
-                sum[r] = add2(sum[r], pack2(x, y));
+                part[r] = add2(part[r], pack2(x, y));
                 p[2 * i + r] = fp16_pack(x, y);
               }
             }
             st_pairs8(s_at + 32 * h + 16 * b, p);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float x, y;
+              unpack2(part[r], x, y);
+              sum[r] = fmaf(x + y, pow2(-by), sum[r]);
+              top[r] = fmaxf(top[r], high[r] - by);
+            }
           }
         };
         if (edge) weights(std::true_type{});
         else weights(std::false_type{});
-        if (__any_sync(~0u, top[0] > limit[0] + by || top[1] > limit[1] + by) || (larger && h == 0)) {
+        if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1]) || (larger && h == 0)) {
           // the reference rises: what is summed is scaled down, and the weights formed again
           float keep[2];
 #pragma unroll
@@ -297,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
             top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
             top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
             keep[r] = 1.f;
-            if (top[r] > limit[r] + by) {
-              const float next = (m[r] == -INFINITY ? 0.f : m[r]) + (top[r] - by);
+            if (top[r] > limit[r]) {
+              const float next = m[r] == -INFINITY ? top[r] : m[r] + top[r];
               keep[r] = exp2_approx(m[r] - next);
               m[r] = next;
               neg[r] = -next;
@@ -325,11 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
           else weights(std::false_type{});
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float x, y;
-          unpack2(sum[r], x, y);
-          l[r] = fmaf(x + y, unby, l[r]);
-        }
+        for (int r = 0; r < 2; ++r) l[r] += sum[r];
         wait_st();
         fence_before();
         __syncwarp();
@@ -457,19 +467,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       fence_smem();
       __syncwarp();
     };
-    // Scales: a lane holds the value scales of tokens lane, lane + 32, +64, +96 of the tile (every warp, so that each finds the
-    // tile's largest by itself), and in the first four warps the key scale of token t.
+    // Scales: a lane holds the two of one token of the warp's 32 (two warps share them; the even one publishes).
+    const uint32_t own32 = (cw >> 1) * 32 + lane;
     const float factor = a.scale * 1.44269504088896340736f;  // log2(e)
-    float k_scale = 0.f, v_scale[4];
+    float k_scale = 0.f, v_scale = 0.f;  // as loaded: nothing waits for them here
     auto fetch_scales = [&](uint32_t j, int32_t pages) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int32_t p = __shfl_sync(~0u, pages, 2 * i + (lane >> 4));
-        const uint32_t tok = j * kTile + 32 * i + lane;
-        const bool is = p >= 0 && (int32_t)tok < most;
-        const uint64_t at = kv_row(c, (uint32_t)p, hk, (tok + skip) & pt_mask);
-        v_scale[i] = is ? c.v_scale[at] : 0.f;
-        if (cw == (uint32_t)i) k_scale = is ? c.k_scale[at] * factor : 0.f;
+      const int32_t p = __shfl_sync(~0u, pages, own32 >> 4);
+      k_scale = v_scale = 0.f;
+      if (p >= 0 && (int32_t)(j * kTile + own32) < most) {
+        const uint64_t at = kv_row(c, (uint32_t)p, hk, (j * kTile + own32 + skip) & pt_mask);
+        k_scale = c.k_scale[at];
+        v_scale = c.v_scale[at];
       }
     };
     int32_t pages = pages_of(0);
@@ -488,21 +496,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       // this K buffer is free since those of tile j - 2 are done.
       // A value scale that is not finite (or so large that its values would not be) makes the token's key scale NaN, and its values
       // zeros: whoever sees the token gets NaN, and a masked weight of 0 meets no infinity.
-      uint32_t top = 0;
-      float mine = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool bad = !(fabsf(v_scale[i]) < 1e36f);
-        if (bad) v_scale[i] = 0.f;
-        if (cw == (uint32_t)i) sts32(base + L::scale + (j & 3) * 512 + 4 * t, bad ? 0x7FC00000u : __float_as_uint(k_scale));
-        top = max(top, __float_as_uint(fabsf(v_scale[i])));
-        if ((first >> 5) == (uint32_t)i) mine = v_scale[i];
+      const bool bad = !(fabsf(v_scale) < 1e36f);
+      const float v = bad ? 0.f : v_scale;
+      // 2^(e_v - 127) <= the largest of the 32 < 2^(e_v - 126)
+      const uint32_t e_v = max(__reduce_max_sync(~0u, __float_as_uint(fabsf(v))) >> 23, 1u);
+      if ((cw & 1) == 0) {
+        sts32(base + L::scale + (j & 3) * 512 + 4 * own32, bad ? 0x7FC00000u : __float_as_uint(k_scale * factor));
+        if (lane == 0) sts32(base + L::info + (j & 3) * 16 + 2 * cw, __float_as_uint((float)(int32_t)(e_v - 127)));
       }
-      top = __reduce_max_sync(~0u, top) >> 23;  // 2^(top - 127) <= the largest scale < 2^(top - 126)
-      const uint32_t e_v = max(top, 1u);
-      if (t == 0) sts32(base + L::info + (j & 3) * 4, __float_as_uint((float)(int32_t)(e_v - 127)));
-      // the scale of row first + lane (mod 32) in [0, 2) as fp16 and what that leaves over, packed
-      const uint32_t row_scale = split_fp16(mine * __uint_as_float((254u - e_v) << 23));
+      // the lane's scale in [0, 2) as fp16 and what that leaves over, packed
+      const uint32_t row_scale = split_fp16(v * __uint_as_float((254u - e_v) << 23));
       turn(std::false_type{}, 0u, base + L::k + buf * L::kOperand, c.v, off);
       if (lane == 0) {
         bar_arrive(bars + kScaleFull + 8 * (j & 3));
