@@ -524,25 +524,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       constexpr uint32_t kS = instr_desc(128, 128, true, false), kO = instr_desc(128, D, false, true);
       const bool lead = elect_one();
       auto scores = [&](uint32_t i, uint32_t buf) {
-        const uint64_t q = smem_desc(base + L::q + i * L::kOperand, 16), k = smem_desc(base + L::k + buf * L::kOperand, 16);
-        if (lead) {
+        const uint32_t q = smem_desc(base + L::q + i * L::kOperand, 16), k = smem_desc(base + L::k + buf * L::kOperand, 16);
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e) {
-            const uint32_t off = ((e / 4) * kHalf + (e % 4) * 32) >> 4;
-            mma_ss(tmem + 128 * i, q + off, k + off, kS, e > 0);
-          }
-          commit(bars + kSFull + 8 * i);
+        for (int e = 0; e < D / 16; ++e) {
+          const uint32_t off = ((e / 4) * kHalf + (e % 4) * 32) >> 4;
+          if (e == 0) mma_ss<false>(tmem + 128 * i, q + off, k + off, kS, lead);
+          else mma_ss<true>(tmem + 128 * i, q + off, k + off, kS, lead);
         }
+        commit(bars + kSFull + 8 * i, lead);
       };
       // tokens 64 h .. 64 h + 63 of the tile
       auto values = [&](uint32_t i, uint32_t buf, uint32_t h, bool add) {
-        const uint64_t v = smem_desc(base + L::v + buf * L::kOperand, kHalf) + h * (4 * 2048 >> 4);
+        const uint32_t v = smem_desc(base + L::v + buf * L::kOperand, kHalf) + h * (4 * 2048 >> 4);
         const uint32_t p = tmem + 128 * i + 32 * h;
-        if (lead) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma_ts(tmem + 256 + D * i, p + 8 * e, v + e * (2048 >> 4), kO, add || e > 0);
-          commit(bars + kOFull + 16 * i + 8 * h);
-        }
+        for (int e = 0; e < 4; ++e) mma_ts(tmem + 256 + D * i, p + 8 * e, v + e * (2048 >> 4), kO, add || e > 0, lead);
+        commit(bars + kOFull + 16 * i + 8 * h, lead);
       };
       auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(~0u, bar_wait(bars + bar, parity, stop)); };
       bool ok = wait(kQFull, 0) && wait(kKFull, 0);
@@ -550,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         fence_after();
         scores(0, 0);
         scores(1, 0);
-        if (lead) commit(bars + kKEmpty);
+        commit(bars + kKEmpty, lead);
       }
       for (uint32_t j = 0; ok && j < tiles; ++j) {
         const uint32_t buf = j & 1, nbuf = buf ^ 1;
@@ -565,19 +562,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
             values(i, buf, h, j > 0 || h > 0);
           }
           if (!ok) break;
-          if (i == 1 && lead) commit(bars + kVEmpty + 8 * buf);
+          if (i == 1) commit(bars + kVEmpty + 8 * buf, lead);
           if (j + 1 < tiles) {
             if (i == 0) ok = wait(kKFull + 8 * nbuf, ((j + 1) >> 1) & 1);
             if (!ok) break;
             fence_after();
             scores(i, nbuf);
-            if (i == 1 && lead) commit(bars + kKEmpty + 8 * nbuf);
+            if (i == 1) commit(bars + kKEmpty + 8 * nbuf, lead);
           }
         }
       }
       if (!ok) {
         // gave up: let the products in flight end (again with a limit) before TMEM goes back
-        if (lead) commit(bars + kDrain);
+        commit(bars + kDrain, lead);
         for (uint32_t i = 0; i < kWaitTries && !bar_try(bars + kDrain, 0); ++i) {
         }
       }
