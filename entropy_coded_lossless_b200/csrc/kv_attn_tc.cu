@@ -3,7 +3,7 @@
 //
 // A block takes 256 rows of one key head: row = (query, head of the group), so every key and value it reads serves all
 // heads of the group, whatever their number. It walks the sequence in tiles of 128 tokens:
-//   S = Q K^T      tcgen05.mma, bf16, M = 128 rows, N = 128 tokens, two of them (rows 0-127, rows 128-255), into TMEM
+//   S = Q K^T      tcgen05.mma, fp16, M = 128 rows, N = 64 tokens, for rows 0-127 and 128-255 and both halves, into TMEM
 //   s = S * k_scale_j * softmax_scale * log2(e);  p = 2^(s - m);  l += p;  P = fp16(p)
 //   O += P V       tcgen05.mma, fp16, P read from TMEM (it takes the place of S)
 // Keys enter as the integers, which bf16 holds exactly, and their scales are applied to the float32 scores: scores have
@@ -19,7 +19,7 @@
 //
 // Roles (896 threads): warps 0-7 and 8-15 the softmax of the two row tiles (16 rows to a warp, so that each scheduler
 // has four of them to hide their latencies), warps 16-23 fetch the tiles and turn INT8 into bf16 operands in shared memory,
-// warp 24 issues the products. While the softmax of one row tile works, the
+// warps 24 and 25 issue the products of a row tile each. While the softmax of one row tile works, the
 // products of the other run. Two K and two V buffers; the next tile's bytes are on their way in registers while the present
 // one is converted.
 // TMEM (512 columns): S0, S1 (128 each; P in their first 64), O0, O1 (D each).
@@ -39,18 +39,18 @@ constexpr uint32_t kIssueWarp = kSoftWarps + kConvertWarps;  // in a warpgroup o
 constexpr uint32_t kThreads = 32 * (kIssueWarp + 4);
 constexpr uint32_t kTile = 128;      // tokens of a tile
 constexpr uint32_t kRows = 256;      // query rows of a block
-constexpr float kRise = 8.f;         // how far (log2) a weight may pass 1 before the reference is raised,
-constexpr float kValueRise = 7.f;    // and a tile's values the range O is held in: 2^15 together, within fp16
-constexpr float kValueFall = -60.f;  // a tile this far below adds nothing to O in fp16
+constexpr float kRise = 256.f;       // how far a weight may pass 1 before the reference is raised,
+constexpr float kValueRise = 7.f;    // and (log2) the values the range O is held in: 2^15 together, within fp16
+constexpr float kValueFall = -60.f, kValueFall2 = 1ull << 60;  // a tile this far below adds nothing to O in fp16
 constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows of 64 bf16
 
 template <int D>
 struct Layout {
   static constexpr uint32_t kOperand = 128 * D * 2;  // one 128 x D bf16 operand
-  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, info = scale + 4 * 512, row_sum = info + 64, bars = row_sum + 8 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
+  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, info = scale + 4 * 512, row_sum = info + 128, bars = row_sum + 8 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
 };
 // barriers
-enum : uint32_t { kQFull = 0, kKFull = 8, kKEmpty = 24, kVFull = 40, kVEmpty = 56, kScaleFull = 72, kSFull = 104, kPFull = 120, kOFull = 152, kDrain = 184 };
+enum : uint32_t { kQFull = 0, kKFull = 8, kKEmpty = 24, kVFull = 40, kVEmpty = 56, kScaleFull = 72, kSFull = 104, kPFull = 136, kOFull = 168, kDrain = 200 };
 
 struct Work {
   uint32_t req, row0, rows;  // request, first row of the block within it, rows of the request
@@ -142,7 +142,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   extern __shared__ __align__(1024) uint8_t smem[];
   using L = Layout<D>;
   const uint32_t base = smem_addr(smem), bars = base + L::bars, stop = base + L::misc;
-  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Roles are counted from the second warpgroup on: the issuing warp is the block's first, which the schedulers serve
+  // before younger ones.
+  const uint32_t lane = threadIdx.x & 31, warp = ((threadIdx.x >> 5) + kIssueWarp) % (kThreads / 32), tid = warp * 32 + lane;
   const uint32_t group = a.q_heads / c.kv_heads, hk = blockIdx.x % c.kv_heads;
 
   after_previous();
@@ -161,12 +163,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   if (tid == 0) {
     bar_init(bars + kQFull, kSoftThreads);
     bar_init(bars + kDrain, 1);
+    bar_init(bars + kDrain + 8, 1);
     for (uint32_t i = 0; i < 2; ++i) {
       bar_init(bars + kKFull + 8 * i, kConvertWarps);
-      bar_init(bars + kKEmpty + 8 * i, 1);
+      bar_init(bars + kKEmpty + 8 * i, 2);
       bar_init(bars + kVFull + 8 * i, kConvertWarps);
-      bar_init(bars + kVEmpty + 8 * i, 1);
-      bar_init(bars + kSFull + 8 * i, 1);
+      bar_init(bars + kVEmpty + 8 * i, 2);
+      bar_init(bars + kSFull + 16 * i, 1);
+      bar_init(bars + kSFull + 16 * i + 8, 1);
       bar_init(bars + kPFull + 16 * i, kSoftWarps / 2);
       bar_init(bars + kPFull + 16 * i + 8, kSoftWarps / 2);
       bar_init(bars + kOFull + 16 * i, 1);
@@ -174,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     }
     for (uint32_t i = 0; i < 4; ++i) bar_init(bars + kScaleFull + 8 * i, kConvertWarps);
     sts32(stop, 0);
+    sts32(base + L::misc + 8, 0);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssueWarp) {
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
 
   if (warp < kSoftWarps) {
     // ---- softmax -------------------------------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     // the queries of the block as an operand, zeros behind the last row
     uint4 qx[kRows * D / 8 / kSoftThreads];  // all loads first: one wait for them
 #pragma unroll
@@ -199,10 +204,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if (row < rows_here)
         qx[i] = *reinterpret_cast<const uint4*>(a.q + (uint64_t)(w.q0 + g / group) * a.q_stride + (uint64_t)(hk * group + g % group) * D + piece * 8);
     }
+    // One power of two brings the block's largest query value just below 2^15; fp16 then holds every bf16 down to 2^-32
+    // of it exactly. (Values that are not finite set no size and stay what they are.)
+    uint32_t top = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kRows * D / 8 / kSoftThreads; ++i) {
+      const uint32_t x[4] = {qx[i].x, qx[i].y, qx[i].z, qx[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = x[e] & 0x7FFFu, hi = x[e] >> 16 & 0x7FFFu;
+        top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+      }
+    }
+    top = __reduce_max_sync(~0u, top);
+    if (lane == 0) atomicMax(reinterpret_cast<uint32_t*>(smem + L::misc + 8), top);
+    asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
+    const int32_t q_exp = max(-100, (int32_t)(lds32(base + L::misc + 8) >> 7) - 127) - 14;  // of the power of two taken out
+    const float down = pow2i(-q_exp);
 #pragma unroll
     for (uint32_t i = 0; i < kRows * D / 8 / kSoftThreads; ++i) {
       const uint32_t at = tid + i * kSoftThreads, row = at / (D / 8), piece = at % (D / 8);
-      sts128(base + L::q + (row / 128) * L::kOperand + (piece / 8) * kHalf + swizzled(row % 128, piece % 8), qx[i]);
+      const uint32_t x[4] = {qx[i].x, qx[i].y, qx[i].z, qx[i].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = fp16_pack(bf16_lo(x[e]) * down, bf16_hi(x[e]) * down);
+      sts128(base + L::q + (row / 128) * L::kOperand + (piece / 8) * kHalf + swizzled(row % 128, piece % 8), make_uint4(y[0], y[1], y[2], y[3]));
     }
     fence_smem();
     bar_arrive(bars + kQFull);
@@ -225,50 +251,66 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     int32_t seen[2];
     float m[2], l[2];
     float neg[2];    // minus the reference (0 while there is none)
-    float limit[2];  // how far a score may be above it
-    float held = 0.f;  // E: O is in units of 2^held
+    float limit[2];  // how large a sum of weights may be before it is raised
+    float held = 0.f, held2 = 1.f;  // E and 2^E: O is in units of it
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       seen[r] = seen_by(half * 128 + lanes + quad + 8 * r);
-      m[r] = -INFINITY, l[r] = 0.f, neg[r] = 0.f, limit[r] = -INFINITY;
+      m[r] = -INFINITY, l[r] = 0.f, neg[r] = 0.f, limit[r] = seen[r] ? -1.f : INFINITY;  // (no reference yet: any sum passes)
     }
     bool ok = true;
     for (uint32_t j = 0; j < tiles && ok; ++j) {
-      ok = bar_wait(bars + kScaleFull + 8 * (j & 3), (j >> 2) & 1, stop) && bar_wait(bars + kSFull + 8 * half, j & 1, stop);
-      ok = __all_sync(~0u, ok);
+      ok = __all_sync(~0u, bar_wait(bars + kScaleFull + 8 * (j & 3), (j >> 2) & 1, stop));
       if (!ok) break;
-      fence_after();
       // the size (log2) of the value scales, 32 tokens a time
-      const uint4 sizes = lds128(base + L::info + (j & 3) * 16);
+      const uint32_t info = after_here(base + L::info + (j & 3) * 32);
+      const uint4 sizes = lds128(info);
       const float size[4] = {__uint_as_float(sizes.x), __uint_as_float(sizes.y), __uint_as_float(sizes.z), __uint_as_float(sizes.w)};
       const float largest = fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3]));
       const bool larger = j > 0 && largest > held + kValueRise;
-      const float lower = larger ? pow2(fmaxf(held - largest, -126.f)) : 1.f;  // what O is scaled by then
-      if (j == 0 || larger) held = largest;
-      // half a tile (64 tokens) at a time: its part of P V can begin while the other half is worked on
+      float lower = 1.f;  // what O is scaled by then
+      if (j == 0 || larger) {
+        lower = pow2(fmaxf(held - largest, -126.f));
+        held = largest;
+        held2 = pow2(held);
+      }
+      // Half a tile (64 tokens) at a time. The first half's scores lie in the 64 columns `here`, the second's in the other 64; both
+      // halves' weights go into `here` (32 columns each). So the columns of the second half are free as soon as its scores
+      // are in registers, and the next tile's first half is put there while this one is still worked on: next to no scores are
+      // ever waited for.
+      const uint32_t here = s_at + (j & 1) * 64;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        ok = __all_sync(~0u, bar_wait(bars + kSFull + 16 * half + 8 * h, j & 1, stop));
+        if (!ok) break;
+        fence_after();
         // s[4n + 2r + e]: row quad + 8r, column 64h + 8n + col + e
         uint32_t s[32];
-        ld_quad32(s_at + 64 * h, s);
+        ld_quad32(s_at + ((j + h) & 1) * 64, s);
         wait_ld();
+        if (h == 1) {
+          // the first half's weights are stored and the second's scores loaded
+          wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(bars + kPFull + 16 * half);
+        }
         const uint32_t scales = after_here(base + L::scale + (j & 3) * 512 + h * 256 + 4 * col);
         const int32_t first = (int32_t)(j * kTile + 64 * h + col);
         const bool edge = __any_sync(~0u, first - (int32_t)col + 64 > min(seen[0], seen[1]));
-        float top[2];
         float sum[2];
-        // Weights against the reference that stands; scores relative to it are watched, not searched first: almost
-        // always none is above the limit and this one pass is all. (Two versions: only tiles at the end of what a row
+        // Weights against the reference that stands; no maximum is searched first. A thread's sum of a row's 16 weights shows
+        // whether one of them has passed the limit, which almost never happens: this one pass is all then. (Two versions: only tiles at the end of what a row
         // sees look at the columns' places.)
         auto weights = [&](auto edge_tag) {
           constexpr bool kEdge = decltype(edge_tag)::value;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) top[r] = -INFINITY, sum[r] = 0.f;
+          for (int r = 0; r < 2; ++r) sum[r] = 0.f;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {  // 32 columns: 16 of packed pairs
-            const float by = fmaxf(size[2 * h + b] - held, kValueFall);  // their weights' power of two
+            const float by = fmaxf(lds32_free(info + 8 * h + 4 * b) - held, kValueFall);  // their weights' power of two
+            const float unby = fminf(held2 * lds32_free(info + 16 + 8 * h + 4 * b), kValueFall2);
             uint64_t part[2] = {0, 0}, ref[2];
-            float high[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int r = 0; r < 2; ++r) ref[r] = pack2(neg[r] + by, neg[r] + by);
             uint32_t p[8];
@@ -285,37 +327,46 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
                   x = first + 8 * n < seen[r] ? x : -INFINITY;
                   y = first + 8 * n + 1 < seen[r] ? y : -INFINITY;
                 }
-                high[r] = max3(high[r], x, y);
                 x = exp2_approx(x), y = exp2_approx(y);
                 part[r] = add2(part[r], pack2(x, y));
                 p[2 * i + r] = fp16_pack(x, y);
               }
             }
-            st_pairs8(s_at + 32 * h + 16 * b, p);
+            st_pairs8(here + 32 * h + 16 * b, p);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               float x, y;
               unpack2(part[r], x, y);
-              sum[r] = fmaf(x + y, pow2(-by), sum[r]);
-              top[r] = fmaxf(top[r], high[r] - by);
+              sum[r] = fmaf(x + y, unby, sum[r]);
             }
           }
         };
         if (edge) weights(std::true_type{});
         else weights(std::false_type{});
-        if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1]) || (larger && h == 0)) {
-          // the reference rises: what is summed is scaled down, and the weights formed again
+        if (__any_sync(~0u, sum[0] > limit[0] || sum[1] > limit[1]) || (larger && h == 0)) {
+          // the reference rises to the row's maximum of this half: what is summed is scaled down, and the weights formed again
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const uint64_t ks = lds64_free(scales + 32 * n);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float x, y;
+              unpack2(mul2(pack2(__uint_as_float(s[4 * n + 2 * r]), __uint_as_float(s[4 * n + 2 * r + 1])), ks), x, y);
+              if (first + 8 * n < seen[r]) top[r] = fmaxf(top[r], x);
+              if (first + 8 * n + 1 < seen[r]) top[r] = fmaxf(top[r], y);
+            }
+          }
           float keep[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
             top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
             keep[r] = 1.f;
-            if (top[r] > limit[r]) {
-              const float next = m[r] == -INFINITY ? top[r] : m[r] + top[r];
-              keep[r] = exp2_approx(m[r] - next);
-              m[r] = next;
-              neg[r] = -next;
+            if (top[r] > m[r]) {
+              keep[r] = exp2_approx(m[r] - top[r]);
+              m[r] = top[r];
+              neg[r] = -top[r];
               limit[r] = kRise;
             }
             l[r] *= keep[r];
@@ -340,11 +391,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) l[r] += sum[r];
-        wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(bars + kPFull + 16 * half + 8 * h);
       }
+      if (!ok) break;
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bars + kPFull + 16 * half + 8);
     }
     // the rows' sums, through shared memory to the threads that write the rows: warps of the same 32 rows take half of the
     // columns each (the barrier comes first: no warp may miss it)
@@ -406,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     }
   } else if (warp < kIssueWarp) {
     // ---- fetch and convert ---------------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     constexpr int kLoads = D / 32;  // 16-byte loads of a thread per operand
     const uint32_t t = tid - kSoftThreads, cw = t >> 5;
     // A warp's load: 4 lanes on 64 values of a row, 8 rows. For D = 128 even warps take the rows' first 64 values.
@@ -451,25 +503,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     auto turn = [&](auto value_tag, uint32_t row_scale, uint32_t dst, const int8_t* src, const int64_t* off) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        uint2 x, y, z, u;
+        uint4 x = raw[i];
+        uint32_t f = 0;
+        if constexpr (decltype(value_tag)::value) f = __shfl_sync(~0u, row_scale, (first + i * 8 + sub) & 31);
+        uint2 y[4] = {fp16x4_of_int8(x.x), fp16x4_of_int8(x.y), fp16x4_of_int8(x.z), fp16x4_of_int8(x.w)};
         if constexpr (decltype(value_tag)::value) {
-          const uint32_t f = __shfl_sync(~0u, row_scale, (first + i * 8 + sub) & 31);
-          const uint32_t hi = __byte_perm(f, 0, 0x1010), lo = __byte_perm(f, 0, 0x3232);
-          x = fp16x4_of_int8(raw[i].x, hi, lo), y = fp16x4_of_int8(raw[i].y, hi, lo);
-          z = fp16x4_of_int8(raw[i].z, hi, lo), u = fp16x4_of_int8(raw[i].w, hi, lo);
-        } else {
-          x = bf16x4_of_int8(raw[i].x), y = bf16x4_of_int8(raw[i].y), z = bf16x4_of_int8(raw[i].z), u = bf16x4_of_int8(raw[i].w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = make_uint2(fp16x2_times(y[e].x, f), fp16x2_times(y[e].y, f));
         }
         raw[i] = fetch(src, off, i);
-        sts128(dst + write_at + i * 1024, make_uint4(x.x, x.y, y.x, y.y));  // row mod 8 is sub: swizzled(row, 2 * chunk)
-        sts128((dst + write_at + i * 1024) ^ 16u, make_uint4(z.x, z.y, u.x, u.y));
+        sts128(dst + write_at + i * 1024, make_uint4(y[0].x, y[0].y, y[1].x, y[1].y));  // row mod 8 is sub: swizzled(row, 2 * chunk)
+        sts128((dst + write_at + i * 1024) ^ 16u, make_uint4(y[2].x, y[2].y, y[3].x, y[3].y));
       }
       fence_smem();
       __syncwarp();
     };
     // Scales: a lane holds the two of one token of the warp's 32 (two warps share them; the even one publishes).
     const uint32_t own32 = (cw >> 1) * 32 + lane;
-    const float factor = a.scale * 1.44269504088896340736f;  // log2(e)
+    float factor = a.scale * 1.44269504088896340736f;  // log2(e); later with the queries' power of two
     float k_scale = 0.f, v_scale = 0.f;  // as loaded: nothing waits for them here
     auto fetch_scales = [&](uint32_t j, int32_t pages) {
       const int32_t p = __shfl_sync(~0u, pages, own32 >> 4);
@@ -488,6 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       for (int i = 0; i < kLoads; ++i) raw[i] = fetch(c.k, off, i);
       fetch_scales(0, pages);
     }
+    if (tiles && __all_sync(~0u, bar_wait(bars + kQFull, 0, stop)))
+      factor *= pow2i(max(-100, (int32_t)(lds32(base + L::misc + 8) >> 7) - 127) - 14);
     for (uint32_t j = 0; j < tiles; ++j) {
       const uint32_t buf = j & 1, use = j >> 1;
       pages = pages_of(j + 1);  // -1 behind the last tile: nothing is fetched for it
@@ -502,10 +555,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       const uint32_t e_v = max(__reduce_max_sync(~0u, __float_as_uint(fabsf(v))) >> 23, 1u);
       if ((cw & 1) == 0) {
         sts32(base + L::scale + (j & 3) * 512 + 4 * own32, bad ? 0x7FC00000u : __float_as_uint(k_scale * factor));
-        if (lane == 0) sts32(base + L::info + (j & 3) * 16 + 2 * cw, __float_as_uint((float)(int32_t)(e_v - 127)));
+        if (lane == 0) {
+          sts32(base + L::info + (j & 3) * 32 + 2 * cw, __float_as_uint((float)(int32_t)(e_v - 127)));
+          sts32(base + L::info + (j & 3) * 32 + 16 + 2 * cw, (254u - e_v) << 23);  // 2^-(e_v - 127)
+        }
       }
-      // the lane's scale in [0, 2) as fp16 and what that leaves over, packed
-      const uint32_t row_scale = split_fp16(v * __uint_as_float((254u - e_v) << 23));
+      const float in_range = v * __uint_as_float((254u - e_v) << 23);  // the lane's scale, in [0, 2)
+      const uint32_t row_scale = fp16_pack(in_range, in_range);
       turn(std::false_type{}, 0u, base + L::k + buf * L::kOperand, c.v, off);
       if (lane == 0) {
         bar_arrive(bars + kScaleFull + 8 * (j & 3));
@@ -518,27 +574,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if (lane == 0) bar_arrive(bars + kVFull + 8 * buf);
     }
   } else {
-    // ---- products: the warp runs the loop as one, an elected thread issues ------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == kIssueWarp && tiles) {
-      constexpr uint32_t kS = instr_desc(128, 128, true, false), kO = instr_desc(128, D, false, true);
+    // ---- products: a warp for each row tile runs the loop as one, an elected thread issues ---------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp < kIssueWarp + 2 && tiles) {
+      const uint32_t i = warp - kIssueWarp;
+      constexpr uint32_t kS = instr_desc(128, 64, false, false), kO = instr_desc(128, D, false, true);
       const bool lead = elect_one();
-      auto scores = [&](uint32_t i, uint32_t buf) {
-        const uint32_t q = smem_desc(base + L::q + i * L::kOperand, 16), k = smem_desc(base + L::k + buf * L::kOperand, 16);
+      // Both for the tokens 64 h .. 64 h + 63 of tile j.
+      auto scores = [&](uint32_t j, uint32_t h) {
+        const uint32_t q = smem_desc(base + L::q + i * L::kOperand, 16), k = smem_desc(base + L::k + (j & 1) * L::kOperand + h * 8192, 16);
+        const uint32_t d = tmem + 128 * i + 64 * ((j + h) & 1);
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) {
           const uint32_t off = ((e / 4) * kHalf + (e % 4) * 32) >> 4;
-          if (e == 0) mma_ss<false>(tmem + 128 * i, q + off, k + off, kS, lead);
-          else mma_ss<true>(tmem + 128 * i, q + off, k + off, kS, lead);
+          if (e == 0) mma_ss<false>(d, q + off, k + off, kS, lead);
+          else mma_ss<true>(d, q + off, k + off, kS, lead);
         }
-        commit(bars + kSFull + 8 * i, lead);
+        commit(bars + kSFull + 16 * i + 8 * h, lead);
       };
-      // tokens 64 h .. 64 h + 63 of the tile
-      auto values = [&](uint32_t i, uint32_t buf, uint32_t h, bool add) {
-        const uint32_t v = smem_desc(base + L::v + buf * L::kOperand, kHalf) + h * (4 * 2048 >> 4);
-        const uint32_t p = tmem + 128 * i + 32 * h;
+      auto values = [&](uint32_t j, uint32_t h) {
+        const uint32_t v = smem_desc(base + L::v + (j & 1) * L::kOperand, kHalf) + h * (4 * 2048 >> 4);
+        const uint32_t p = tmem + 128 * i + 64 * (j & 1) + 32 * h;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mma_ts(tmem + 256 + D * i, p + 8 * e, v + e * (2048 >> 4), kO, add || e > 0, lead);
+        for (int e = 0; e < 4; ++e) mma_ts(tmem + 256 + D * i, p + 8 * e, v + e * (2048 >> 4), kO, j > 0 || h > 0 || e > 0, lead);
         commit(bars + kOFull + 16 * i + 8 * h, lead);
       };
       auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(~0u, bar_wait(bars + bar, parity, stop)); };
@@ -546,36 +604,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if (ok) {
         fence_after();
         scores(0, 0);
-        scores(1, 0);
+        scores(0, 1);
         commit(bars + kKEmpty, lead);
       }
       for (uint32_t j = 0; ok && j < tiles; ++j) {
         const uint32_t buf = j & 1, nbuf = buf ^ 1;
         ok = wait(kVFull + 8 * buf, (j >> 1) & 1);
 #pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) {
-#pragma unroll
-          for (uint32_t h = 0; h < 2; ++h) {
-            ok = ok && wait(kPFull + 16 * i + 8 * h, j & 1);
-            if (!ok) break;
-            fence_after();
-            values(i, buf, h, j > 0 || h > 0);
-          }
+        for (uint32_t h = 0; h < 2; ++h) {
+          ok = ok && wait(kPFull + 16 * i + 8 * h, j & 1);
           if (!ok) break;
-          if (i == 1) commit(bars + kVEmpty + 8 * buf, lead);
+          fence_after();
+          values(j, h);
+          if (h == 1) commit(bars + kVEmpty + 8 * buf, lead);
           if (j + 1 < tiles) {
-            if (i == 0) ok = wait(kKFull + 8 * nbuf, ((j + 1) >> 1) & 1);
+            if (h == 0) ok = wait(kKFull + 8 * nbuf, ((j + 1) >> 1) & 1);
             if (!ok) break;
             fence_after();
-            scores(i, nbuf);
-            if (i == 1) commit(bars + kKEmpty + 8 * nbuf, lead);
+            scores(j + 1, h);
+            if (h == 1) commit(bars + kKEmpty + 8 * nbuf, lead);
           }
         }
       }
       if (!ok) {
         // gave up: let the products in flight end (again with a limit) before TMEM goes back
-        commit(bars + kDrain, lead);
-        for (uint32_t i = 0; i < kWaitTries && !bar_try(bars + kDrain, 0); ++i) {
+        commit(bars + kDrain + 8 * i, lead);
+        for (uint32_t n = 0; n < kWaitTries && !bar_try(bars + kDrain + 8 * i, 0); ++n) {
         }
       }
     }

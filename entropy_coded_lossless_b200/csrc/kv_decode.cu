@@ -34,13 +34,6 @@ __device__ __forceinline__ uint32_t transposed8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// two fp16 of 1024 + byte -> the signed bytes (their sign bits inverted before)
-__device__ __forceinline__ uint32_t minus1152(uint32_t t) {
-  uint32_t x;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(t), "r"(0x64806480u));
-  return x;
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_kernel(KvPages c, KvAttnArgs a, DecodePlan pl) {
   constexpr uint32_t kRows = 8 * NT;

@@ -145,16 +145,16 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// 8 bytes of shared memory that nothing writes while they are read. The compiler may place the load freely after what
+// Shared memory that nothing writes while they are read. The compiler may place the load freely after what
 // the address depends on; `after_here` makes an address depend on a place in the program (behind a wait).
 __device__ __forceinline__ uint32_t after_here(uint32_t a) {
   asm volatile("" : "+r"(a)::"memory");
   return a;
+}
+__device__ __forceinline__ float lds32_free(uint32_t a) {
+  float v;
+  asm("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
 }
 __device__ __forceinline__ uint64_t lds64_free(uint32_t a) {
   uint64_t v;
@@ -170,21 +170,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // 2^n, exactly, for a whole number n in [-126, 127]
 __device__ __forceinline__ float pow2(float n) { return __int_as_float(((int)n + 127) << 23); }
 
-// INT8 -> bf16, exactly. bf16 has 8 significant bits, so from 128 to 255 its step is 1: 0x4300 | m is 128 + m for a
-// 7-bit m, and 0x4380 is 256. With a byte x = m - 128 s (m its low 7 bits, s its sign bit), x = (128 + m) - (s ? 256 : 128)
-// = bf16(0x4300 | x & 0x7F) - bf16(0x4300 | x & 0x80): two bytes a time with one byte permute, two logic instructions
-// and one subtraction, none of which rounds.
-__device__ __forceinline__ uint32_t bf16x2_of_int8(uint32_t w, uint32_t sel) {
-  const uint32_t t = __byte_perm(w, 0x43434343u, sel);
-  const uint32_t a = t & 0xFF7FFF7Fu, b = t & 0xFF80FF80u;
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// the 4 bytes of w in order, as 2 x bf16x2
-__device__ __forceinline__ uint2 bf16x4_of_int8(uint32_t w) {
-  return make_uint2(bf16x2_of_int8(w, 0x4140), bf16x2_of_int8(w, 0x4342));
-}
+__device__ __forceinline__ float pow2i(int32_t n) { return __int_as_float((n + 127) << 23); }
 
 // (lo, hi) rounded to fp16, packed
 __device__ __forceinline__ uint32_t fp16_pack(float lo, float hi) {
@@ -192,25 +178,21 @@ __device__ __forceinline__ uint32_t fp16_pack(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// x as fp16 (low half) and what that leaves over, in fp16 (high half): x to about 22 bits where it is near 1
-__device__ __forceinline__ uint32_t split_fp16(float x) {
-  const __half hi = __float2half_rn(x);
-  const __half lo = __float2half_rn(x - __half2float(hi));
-  return (uint32_t)__half_as_ushort(hi) | (uint32_t)__half_as_ushort(lo) << 16;
-}
-// Two bytes times a scale hi + lo (each twice), rounded to fp16. 0x6400 | u is 1024 + u in fp16, u = x + 128: minus
-// 1152 that is x, exactly. x * lo is rounded far below fp16's last bit of x * hi, and the sum once.
-__device__ __forceinline__ uint32_t fp16x2_of_int8(uint32_t w, uint32_t sel, uint32_t hi, uint32_t lo) {
-  const uint32_t t = __byte_perm(w, 0x64646464u, sel);
-  uint32_t x, y, r;
+// Two fp16 of 1024 + u, u = x + 128 (a byte in the last bits of 0x6400), minus 1152: x, exactly.
+__device__ __forceinline__ uint32_t minus1152(uint32_t t) {
+  uint32_t x;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x) : "r"(t), "r"(0x64806480u));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(lo));
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(hi), "r"(y));
-  return r;
+  return x;
 }
-__device__ __forceinline__ uint2 fp16x4_of_int8(uint32_t w, uint32_t hi, uint32_t lo) {
+// The 4 bytes of w in order, as 2 x fp16x2, exactly.
+__device__ __forceinline__ uint2 fp16x4_of_int8(uint32_t w) {
   w ^= 0x80808080u;
-  return make_uint2(fp16x2_of_int8(w, 0x4140, hi, lo), fp16x2_of_int8(w, 0x4342, hi, lo));
+  return make_uint2(minus1152(__byte_perm(w, 0x64646464u, 0x4140)), minus1152(__byte_perm(w, 0x64646464u, 0x4342)));
+}
+__device__ __forceinline__ uint32_t fp16x2_times(uint32_t x, uint32_t f) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(f));
+  return r;
 }
 
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
