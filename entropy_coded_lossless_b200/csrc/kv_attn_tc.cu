@@ -67,8 +67,10 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
   const uint32_t run = (a.n_reqs + kThreads - 1) / kThreads;
   const uint32_t r0 = min(a.n_reqs, t * run), r1 = min(a.n_reqs, r0 + run);
   uint32_t own = 0;
+  int32_t kv_len = 0;  // of the run's last request: with up to kThreads requests the one that is meant
   for (uint32_t r = r0; r < r1; ++r) {
     const int32_t b = a.cu_q[r], e = a.cu_q[r + 1];
+    kv_len = a.kv_len[r];
     if (b < 0 || e < b || (uint32_t)e > a.n_tokens) report(a.st, SHN_ERR_INVALID_ARG, r);
     else own += ((uint32_t)(e - b) * group + kRows - 1) / kRows;
   }
@@ -98,8 +100,11 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
       if (b < 0 || e < b || (uint32_t)e > a.n_tokens) continue;
       const uint32_t n = ((uint32_t)(e - b) * group + kRows - 1) / kRows;
       if (left < n) {
+        scan[28] = (uint32_t)b;
+        scan[29] = (uint32_t)(e - b);
         scan[30] = r;
         scan[31] = left;
+        scan[32] = (uint32_t)(run == 1 ? kv_len : a.kv_len[r]);
         break;
       }
       left -= n;
@@ -109,11 +114,11 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
   w.req = scan[30];
   if (w.req >= a.n_reqs) return false;
   w.row0 = scan[31] * kRows;
-  w.q0 = a.cu_q[w.req];
-  w.nq = a.cu_q[w.req + 1] - w.q0;
+  w.q0 = (int32_t)scan[28];
+  w.nq = (int32_t)scan[29];
   w.rows = (uint32_t)w.nq * group;
   const int64_t holds = (int64_t)a.max_blocks << c.log2_pt;
-  int32_t len = a.kv_len[w.req];
+  int32_t len = (int32_t)scan[32];
   if (len < 0 || len > holds) {
     if (t == 0) report(a.st, SHN_ERR_INVALID_ARG, w.req);
     len = len < 0 ? 0 : (int32_t)holds;
@@ -149,11 +154,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
 
   after_previous();
   let_next();
-  // after a wait that gave up the call has failed: the other blocks do not start on it
-  if (__syncthreads_or(*reinterpret_cast<volatile uint32_t*>(&a.st->status) == SHN_ERR_TIMEOUT)) return;
+  const uint32_t status = *reinterpret_cast<volatile uint32_t*>(&a.st->status);
   Work w;
   if constexpr (kPart) find_part(c, a, pl, group, w);
   else if (!find_work(c, a, group, blockIdx.x / c.kv_heads, reinterpret_cast<uint32_t*>(smem + L::scan), w)) return;
+  // after a wait that gave up the call has failed: the other blocks do not start on it
+  if (__syncthreads_or(status == SHN_ERR_TIMEOUT)) return;
   const uint32_t rows_here = min(kRows, w.rows - w.row0);
   // tokens the block's last row sees; every row of the block sees at most as many
   const int32_t shift = w.len - w.nq + 1;  // query i sees shift + i tokens
@@ -341,9 +347,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
             }
           }
         };
-        if (edge) weights(std::true_type{});
-        else weights(std::false_type{});
-        if (__any_sync(~0u, sum[0] > limit[0] || sum[1] > limit[1]) || (larger && h == 0)) {
+        bool rise = j == 0 && h == 0;  // there is no reference yet
+        if (!rise) {
+          if (edge) weights(std::true_type{});
+          else weights(std::false_type{});
+          rise = __any_sync(~0u, sum[0] > limit[0] || sum[1] > limit[1]) || (larger && h == 0);
+        }
+        if (rise) {
           // the reference rises to the row's maximum of this half: what is summed is scaled down, and the weights formed again
           float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
