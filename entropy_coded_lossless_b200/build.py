@@ -1,4 +1,5 @@
-"""Build libshn.so (the CUDA kernels + C ABI) in-tree for sm_100a with nvcc.
+"""Build libshn.so (the CUDA kernels + C ABI) in-tree for sm_100a with nvcc, and _kv.so (the Python calls of the paged
+KV cache over it) with g++.
 
     python -m entropy_coded_lossless_b200.build [--force]
 """
@@ -16,6 +17,7 @@ HEADERS = [os.path.join(CSRC, "shn_internal.cuh"), os.path.join(ROOT, "include",
 # the paged KV cache's sources (kv_*.cu) alone include these
 KV_HEADERS = [os.path.join(CSRC, "kv_internal.cuh"), os.path.join(CSRC, "kv_tc.cuh"),
               os.path.join(CSRC, "kv_decode.cuh"), os.path.join(ROOT, "include", "shn_kv.h")]
+BINDING = os.path.join(HERE, "_kv.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
@@ -29,6 +31,32 @@ def _stale(target, deps):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    lib = build_lib(force, verbose)
+    build_binding(force, verbose)
+    return lib
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "kv_binding.cpp")
+    if not force and not _stale(BINDING, [src, os.path.join(ROOT, "include", "shn_kv.h"), os.path.join(ROOT, "include", "shn.h")]):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    libs = [os.path.join(os.path.dirname(torch.__file__), "lib")]
+    includes = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for i in includes for a in ("-isystem", i)], src, "-o", BINDING, f"-L{HERE}", "-l:libshn.so", *[f"-L{d}" for d in libs], "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.check_call(cmd)
+    return BINDING
+
+
+def build_lib(force: bool = False, verbose: bool = False) -> str:
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     if not force and not _stale(LIB, srcs + HEADERS + KV_HEADERS):
         return LIB

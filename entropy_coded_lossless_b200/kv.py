@@ -1,4 +1,5 @@
-"""ctypes binding of the paged INT8 KV cache (include/shn_kv.h) — argument marshalling only.
+"""Binding of the paged INT8 KV cache (include/shn_kv.h) — tensor checks and argument marshalling only, the calls' in
+csrc/kv_binding.cpp (a small batch's kernels take microseconds, and so must what comes before them).
 
 Plan (block tables and slots from request lengths), store (norm, rotation, quantisation into the pages),
 load (rows as bf16) and attention over the pages, for packed prompts and for single tokens that share a prefix:
@@ -23,8 +24,12 @@ import torch
 from . import shn
 from .shn import ShnError, _check  # noqa: F401  (ShnError: what the calls raise)
 
+try:
+    from . import _kv
+except ImportError as e:  # pragma: no cover - not built
+    raise ImportError(f"_kv.so not built beside this file ({e}); run python -m entropy_coded_lossless_b200.build") from e
+
 WORKSPACE_BYTES = 256
-_I32, _BF16 = torch.int32, torch.bfloat16
 
 
 class _CacheStruct(ctypes.Structure):
@@ -60,26 +65,6 @@ def _lib():
     return _bound
 
 
-class _on:
-    """The device of a call made current around it, where it is not, and the stream the call runs on."""
-
-    __slots__ = ("device", "guard", "stream")
-
-    def __init__(self, device, stream):
-        self.device = device
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.stream = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
-
-
 def _dev(t, name, dtype, device, shape=None):
     """Device address of a contiguous tensor of this type on this device (shape: what it must be, where given)."""
     if not isinstance(t, torch.Tensor) or t.device != device:
@@ -91,32 +76,6 @@ def _dev(t, name, dtype, device, shape=None):
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     return t.data_ptr()
-
-
-def _rows(t, name, device, head_dim, heads=None, tokens=None):
-    """Address and token stride of bf16 rows [tokens, heads, head_dim] whose heads are contiguous."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != _BF16 or t.dim() != 3:
-        raise ValueError(f"{name} must be bfloat16 [tokens, heads, head_dim]")
-    n, h, d = t.shape
-    if d != head_dim or (heads is not None and h != heads) or (tokens is not None and n != tokens):
-        raise ValueError(f"{name} has the shape {tuple(t.shape)}; expected [{'tokens' if tokens is None else tokens}, "
-                         f"{'heads' if heads is None else heads}, {head_dim}]")
-    st, sh, sd = t.stride()
-    if (d > 1 and sd != 1) or (h > 1 and sh != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if n <= 1:
-        st = h * d  # the stride of a single token means nothing
-    if st < 0 or (n > 1 and st < h * d):
-        raise ValueError(f"{name}: tokens overlap")
-    return t.data_ptr(), st
-
-
-def _work(t, device):
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.uint8 or not t.is_contiguous():
-        raise ValueError(f"work must be a contiguous uint8 tensor on {device}")
-    return t.data_ptr(), t.numel()
 
 
 def _device(t, name):
@@ -151,6 +110,7 @@ class Cache:
                               _dev(v_scale, "v_scale", torch.float32, self.device, shape[:3]), pages, heads, page_tokens,
                               head_dim)
         _check(_lib().shn_kv_check_cache(ctypes.byref(self.c)), "shn_kv_check_cache")
+        self.handle = ctypes.addressof(self.c), self.device.index  # what the calls take (self.c lives as long as this)
 
     @classmethod
     def empty(cls, n_pages, kv_heads, page_tokens, head_dim, device="cuda"):
@@ -174,79 +134,38 @@ class Cache:
 # the calls, one-to-one with the C ABI
 
 
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
+
+
 def shn_kv_plan(ctx_len, new_len, page_tokens, block_table, free_pages, free_head, free_next, cu_new, kv_len, positions,
                 slots, work, stream=None):
-    dev = _device(ctx_len, "ctx_len")
-    n = ctx_len.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != n:
-        raise ValueError(f"block_table must be [{n}, max_blocks]")
-    if positions.shape != slots.shape:
-        raise ValueError("positions and slots must have the same length")
-    w, nw = _work(work, dev)
-    with _on(dev, stream) as s:
-        _check(_lib().shn_kv_plan(
-            _dev(ctx_len, "ctx_len", _I32, dev, (n,)), _dev(new_len, "new_len", _I32, dev, (n,)), n, page_tokens,
-            _dev(block_table, "block_table", _I32, dev), block_table.shape[1], _dev(free_pages, "free_pages", _I32, dev),
-            free_pages.numel(), _dev(free_head, "free_head", _I32, dev, (1,)), _dev(free_next, "free_next", _I32, dev, (1,)),
-            _dev(cu_new, "cu_new", _I32, dev, (n + 1,)), _dev(kv_len, "kv_len", _I32, dev, (n,)),
-            _dev(positions, "positions", _I32, dev), _dev(slots, "slots", _I32, dev), slots.numel(), w, nw, s), "shn_kv_plan")
+    code = _kv.plan(ctx_len, new_len, page_tokens, block_table, free_pages, free_head, free_next, cu_new, kv_len,
+                    positions, slots, work, _raw(stream))
+    if code:
+        raise ShnError(code, "shn_kv_plan")
 
 
 def shn_kv_store(q, k, v, positions, slots, cache, q_out, work, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None,
                  pairs=False, stream=None):
     """q and q_out may be None (keys and values only); positions may be None without cos_sin."""
-    dev, d, hk, c = cache.device, cache.head_dim, cache.kv_heads, cache.c
-    kp, ks = _rows(k, "k", dev, d, hk)
-    n = k.shape[0]
-    vp, vs = _rows(v, "v", dev, d, hk, n)
-    qp, qs, op, os_, h = None, 0, None, 0, 0
-    if q is not None:
-        qp, qs = _rows(q, "q", dev, d, tokens=n)
-        h = q.shape[1]
-        op, os_ = _rows(q_out, "q_out", dev, d, h, n)
-    if cos_sin is not None and cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [positions, rot_dim]")
-    w, nw = _work(work, dev)
-    with _on(dev, stream) as s:
-        _check(_lib().shn_kv_store(
-            qp, qs, h, kp, ks, vp, vs, n, None if positions is None else _dev(positions, "positions", _I32, dev, (n,)),
-            _dev(slots, "slots", _I32, dev, (n,)), None if q_weight is None else _dev(q_weight, "q_weight", _BF16, dev, (d,)),
-            None if k_weight is None else _dev(k_weight, "k_weight", _BF16, dev, (d,)), eps,
-            None if cos_sin is None else _dev(cos_sin, "cos_sin", torch.float32, dev),
-            0 if cos_sin is None else cos_sin.shape[0], 0 if cos_sin is None else cos_sin.shape[1], int(bool(pairs)),
-            ctypes.byref(c), op, os_, w, nw, s), "shn_kv_store")
+    code = _kv.store(*cache.handle, q, k, v, positions, slots, q_out, work, q_weight, k_weight, eps, cos_sin, pairs,
+                     _raw(stream))
+    if code:
+        raise ShnError(code, "shn_kv_store")
 
 
 def shn_kv_load(cache, slots, k_out, v_out, work, stream=None):
     """k_out or v_out may be None."""
-    dev, d, hk = cache.device, cache.head_dim, cache.kv_heads
-    n = slots.numel()
-    kp, ks = (None, 0) if k_out is None else _rows(k_out, "k_out", dev, d, hk, n)
-    vp, vs = (None, 0) if v_out is None else _rows(v_out, "v_out", dev, d, hk, n)
-    w, nw = _work(work, dev)
-    with _on(dev, stream) as s:
-        _check(_lib().shn_kv_load(ctypes.byref(cache.c), _dev(slots, "slots", _I32, dev), n, kp, ks, vp, vs, w, nw, s),
-               "shn_kv_load")
-
-
-def _attn(q, cache, block_table, kv_len, out):
-    dev, d = cache.device, cache.head_dim
-    qp, qs = _rows(q, "q", dev, d)
-    n, h = q.shape[:2]
-    op, os_ = _rows(out, "out", dev, d, h, n)
-    b = kv_len.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != b:
-        raise ValueError(f"block_table must be [{b}, max_blocks]")
-    return dev, qp, qs, n, h, op, os_, b, _dev(block_table, "block_table", _I32, dev), _dev(kv_len, "kv_len", _I32, dev)
+    code = _kv.load(*cache.handle, slots, k_out, v_out, work, _raw(stream))
+    if code:
+        raise ShnError(code, "shn_kv_load")
 
 
 def shn_kv_attn_prompt(q, cache, block_table, cu_q, kv_len, scale, out, work, stream=None):
-    dev, qp, qs, n, h, op, os_, b, tp, lp = _attn(q, cache, block_table, kv_len, out)
-    w, nw = _work(work, dev)
-    with _on(dev, stream) as s:
-        _check(_lib().shn_kv_attn_prompt(qp, qs, n, h, ctypes.byref(cache.c), tp, block_table.shape[1],
-                                         _dev(cu_q, "cu_q", _I32, dev, (b + 1,)), lp, b, scale, op, os_, w, nw, s),
-               "shn_kv_attn_prompt")
+    code = _kv.attn_prompt(*cache.handle, q, block_table, cu_q, kv_len, scale, out, work, _raw(stream))
+    if code:
+        raise ShnError(code, "shn_kv_attn_prompt")
 
 
 def attn_shared_workspace_bytes(cache, n_reqs: int, q_heads: int) -> int:
@@ -255,13 +174,6 @@ def attn_shared_workspace_bytes(cache, n_reqs: int, q_heads: int) -> int:
 
 def shn_kv_attn_shared(q, cache, prefix_pages, prefix_len, block_table, kv_len, scale, out, work, stream=None):
     """q, out: [requests, heads, head_dim]. prefix_pages may be None (then prefix_len holds 0)."""
-    dev, qp, qs, n, h, op, os_, b, tp, lp = _attn(q, cache, block_table, kv_len, out)
-    if n != b:
-        raise ValueError(f"q has {n} queries for {b} requests")
-    w, nw = _work(work, dev)
-    with _on(dev, stream) as s:
-        _check(_lib().shn_kv_attn_shared(qp, qs, n, h, ctypes.byref(cache.c),
-                                         None if prefix_pages is None else _dev(prefix_pages, "prefix_pages", _I32, dev),
-                                         0 if prefix_pages is None else prefix_pages.numel(),
-                                         _dev(prefix_len, "prefix_len", _I32, dev, (1,)), tp, block_table.shape[1], lp,
-                                         scale, op, os_, w, nw, s), "shn_kv_attn_shared")
+    code = _kv.attn_shared(*cache.handle, q, prefix_pages, prefix_len, block_table, kv_len, scale, out, work, _raw(stream))
+    if code:
+        raise ShnError(code, "shn_kv_attn_shared")
