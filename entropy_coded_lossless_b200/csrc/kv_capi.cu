@@ -19,7 +19,7 @@ constexpr uint32_t kMaxGroup = 64;
 
 int check_cache(const shn_kv_cache* c) {
   if (!c || !c->d_k || !c->d_v || !c->d_k_scale || !c->d_v_scale) return SHN_ERR_INVALID_ARG;
-  if (!aligned(c->d_k, 16) || !aligned(c->d_v, 16) || !aligned(c->d_k_scale, 4) || !aligned(c->d_v_scale, 4))
+  if (!aligned(c->d_k, 16) || !aligned(c->d_v, 16) || !aligned(c->d_k_scale, 16) || !aligned(c->d_v_scale, 16))
     return SHN_ERR_INVALID_ARG;
   if (c->n_pages == 0 || c->kv_heads == 0 || c->kv_heads > 1024) return SHN_ERR_INVALID_ARG;
   if (!power_of_two(c->page_tokens) || c->page_tokens < 16 || c->page_tokens > 1024) return SHN_ERR_INVALID_ARG;
@@ -183,8 +183,7 @@ int shn_kv_load(const shn_kv_cache* cache, const int32_t* d_slots, uint32_t n_to
   a.st = clear_status(d_work, s);
   if (!a.st) return SHN_ERR_CUDA;
   if (n_tokens == 0 || (!d_k_out && !d_v_out)) return SHN_OK;
-  return launch_kv_load(pages_of(cache), cache->head_dim, a, sm_count_for_launch(), s) == cudaSuccess ? SHN_OK
-                                                                                                      : SHN_ERR_CUDA;
+  return launch_kv_load(pages_of(cache), cache->head_dim, a, s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
 }
 
 int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32_t q_heads,

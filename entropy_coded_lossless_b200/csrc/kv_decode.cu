@@ -1,10 +1,10 @@
 // kv_decode.cu — attention of single tokens over the paged INT8 cache, with a prefix that the requests share
 // (shn_kv_attn_shared).
 //
-// Bound by reading the cache: a token's keys and values of one key head are 2 (head_dim + 4) bytes, used by few rows. So
-// bytes go from global memory straight into the registers that feed mma.sync, no shared memory between: with the
-// order of the contracted dimension free (as long as both operands agree) a lane's 16 consecutive bytes are its
-// operands of several steps. Rows are the narrow side:
+// Bound by reading the cache: a token's keys and values of one key head are 2 (head_dim + 4) bytes, used by few rows. Each
+// warp brings its own 16 tokens a step through a ring of stages in shared memory with cp.async, the next steps on their
+// way while one is worked on, and no warp waits for another. With the order of the contracted dimension free (as long as
+// both operands agree) a lane's 16 consecutive bytes are its operands of several mma.sync steps. Rows are the narrow side:
 //   S' = K Q'   m16 (tokens) n8 (query rows) k16, 16 tokens a step
 //   O' = V' P'  m16 (values of a head) n8 (query rows) k16 (the 16 tokens); P' is S' transposed by movmatrix
 // INT8 enters as fp16, exactly (1024 + u with u = x + 128 is a byte put into fp16's last bits; minus 1152 it is x). A query row
@@ -34,10 +34,27 @@ __device__ __forceinline__ uint32_t transposed8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
+// A warp's ring: stages of 16 tokens' keys, values and scales; two blocks of 8 warps to an SM.
+template <int D>
+struct Ring {
+  static constexpr uint32_t kStages = D == 128 ? 3 : 6, kStage = 32 * D + 128, kBytes = kDecodeThreads / 32 * kStages * kStage;
+};
+// What a row's chunk numbers are XORed with. Rows of 128 bytes: the 8 lanes that read at a time have rows g, g + 1 and 4
+// chunks of keys (the lowest bit of the row moves them to the other half), or rows 2 cc and chunks g, g + 1 of values (the
+// other bits spread them). Rows of 64 bytes lie in pairs; only values meet a bank twice there.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_swap(uint32_t tok) {
+  return D == 128 ? (tok & 2) | (((tok >> 2) ^ tok) & 1) << 2 : tok >> 1 & 3;
+}
+__device__ __forceinline__ void cp16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_kernel(KvPages c, KvAttnArgs a, DecodePlan pl) {
   constexpr uint32_t kRows = 8 * NT;
   constexpr int kKLoads = D / 64;  // 16-byte loads of a token's keys per lane
+  constexpr uint32_t kStages = Ring<D>::kStages, kStage = Ring<D>::kStage;
   __shared__ UnitScan scan;
   const uint32_t lane = threadIdx.x & 31, g = lane >> 2, cc = lane & 3;
   const uint32_t w = blockIdx.x * (kDecodeThreads / 32) + (threadIdx.x >> 5);
@@ -89,7 +106,9 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
     }
   }
   const float log2e_scale = a.scale * 1.44269504088896340736f;
-  const uint32_t lane_k = g * D + cc * 16, lane_v = 2 * cc * D + g * (D / 8);
+  extern __shared__ __align__(128) uint8_t stages[];
+  const uint32_t ring = smem_addr(stages) + (threadIdx.x >> 5) * kStages * kStage;
+  uint32_t stage = 0;
 
   while (u < u_end) {
     // ---- a piece: units [u, piece_end) of one segment ----
@@ -104,66 +123,43 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
     const int32_t t_from = own ? prefix : 0;
     const int32_t* pages = own ? a.table + (uint64_t)r * a.max_blocks : a.prefix_pages;
 
-    // 16 tokens a step: where their keys and values lie, and whether there is a page (warp-uniform)
-    auto row_of = [&](uint32_t t, uint64_t& row) -> bool {
-      if (t >= t_last) return false;
-      const int32_t p = __ldg(pages + (t >> c.log2_pt));
+    // 16 tokens a step: the row of the first in the cache, ~0 where there is none (warp-uniform)
+    auto page_of = [&](uint32_t t) -> int32_t { return t < t_last ? __ldg(pages + (t >> c.log2_pt)) : -1; };
+    auto row_of = [&](uint32_t t, int32_t p) -> uint64_t {
+      if (t >= t_last) return ~0ull;
       if (p < 0 || (uint32_t)p >= c.n_pages) {
         if (lane == 0) report(a.st, SHN_ERR_INVALID_ARG, r);
-        return false;
+        return ~0ull;
       }
-      row = kv_row(c, (uint32_t)p, hk, t & ((1u << c.log2_pt) - 1));
-      return true;
+      return kv_row(c, (uint32_t)p, hk, t & ((1u << c.log2_pt) - 1));
     };
-    uint4 kr[2][kKLoads];    // tokens g, g + 8
-    uint32_t vr[4][D / 32];  // tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9: D/8 bytes at g D/8
-    float ks[2], vs[2];
-    auto load_k = [&](bool is, uint64_t row) {
-      if (is) {
-        const int8_t* src = c.k + row * D + lane_k;
-        const float *k_scale = c.k_scale + row + g, *v_scale = c.v_scale + row + g;
+    // One step into a stage: rows in order, the 16-byte chunks of a row exchanged so that the lanes of a fragment load meet no
+    // bank twice. Where there is no page the bytes stay what they were and the scales are zeros: scores of 0, values of 0.
+    auto fetch = [&](uint32_t stage, uint64_t row) {
+      const uint32_t at = ring + stage * kStage;
+      if (row != ~0ull) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int h = 0; h < kKLoads; ++h) kr[i][h] = __ldg(reinterpret_cast<const uint4*>(src + 8 * i * D + h * 64));
-          ks[i] = __ldg(k_scale + 8 * i);
-          vs[i] = __ldg(v_scale + 8 * i);
+        for (int i = 0; i < D / 32; ++i) {
+          const uint32_t x = i * 32 + lane, tok = x / (D / 16), chunk = x % (D / 16);
+          const uint32_t to = tok * D + ((chunk ^ chunk_swap<D>(tok)) << 4);
+          cp16(at + to, c.k + row * D + x * 16);
+          cp16(at + 16 * D + to, c.v + row * D + x * 16);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int h = 0; h < kKLoads; ++h) kr[i][h] = make_uint4(0, 0, 0, 0);
-          ks[i] = vs[i] = 0.f;
-        }
+        if (lane < 8) cp16(at + 32 * D + lane * 16, (lane < 4 ? c.k_scale : c.v_scale) + row + (lane & 3) * 4);
+      } else if (lane < 8) {
+        sts128(at + 32 * D + lane * 16, make_uint4(0, 0, 0, 0));
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto load_v = [&](bool is, uint64_t row) {
-      if (is) {
-        const int8_t* src = c.v + row * D + lane_v;
+    int32_t page_next;
+    {
+      int32_t first_pages[kStages];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int8_t* at = src + ((i & 1) + 8 * (i >> 1)) * D;
-          if constexpr (D == 128) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
-            vr[i][0] = x.x, vr[i][1] = x.y, vr[i][D / 32 - 2] = x.z, vr[i][D / 32 - 1] = x.w;
-          } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
-            vr[i][0] = x.x, vr[i][1] = x.y;
-          }
-        }
-      } else {
+      for (int i = 0; i < kStages; ++i) first_pages[i] = page_of(t_first + 16 * i);
+      page_next = first_pages[kStages - 1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int h = 0; h < D / 32; ++h) vr[i][h] = 0;
-      }
-    };
-    uint64_t row_now = 0, row_next = 0;
-    const bool is_now = row_of(t_first, row_now);
-    bool is_next = row_of(t_first + 16, row_next);
-    load_k(is_now, row_now);
-    load_v(is_now, row_now);
+      for (int i = 0; i < kStages - 1; ++i) fetch((stage + i) % kStages, row_of(t_first + 16 * i, first_pages[i]));
+    }
 
     // queries: B operands. Lane (g, cc) holds row g's values 16 cc + 4 k + j (and 64 + ...) for step k
     uint32_t qb[NT][D / 16][2];
@@ -227,32 +223,46 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
 
 #pragma unroll 1
     for (uint32_t t = t_first; t < t_last; t += 16) {
-      uint64_t row_after = 0;
-      const bool is_after = row_of(t + 32, row_after);
+      // the step kStages - 1 ahead into the stage that the last step left
+      const uint32_t ahead = t + 16 * (kStages - 1);
+      fetch((stage + kStages - 1) % kStages, row_of(ahead, page_next));
+      page_next = page_of(ahead + 16);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      const uint32_t at = ring + stage * kStage;
       float s[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
       // keys of tokens g, g + 8 -> scores
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t af[4];
+      for (int h = 0; h < kKLoads; ++h) {
+        uint4 x[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 x = kr[i][k / 4];
-          const uint32_t wd = ((k & 3) == 0 ? x.x : (k & 3) == 1 ? x.y : (k & 3) == 2 ? x.z : x.w) ^ 0x80808080u;
-          af[i] = minus1152(__byte_perm(wd, 0x64646464u, 0x4140));
-          af[i + 2] = minus1152(__byte_perm(wd, 0x64646464u, 0x4342));
+        for (int i = 0; i < 2; ++i) x[i] = lds128(at + (g + 8 * i) * D + (((h * 4 + cc) ^ chunk_swap<D>(g + 8 * i)) << 4));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t af[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t wd = (k == 0 ? x[i].x : k == 1 ? x[i].y : k == 2 ? x[i].z : x[i].w) ^ 0x80808080u;
+            af[i] = minus1152(__byte_perm(wd, 0x64646464u, 0x4140));
+            af[i + 2] = minus1152(__byte_perm(wd, 0x64646464u, 0x4342));
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], af, qb[nt][h * 4 + k][0], qb[nt][h * 4 + k][1]);
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], af, qb[nt][k][0], qb[nt][k][1]);
       }
-      float vs_now[2] = {vs[0], vs[1]};
+      float ks[2], vs_now[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ks[i] = __uint_as_float(lds32(at + 32 * D + 4 * (g + 8 * i)));
+        vs_now[i] = __uint_as_float(lds32(at + 32 * D + 64 + 4 * (g + 8 * i)));
+      }
       // scores -> x: s[2 i + e] is token g + 8 i, query column 2 cc + e
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[nt][i] *= ks[i >> 1] * mul[nt][i & 1];
-      load_k(is_next, row_next);
       const bool edge = (int32_t)t < t_from || (int32_t)t + 16 > full_to;
       if (edge) {
 #pragma unroll
@@ -329,6 +339,19 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
       if (edge) weights(std::true_type{});
       else weights(std::false_type{});
       // values -> sums: a lane's bytes are values g D/8 + 2k, + 1 of step k, for tokens 2 cc, 2 cc + 1 (and + 8, + 9)
+      uint32_t vr[4][D / 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t tok = 2 * cc + (i & 1) + 8 * (i >> 1), byte = g * (D / 8);
+        const uint32_t from = at + 16 * D + tok * D + ((((byte >> 4) ^ chunk_swap<D>(tok)) << 4) | (byte & 15));
+        if constexpr (D == 128) {
+          const uint4 x = lds128(from);
+          vr[i][0] = x.x, vr[i][1] = x.y, vr[i][D / 32 - 2] = x.z, vr[i][D / 32 - 1] = x.w;
+        } else {
+          const uint2 x = lds64(from);
+          vr[i][0] = x.x, vr[i][1] = x.y;
+        }
+      }
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         uint32_t af[4];
@@ -345,9 +368,11 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][k], af, pb[nt][0], pb[nt][1]);
       }
-      load_v(is_next, row_next);
-      row_next = row_after, is_next = is_after;
+      __syncwarp();  // the stage is read: the next turn may fill it
+      stage = (stage + 1) % kStages;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // (what was fetched ahead of the end is nothing)
+    __syncwarp();
 
     // ---- the piece's result ----
     const uint32_t seg = own ? prefix_segs + r * seg_per_req + sub : sub;
@@ -521,8 +546,11 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
 template <int D>
 cudaError_t launch(const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s) {
   const dim3 blocks(pl.warps / (kDecodeThreads / 32));
-  const cudaError_t e = pl.rows == 8 ? launch_behind(kv_decode_kernel<D, 1>, blocks, kDecodeThreads, 0, s, c, a, pl)
-                                     : launch_behind(kv_decode_kernel<D, 2>, blocks, kDecodeThreads, 0, s, c, a, pl);
+  cudaError_t e = cudaFuncSetAttribute(pl.rows == 8 ? kv_decode_kernel<D, 1> : kv_decode_kernel<D, 2>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  e = pl.rows == 8 ? launch_behind(kv_decode_kernel<D, 1>, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl)
+                   : launch_behind(kv_decode_kernel<D, 2>, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl);
   if (e != cudaSuccess) return e;
   // few rows may have hundreds of pieces each: as many warps to a row as fill the warps that ran before, 8 at most
   const uint32_t items = a.n_reqs * a.q_heads;

@@ -91,7 +91,7 @@ struct KvLoadArgs {
   uint64_t k_stride, v_stride;
   DeviceStatus* st;
 };
-cudaError_t launch_kv_load(const KvPages& c, uint32_t head_dim, const KvLoadArgs& a, int sm_count, cudaStream_t s);
+cudaError_t launch_kv_load(const KvPages& c, uint32_t head_dim, const KvLoadArgs& a, cudaStream_t s);
 
 // Both attention calls. cu_q is null for single tokens (request r has query r).
 struct KvAttnArgs {

@@ -2,9 +2,10 @@
 //
 // Two exclusive sums over the requests (new tokens; pages to take), then one independent item per new
 // token and per new page, each finding its request by a search in the sums. Little is read or written
-// (about 16 bytes per request and 8 per token), so the call is bound by latency: one launch, and one
-// cluster of up to 8 blocks so that a barrier can separate the reading of the free-list head from its
-// update. Every block forms the sums for itself, which costs less than handing them around.
+// (about 16 bytes per request and 8 per token), so the call is bound by latency. Every block forms the sums
+// for itself, which costs less than handing them around, and takes a token per thread. A step that one block
+// covers is one launch; for more a small kernel in front keeps the free-list head as it was before the call, since
+// the caller may have it updated in place.
 #include "kv_internal.cuh"
 
 namespace shn {
@@ -20,16 +21,24 @@ __device__ __forceinline__ long long pages_of(long long tokens, uint32_t log2_pt
   return (tokens + (1ll << log2_pt) - 1) >> log2_pt;
 }
 
+// Clears the status and keeps the head (behind the status word) for the kernel that follows.
+__global__ void kv_plan_begin_kernel(KvPlanArgs a) {
+  let_next();
+  if (threadIdx.x == 0) a.st->status = 0, a.st->detail = 0, reinterpret_cast<int32_t*>(a.st)[2] = *a.free_head;
+}
+
+template <bool kOne>  // one block, no kernel in front
 __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
   __shared__ Sum2 before[kThreads + 1];  // sums in front of each thread's run of requests
   __shared__ Sum2 warp_sum[32];
   __shared__ uint32_t bad_code, bad_detail;
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const uint32_t rank = blockIdx.x, ranks = gridDim.x;  // one cluster: its blocks are the grid
+  const uint32_t rank = blockIdx.x, ranks = gridDim.x;
   const uint32_t run = (a.n + kThreads - 1) / kThreads;
   const uint32_t r0 = min(a.n, t * run), r1 = min(a.n, r0 + run);
   if (t == 0) bad_code = 0, bad_detail = 0xFFFFFFFFu;
-  const long long head = *a.free_head;
+  long long head = 0;
+  if constexpr (kOne) head = *a.free_head;
   __syncthreads();
 
   Sum2 own = {0, 0};
@@ -73,15 +82,22 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
   __syncthreads();
   const Sum2 total = before[kThreads];
 
+  if constexpr (!kOne) {
+    after_previous();
+    head = reinterpret_cast<const volatile int32_t*>(a.st)[2];
+  }
   uint32_t code = bad_code == 2 ? SHN_ERR_INVALID_ARG : bad_code == 1 ? SHN_ERR_CAPACITY : SHN_OK;
   uint32_t detail = code ? bad_detail : 0;
   if (code == SHN_OK && (head < 0 || head > (long long)a.n_free)) code = SHN_ERR_INVALID_ARG;
   if (code == SHN_OK && (total.tokens > (long long)a.max_tokens || head + total.pages > (long long)a.n_free))
     code = SHN_ERR_CAPACITY;
   const bool ok = code == SHN_OK;
-  if (rank == 0 && t == 0) a.st->status = code, a.st->detail = detail;
-  // every block has read the head (and the first has set the status) before anything is written
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  if constexpr (kOne) {
+    if (t == 0) a.st->status = code, a.st->detail = detail;
+    __syncthreads();  // the head is read and the status set before anything is written
+  } else if (rank == 0 && t == 0 && code) {
+    report(a.st, code, detail);
+  }
   if (rank == 0 && t == 0) {
     *a.free_next = (int32_t)(ok ? head + total.pages : head);
     a.cu[a.n] = (int32_t)(ok ? total.tokens : 0);
@@ -149,21 +165,16 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t s) {
-  // a block per 4096 tokens (4 per thread) until the cluster's 8: below that a second block's start costs more
-  // than the tokens it takes over
-  uint32_t ranks = 1;
-  while (ranks < 8 && ranks * 4096ull < a.max_tokens) ranks *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ranks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ranks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_plan_kernel, a);
+  // one block up to 2 tokens a thread: a second launch costs about what they do
+  if (a.max_tokens <= 2 * kThreads) {
+    kv_plan_kernel<true><<<1, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  kv_plan_begin_kernel<<<1, 32, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const uint32_t most = 2u * sm_count_for_launch(), blocks = (a.max_tokens + kThreads - 1) / kThreads;
+  return launch_behind(kv_plan_kernel<false>, dim3(blocks < most ? blocks : most), kThreads, 0, s, a);
 }
 
 }  // namespace shn

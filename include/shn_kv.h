@@ -34,7 +34,7 @@ extern "C" {
 /* Workspace of every call here but shn_kv_attn_shared, 256-byte aligned. */
 #define SHN_KV_WORKSPACE_BYTES 256u
 
-/* One layer's cache. d_k, d_v: 16-byte aligned; the scales: 4-byte aligned. */
+/* One layer's cache. All four pointers are 16-byte aligned. */
 typedef struct shn_kv_cache {
   int8_t* d_k;           /* [n_pages][kv_heads][page_tokens][head_dim] */
   int8_t* d_v;
