@@ -16,139 +16,197 @@ __global__ void kv_begin_kernel(DeviceStatus* st) {
 // rotation needs no other lane; what is not rotated is dealt to the lanes behind. A row's sum of squares and its largest
 // magnitude are log2(D/8) shuffles away. A lane covers the same dimensions in every row it takes, so the token's cosines and
 // sines and the weights are loaded once, and a block's rows are asked for before anything else is waited for.
-// All arithmetic is float32 (two values an instruction); the query is rounded once to bf16, key and value once to INT8.
+// All arithmetic is float32 (two values an instruction); the query is rounded once to bf16, key and value once to INT8:
+// what is bound by issuing instructions before it is bound by memory has no division in its inner part, and rounds
+// y / scale by adding 1.5 * 2^23, which leaves the integer in the last byte.
 constexpr int kStoreThreads = 256;
-constexpr int kAtOnce = 4;  // rows of a lane that are on their way together
+constexpr int kAtOnce = 4;  // query rows of a lane that are on their way together
+
+// A lane's 8 values of a row, two by two: [0], [1] the first 4, [2], [3] the other 4.
+struct Row8 {
+  uint64_t x[4];
+};
+struct RawRow {
+  uint2 lo, hi;
+  __device__ __forceinline__ Row8 values() const {
+    using tc::pack2;
+    return Row8{{pack2(bf16_lo(lo.x), bf16_hi(lo.x)), pack2(bf16_lo(lo.y), bf16_hi(lo.y)), pack2(bf16_lo(hi.x), bf16_hi(hi.x)),
+                 pack2(bf16_lo(hi.y), bf16_hi(hi.y))}};
+  }
+};
+// The token's rotation of the lane's values: (x_i, x_{i+4}) by the angle of c[i / 2]'s i mod 2; or (pairs) (x_0, x_1), (x_2, x_3),
+// (x_4, x_5), (x_6, x_7) by the four angles in order.
+struct Turn {
+  uint64_t c[2], s[2], minus_s[2];
+  __device__ __forceinline__ void apply(Row8& v, bool pairs) const {
+    using namespace tc;
+    if (!pairs) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint64_t u = v.x[e], w = v.x[e + 2];
+        v.x[e] = fma2(u, c[e], mul2(w, minus_s[e]));
+        v.x[e + 2] = fma2(w, c[e], mul2(u, s[e]));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float u, w, c0, c1, s0, s1;
+        unpack2(v.x[e], u, w);
+        unpack2(c[e / 2], c0, c1);
+        unpack2(s[e / 2], s0, s1);
+        const float co = e & 1 ? c1 : c0, si = e & 1 ? s1 : s0;
+        v.x[e] = pack2(u * co - w * si, w * co + u * si);
+      }
+    }
+  }
+};
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 template <int D>
-__global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(KvPages c, KvStoreArgs a) {
+__global__ void __launch_bounds__(kStoreThreads, 3) kv_store_kernel(KvPages c, KvStoreArgs a) {
   using namespace tc;
   constexpr uint32_t kLanes = D / 8, kGroups = kStoreThreads / kLanes;
-  const uint32_t token = blockIdx.x, lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
-  const uint32_t rows = a.q_heads + 2 * c.kv_heads;
-  // a block's rows are consecutive; all lanes of a warp run the same number of turns (the shuffles are full)
-  const uint32_t per_block = (rows + gridDim.y - 1) / gridDim.y;
-  const uint32_t first = blockIdx.y * per_block, last = min(rows, first + per_block);
+  const uint32_t lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
+  // The block's share of the query rows, and of the key and value rows (keys first); all lanes of a warp run the same
+  // number of turns (the shuffles are full).
+  const uint32_t q_share = (a.q_heads + gridDim.y - 1) / gridDim.y, kv_share = (2 * c.kv_heads + gridDim.y - 1) / gridDim.y;
+  const uint32_t q0 = blockIdx.y * q_share, q1 = min(a.q_heads, q0 + q_share);
+  const uint32_t kv0 = blockIdx.y * kv_share, kv1 = min(2 * c.kv_heads, kv0 + kv_share);
   // the lane's dimensions: 4 from d_lo, 4 from d_hi
   const uint32_t pair = a.rot / 8;  // lanes that rotate
   const bool turns = lane < pair;
   const uint32_t d_lo = turns ? 4 * lane : a.rot + 8 * (lane - pair), d_hi = turns ? d_lo + a.rot / 2 : d_lo + 4;
 
-  uint2 raw[kAtOnce][2];
-  auto ask = [&](uint32_t base) {
+  const uint32_t further = d_hi - d_lo;
+  RawRow raw[kAtOnce], raw_kv;
+  auto ask = [&](const uint16_t* src, RawRow& r) {
+    r.lo = *reinterpret_cast<const uint2*>(src);
+    r.hi = *reinterpret_cast<const uint2*>(src + further);
+  };
+  const uint16_t *q_src, *k_src, *v_src;  // the token's rows
+  auto ask_q = [&](uint32_t base) {
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const uint32_t row = base + i * kGroups + sub;
-      raw[i][0] = raw[i][1] = make_uint2(0, 0);
-      if (row < last) {
-        const uint16_t* src = row < a.q_heads                 ? a.q + (uint64_t)token * a.q_stride + (uint64_t)row * D
-                              : row < a.q_heads + c.kv_heads ? a.k + (uint64_t)token * a.k_stride + (uint64_t)(row - a.q_heads) * D
-                                                             : a.v + (uint64_t)token * a.v_stride + (uint64_t)(row - a.q_heads - c.kv_heads) * D;
-        raw[i][0] = *reinterpret_cast<const uint2*>(src + d_lo);
-        raw[i][1] = *reinterpret_cast<const uint2*>(src + d_hi);
-      }
+      raw[i].lo = raw[i].hi = make_uint2(0, 0);
+      if (row < q1) ask(q_src + row * D, raw[i]);
     }
   };
-  ask(first);
-  const int32_t slot = a.slots[token];
-  const int32_t pos = a.rot ? a.positions[token] : 0;
-  auto weights = [&](const uint16_t* w, uint64_t* f) {
-    if (!w) return;
-    const uint2 x = *reinterpret_cast<const uint2*>(w + d_lo), y = *reinterpret_cast<const uint2*>(w + d_hi);
-    f[0] = pack2(bf16_lo(x.x), bf16_hi(x.x)), f[1] = pack2(bf16_lo(x.y), bf16_hi(x.y));
-    f[2] = pack2(bf16_lo(y.x), bf16_hi(y.x)), f[3] = pack2(bf16_lo(y.y), bf16_hi(y.y));
+  auto ask_kv = [&](uint32_t row) {
+    raw_kv.lo = raw_kv.hi = make_uint2(0, 0);
+    if (row < kv1) ask(row < c.kv_heads ? k_src + row * D : v_src + (row - c.kv_heads) * D, raw_kv);
   };
-  uint64_t wq[4] = {0, 0, 0, 0}, wk[4] = {0, 0, 0, 0};
-  weights(a.q_weight, wq);
-  weights(a.k_weight, wk);
+  auto weights = [&](const uint16_t* w) {
+    RawRow r = {make_uint2(0, 0), make_uint2(0, 0)};
+    if (w) r.lo = *reinterpret_cast<const uint2*>(w + d_lo), r.hi = *reinterpret_cast<const uint2*>(w + d_hi);
+    return r.values();
+  };
+  const Row8 wq = weights(a.q_weight), wk = weights(a.k_weight);
+  auto normed = [&](Row8& v, const Row8& w, bool is) {
+    uint64_t s2 = mul2(v.x[0], v.x[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) s2 = fma2(v.x[e], v.x[e], s2);
+    float s0, s1;
+    unpack2(s2, s0, s1);
+    float ss = s0 + s1;
+#pragma unroll
+    for (int d = kLanes / 2; d; d >>= 1) ss += __shfl_xor_sync(~0u, ss, d);
+    const float r = rsqrtf(ss * (1.f / D) + a.eps);
+    const uint64_t r2 = pack2(r, r);
+    if (is) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v.x[e] = mul2(mul2(v.x[e], r2), w.x[e]);
+    }
+  };
+  // a block's tokens one after another; the next one's slot and position are read a turn ahead
+  int32_t slot = blockIdx.x < a.n_tokens ? a.slots[blockIdx.x] : -1, pos = a.rot && blockIdx.x < a.n_tokens ? a.positions[blockIdx.x] : 0;
   after_previous();
-  if ((slot >= 0 && ((uint32_t)slot >> c.log2_pt) >= c.n_pages) || (a.rot && (pos < 0 || (uint32_t)pos >= a.n_positions))) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) report(a.st, SHN_ERR_INVALID_ARG, token);
-    return;
-  }
-  // cosines and sines of the lane's pairs: (x_i, x_{i+4}) by angle d_lo + i, or with a.pairs (x_0, x_1), (x_2, x_3) by angles
-  // d_lo / 2, + 1 and (x_4, x_5), (x_6, x_7) by d_hi / 2, + 1
-  float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (turns) {
-    const float *cp = a.cos_sin + (uint64_t)pos * a.rot, *sp = cp + a.rot / 2;
-    if (a.pairs) {
-      const float2 c0 = *reinterpret_cast<const float2*>(cp + d_lo / 2), c1 = *reinterpret_cast<const float2*>(cp + d_hi / 2);
-      const float2 s0 = *reinterpret_cast<const float2*>(sp + d_lo / 2), s1 = *reinterpret_cast<const float2*>(sp + d_hi / 2);
-      cs = make_float4(c0.x, c0.y, c1.x, c1.y), sn = make_float4(s0.x, s0.y, s1.x, s1.y);
-    } else {
-      cs = *reinterpret_cast<const float4*>(cp + d_lo), sn = *reinterpret_cast<const float4*>(sp + d_lo);
+  for (uint32_t token = blockIdx.x; token < a.n_tokens; token += gridDim.x) {
+    q_src = a.q + (uint64_t)token * a.q_stride + d_lo;
+    k_src = a.k + (uint64_t)token * a.k_stride + d_lo, v_src = a.v + (uint64_t)token * a.v_stride + d_lo;
+    ask_q(q0);
+    ask_kv(kv0 + sub);
+    const int32_t slot_now = slot, pos_now = pos;
+    if (token + gridDim.x < a.n_tokens) {
+      slot = a.slots[token + gridDim.x];
+      if (a.rot) pos = a.positions[token + gridDim.x];
     }
-  }
-  for (uint32_t base = first; base < last; base += kAtOnce * kGroups) {
-    if (base != first) ask(base);
+    if ((slot_now >= 0 && ((uint32_t)slot_now >> c.log2_pt) >= c.n_pages) || (a.rot && (pos_now < 0 || (uint32_t)pos_now >= a.n_positions))) {
+      if (threadIdx.x == 0 && blockIdx.y == 0) report(a.st, SHN_ERR_INVALID_ARG, token);
+      continue;
+    }
+    Turn turn = {};
+    if (turns) {
+      const float *cp = a.cos_sin + (uint64_t)pos_now * a.rot, *sp = cp + a.rot / 2;
+      float4 cs, sn;
+      if (a.pairs) {
+        const float2 c0 = *reinterpret_cast<const float2*>(cp + d_lo / 2), c1 = *reinterpret_cast<const float2*>(cp + d_hi / 2);
+        const float2 s0 = *reinterpret_cast<const float2*>(sp + d_lo / 2), s1 = *reinterpret_cast<const float2*>(sp + d_hi / 2);
+        cs = make_float4(c0.x, c0.y, c1.x, c1.y), sn = make_float4(s0.x, s0.y, s1.x, s1.y);
+      } else {
+        cs = *reinterpret_cast<const float4*>(cp + d_lo), sn = *reinterpret_cast<const float4*>(sp + d_lo);
+      }
+      turn = {{pack2(cs.x, cs.y), pack2(cs.z, cs.w)}, {pack2(sn.x, sn.y), pack2(sn.z, sn.w)}, {pack2(-sn.x, -sn.y), pack2(-sn.z, -sn.w)}};
+    }
+    // ---- queries
+    uint16_t* q_dst = a.q_out + (uint64_t)token * a.q_out_stride + d_lo;
+    for (uint32_t base = q0; base < q1; base += kAtOnce * kGroups) {
+      if (base != q0) ask_q(base);
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (base + i * kGroups >= last) break;
-      const uint32_t row = base + i * kGroups + sub;
-      const bool real = row < last;
-      const bool is_q = row < a.q_heads, is_k = !is_q && row < a.q_heads + c.kv_heads;
-      // x[0], x[1]: the first 4 values, x[2], x[3]: the other 4
-      uint64_t x[4] = {pack2(bf16_lo(raw[i][0].x), bf16_hi(raw[i][0].x)), pack2(bf16_lo(raw[i][0].y), bf16_hi(raw[i][0].y)),
-                       pack2(bf16_lo(raw[i][1].x), bf16_hi(raw[i][1].x)), pack2(bf16_lo(raw[i][1].y), bf16_hi(raw[i][1].y))};
-      if (a.q_weight || a.k_weight) {
-        uint64_t s2 = mul2(x[0], x[0]);
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (base + i * kGroups >= q1) break;
+        const uint32_t row = base + i * kGroups + sub;
+        Row8 v = raw[i].values();
+        if (a.q_weight) normed(v, wq, true);
+        if (turns) turn.apply(v, a.pairs);
+        if (row < q1) {
+          float y[8];
 #pragma unroll
-        for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
-        float s0, s1;
-        unpack2(s2, s0, s1);
-        float ss = s0 + s1;
-#pragma unroll
-        for (int d = kLanes / 2; d; d >>= 1) ss += __shfl_xor_sync(~0u, ss, d);
-        if (is_q ? a.q_weight != nullptr : is_k && a.k_weight) {
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
-          const uint64_t r2 = pack2(r, r);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], r2), is_q ? wq[e] : wk[e]);
+          for (int e = 0; e < 4; ++e) unpack2(v.x[e], y[2 * e], y[2 * e + 1]);
+          uint16_t* dst = q_dst + row * D;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(bf16_pack(y[0], y[1]), bf16_pack(y[2], y[3]));
+          *reinterpret_cast<uint2*>(dst + further) = make_uint2(bf16_pack(y[4], y[5]), bf16_pack(y[6], y[7]));
         }
       }
+    }
+    // ---- keys and values
+    if (slot_now < 0) continue;
+    for (uint32_t base = kv0; base < kv1; base += kGroups) {
+      const uint32_t row = base + sub;
+      const bool is_k = row < c.kv_heads;
+      Row8 v = raw_kv.values();
+      if (base + kGroups < kv1) ask_kv(row + kGroups);
+      if (a.k_weight && base < c.kv_heads) normed(v, wk, is_k);
+      if (turns && is_k) turn.apply(v, a.pairs);
       float y[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) unpack2(x[e], y[2 * e], y[2 * e + 1]);
-      if (turns && (is_q || is_k)) {
-        auto turn = [&](float& u, float& w, float co, float si) {
-          const float u0 = u, w0 = w;
-          u = u0 * co - w0 * si;
-          w = w0 * co + u0 * si;
-        };
-        if (a.pairs) {
-          turn(y[0], y[1], cs.x, sn.x), turn(y[2], y[3], cs.y, sn.y), turn(y[4], y[5], cs.z, sn.z), turn(y[6], y[7], cs.w, sn.w);
-        } else {
-          turn(y[0], y[4], cs.x, sn.x), turn(y[1], y[5], cs.y, sn.y), turn(y[2], y[6], cs.z, sn.z), turn(y[3], y[7], cs.w, sn.w);
-        }
-      }
-      uint32_t top = 0;
-      if (__any_sync(~0u, real && !is_q)) {
-        // largest magnitude as an integer maximum of the bits: a NaN is larger than infinity and stays
+      for (int e = 0; e < 4; ++e) unpack2(v.x[e], y[2 * e], y[2 * e + 1]);
+      float top = fabsf(y[0]);  // a NaN among them stays
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+      for (int e = 1; e < 8; ++e) top = max_nan(top, fabsf(y[e]));
 #pragma unroll
-        for (int d = kLanes / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
-      }
-      if (!real) continue;
-      if (is_q) {
-        uint16_t* dst = a.q_out + (uint64_t)token * a.q_out_stride + (uint64_t)row * D;
-        *reinterpret_cast<uint2*>(dst + d_lo) = make_uint2(bf16_pack(y[0], y[1]), bf16_pack(y[2], y[3]));
-        *reinterpret_cast<uint2*>(dst + d_hi) = make_uint2(bf16_pack(y[4], y[5]), bf16_pack(y[6], y[7]));
-      } else if (slot >= 0) {
-        const float scale = (top > 0x7F800000u ? __uint_as_float(top) : fmaxf(__uint_as_float(top), 1e-30f)) / 127.f;
-        uint32_t w[2] = {0, 0};
+      for (int d = kLanes / 2; d; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
+      if (row >= kv1) continue;
+      const float scale = max_nan(top, 1e-30f) / 127.f, inverse = 1.f / scale;
+      const uint64_t by = pack2(inverse, inverse), round = pack2(12582912.f, 12582912.f);
+      uint32_t w[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          // |y / scale| <= 127 up to rounding; y / inf = 0 and NaN -> 0, so a poisoned row is 0 * its scale = NaN
-          const int v = max(-127, min(127, __float2int_rn(y[e] / scale)));
-          w[e / 4] |= ((uint32_t)v & 0xFFu) << (8 * (e % 4));
-        }
-        const uint64_t at = kv_row_of_slot(c, (uint32_t)slot, row - a.q_heads - (is_k ? 0 : c.kv_heads));
-        int8_t* dst = (is_k ? c.k : c.v) + at * D;
-        *reinterpret_cast<uint32_t*>(dst + d_lo) = w[0];
-        *reinterpret_cast<uint32_t*>(dst + d_hi) = w[1];
-        if (lane == 0) (is_k ? c.k_scale : c.v_scale)[at] = scale;
+      for (int e = 0; e < 2; ++e) {
+        float f[4];
+        unpack2(fma2(v.x[2 * e], by, round), f[0], f[1]);
+        unpack2(fma2(v.x[2 * e + 1], by, round), f[2], f[3]);
+        w[e] = __byte_perm(__byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040),
+                           __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040), 0x5410);
       }
+      const uint64_t at = kv_row_of_slot(c, (uint32_t)slot_now, is_k ? row : row - c.kv_heads);
+      int8_t* dst = (is_k ? c.k : c.v) + at * D + d_lo;
+      *reinterpret_cast<uint32_t*>(dst) = w[0];
+      *reinterpret_cast<uint32_t*>(dst + further) = w[1];
+      if (lane == 0) (is_k ? c.k_scale : c.v_scale)[at] = scale;
     }
   }
 }
@@ -207,11 +265,13 @@ cudaError_t launch_kv_begin(DeviceStatus* st, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_store(const KvPages& c, uint32_t head_dim, const KvStoreArgs& a, int sm_count, cudaStream_t s) {
-  const uint32_t groups = kStoreThreads * 8 / head_dim, rows = a.q_heads + 2 * c.kv_heads;
+  const uint32_t groups = kStoreThreads * 8 / head_dim, rows = a.q_heads > 2 * c.kv_heads ? a.q_heads : 2 * c.kv_heads;
   // few tokens: their rows over several blocks, until the SMs have two blocks each or a block has one row per group
   uint32_t parts = 1;
   while ((uint64_t)parts * a.n_tokens < 2ull * sm_count && parts * groups < rows) ++parts;
-  const dim3 grid(a.n_tokens, parts);
+  // three blocks to an SM, each with its tokens
+  const uint32_t most = 3u * sm_count;
+  const dim3 grid(a.n_tokens < most ? a.n_tokens : most, parts);
   return head_dim == 128 ? launch_behind(kv_store_kernel<128>, grid, kStoreThreads, 0, s, c, a)
                          : launch_behind(kv_store_kernel<64>, grid, kStoreThreads, 0, s, c, a);
 }

@@ -85,7 +85,8 @@ int shn_kv_plan(const int32_t* d_ctx_len, const int32_t* d_new_len, uint32_t n_r
  *     pairs = 0: (y_i, y_{i + rot/2}) by angle i;  pairs = 1: (y_2i, y_2i+1) by angle i:
  *     (a, b) -> (a cos - b sin, b cos + a sin)
  *   query: bfloat16(y);  key, and value with y = x: scale = max(|y|max, 1e-30) / 127,
- *     int8 = round_half_even(y / scale) in [-127, 127]. A row with an infinity or NaN gets that as its scale.
+ *     int8 = round_half_even(y / scale) in [-127, 127], the quotient to 2^-22 of itself. A row with an infinity or NaN
+ *     gets that as its scale, so that it reads as values that are not finite.
  *  d_q, d_k, d_v  device, [n_tokens][heads][head_dim], heads contiguous, tokens *_stride values apart (a
  *                 multiple of 8); 16-byte aligned. d_q may be NULL (q_heads 0: keys and values only).
  *  d_q_out        device, [n_tokens][q_heads][head_dim], tokens q_out_stride values apart; may be d_q with the same
