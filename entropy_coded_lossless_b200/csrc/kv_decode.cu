@@ -456,12 +456,14 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   after_previous();
-  // 32 results at a time: a lane finds one's place and reads its (mt, ms, l); then all lanes add them up one after another
-  for (uint32_t k0 = 32 * (warp % kTeam); k0 < all; k0 += 32 * kTeam) {
+  // Each warp of the team takes its share of them in a row, 32 at a time: a lane finds one's place and reads its (mt, ms, l);
+  // then all lanes add them up one after another.
+  const uint32_t share_n = (all + kTeam - 1) / kTeam, k_end = min(all, share_n * (warp % kTeam + 1));
+  for (uint32_t k0 = share_n * (warp % kTeam); k0 < k_end; k0 += 32) {
     const uint32_t k = k0 + lane;
     const float* src = nullptr;
     float4 x = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-    if (k < all) {
+    if (k < k_end) {
       const bool part = k >= pn && k < pn + pl.splits;
       if (part) {
         const uint64_t q = (uint64_t)(k - pn) * a.n_reqs * a.q_heads + item;
@@ -494,8 +496,8 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
     for (int d = 16; d; d >>= 1) share += __shfl_xor_sync(~0u, share, d);
     l += share;
     const uint32_t have = __ballot_sync(~0u, src != nullptr);
-    const uint32_t last = min(32u, all - k0);
-#pragma unroll 4
+    const uint32_t last = min(32u, k_end - k0);
+#pragma unroll 8
     for (uint32_t i = 0; i < last; ++i) {
       const float* from = reinterpret_cast<const float*>(__shfl_sync(~0u, (unsigned long long)src, i));
       const float f = __shfl_sync(~0u, by, i);
@@ -552,9 +554,9 @@ cudaError_t launch(const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, 
   e = pl.rows == 8 ? launch_behind(kv_decode_kernel<D, 1>, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl)
                    : launch_behind(kv_decode_kernel<D, 2>, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl);
   if (e != cudaSuccess) return e;
-  // few rows may have hundreds of pieces each: as many warps to a row as fill the warps that ran before, 8 at most
+  // few rows may have hundreds of pieces each: as many warps to a row as make twice the warps that ran before, 8 at most
   const uint32_t items = a.n_reqs * a.q_heads;
-  const uint64_t twice = 2ull * items;
+  const uint64_t twice = items;
   if (twice > pl.warps) return launch_behind(kv_join_kernel<D, 1>, dim3((items + 7) / 8), kDecodeThreads, 0, s, c, a, pl);
   if (2 * twice > pl.warps) return launch_behind(kv_join_kernel<D, 2>, dim3((items + 3) / 4), kDecodeThreads, 0, s, c, a, pl);
   if (4 * twice > pl.warps) return launch_behind(kv_join_kernel<D, 4>, dim3((items + 1) / 2), kDecodeThreads, 0, s, c, a, pl);
