@@ -162,6 +162,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   if (__syncthreads_or(status == SHN_ERR_TIMEOUT)) return;
   const uint32_t rows_here = min(kRows, w.rows - w.row0);
   // tokens the block's last row sees; every row of the block sees at most as many
+  // row i of the block is query base_q + x and head y of the group, x = (rest + i) / group: with i + rest < 320 and group <= 64 that
+  // is a multiplication by 2^16 / group, rounded up
+  const uint32_t base_q = w.row0 / group, rest = w.row0 - base_q * group, inv_group = (65536u + group - 1) / group;
+  auto query_of = [&](uint32_t i, uint32_t& head) -> uint32_t {
+    const uint32_t x = ((rest + i) * inv_group) >> 16;
+    head = rest + i - x * group;
+    return base_q + x;
+  };
   const int32_t shift = w.len - w.nq + 1;  // query i sees shift + i tokens
   const int32_t most = kPart ? max(0, w.len) : max(0, min(w.len, shift + (int32_t)((w.row0 + rows_here - 1) / group)));
   const uint32_t tiles = ((uint32_t)most + kTile - 1) / kTile;
@@ -202,13 +210,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     // ---- softmax -------------------------------------------------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     // the queries of the block as an operand, zeros behind the last row
+    const uint16_t* q_src = a.q + (uint64_t)w.q0 * a.q_stride + (uint64_t)hk * group * D;
     uint4 qx[kRows * D / 8 / kSoftThreads];  // all loads first: one wait for them
 #pragma unroll
     for (uint32_t i = 0; i < kRows * D / 8 / kSoftThreads; ++i) {
-      const uint32_t at = tid + i * kSoftThreads, row = at / (D / 8), piece = at % (D / 8), g = w.row0 + row;
+      const uint32_t at = tid + i * kSoftThreads, row = at / (D / 8), piece = at % (D / 8);
+      uint32_t head;
+      const uint32_t query = query_of(row, head);
       qx[i] = make_uint4(0, 0, 0, 0);
-      if (row < rows_here)
-        qx[i] = *reinterpret_cast<const uint4*>(a.q + (uint64_t)(w.q0 + g / group) * a.q_stride + (uint64_t)(hk * group + g % group) * D + piece * 8);
+      if (row < rows_here) qx[i] = *reinterpret_cast<const uint4*>(q_src + (uint64_t)query * a.q_stride + head * D + piece * 8);
     }
     // One power of two brings the block's largest query value just below 2^15; fp16 then holds every bf16 down to 2^-32
     // of it exactly. (Values that are not finite set no size and stay what they are.)
@@ -247,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     const uint32_t s_at = at + half * 128, o_at = at + 256 + half * D;
     auto seen_by = [&](uint32_t row) -> int32_t {
       if (row >= rows_here) return 0;
-      const uint32_t q = (w.row0 + row) / group;
+      uint32_t head;
+      const uint32_t q = query_of(row, head);
       if constexpr (kPart) {
         bool bad;
         return max(0, min(w.len, decode_len(c, a, (int32_t)w.t0 + w.len, q, bad) - (int32_t)w.t0));
@@ -423,46 +434,69 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     if (ok && tiles) ok = __all_sync(~0u, bar_wait(bars + kOFull + 16 * half + 8, (tiles - 1) & 1, stop));
     if (ok) {
       fence_after();
-      const uint32_t row = half * 128 + rows32 + lane, g = w.row0 + row;
+      // Each warp takes half the columns of its 32 rows, 32 at a time: a thread has a row, and a row a thread is written as lines
+      // would be, so the values change hands in shared memory (the queries' place, which no product reads any more: 4 KB a warp).
+      const uint32_t row = half * 128 + rows32 + lane;
       const bool any = seen_by(row) > 0;
       // no token seen: zeros. (A sum that is not positive although tokens were seen is a NaN's or an infinity's.)
       const float sum = __uint_as_float(lds32(sums + 4 * (rows32 + lane)));
-      const float inv = any ? pow2(held) / sum : 0.f;
-      const uint32_t first = (warp >> 2 & 1) * (D / 2);
-      const uint64_t query = (uint64_t)(w.q0 + g / group), head = hk * group + g % group;
-      uint16_t* dst = a.out + query * a.out_stride + head * D + first;
-      float* part = nullptr;
+      const float inv = any ? held2 / sum : 0.f;
+      const uint32_t first = (warp >> 2 & 1) * (D / 2), mine = base + L::q + half * L::kOperand + (warp & 7) * (L::kOperand / 8);
+      const uint64_t part0 = kPart ? (uint64_t)(blockIdx.x / c.kv_heads % pl.splits) * a.n_reqs : 0;
       if constexpr (kPart) {
-        const uint64_t at = ((uint64_t)(blockIdx.x / c.kv_heads % pl.splits) * a.n_reqs + query) * a.q_heads + head;
-        part = pl.split_out + at * D + first;
+        uint32_t head;
+        const uint32_t query = query_of(row, head);
         if (row < rows_here && first == 0) {
           const float ref = __uint_as_float(lds32(refs + 4 * (rows32 + lane)));
-          pl.split_ml[at] = make_float4(tiles ? ref + held : -INFINITY, ref, tiles ? sum : 0.f, 0.f);
+          pl.split_ml[(part0 + query) * a.q_heads + hk * group + head] = make_float4(tiles ? ref + held : -INFINITY, ref, tiles ? sum : 0.f, 0.f);
         }
       }
-#pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
+      // a row's 32 columns are `kChunks` pieces of 16 bytes; a turn of the warp writes 32 / kChunks rows of them
+      constexpr uint32_t kColumns = kPart && D == 64 ? 16 : 32, kChunks = kPart ? kColumns / 4 : kColumns / 8;
+#pragma unroll 1
+      for (uint32_t q = 0; q < D / 2; q += kColumns) {
         uint32_t o[32];
         if (tiles) {
-          ld32(tmem + (rows32 << 16) + 256 + half * D + first + 32 * q, o);
+          const uint32_t from = tmem + (rows32 << 16) + 256 + half * D + first + q;
+          if constexpr (kColumns == 32) {
+            ld32(from, o);
+          } else {
+            ld8(from, o);
+            ld8(from + 8, o + 8);
+          }
           wait_ld();
         }
-        if constexpr (kPart) {
-          if (row < rows_here && tiles) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(part + 32 * q + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-        } else if (row < rows_here) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t y[4];
+        for (uint32_t e = 0; e < kChunks; ++e) {
+          uint4 y;
+          if constexpr (kPart) {
+            y = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint32_t z[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              y[i] = any ? bf16_pack(__uint_as_float(o[8 * e + 2 * i]) * inv, __uint_as_float(o[8 * e + 2 * i + 1]) * inv) : 0u;
-            *reinterpret_cast<uint4*>(dst + 32 * q + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
+              z[i] = any ? bf16_pack(__uint_as_float(o[8 * e + 2 * i]) * inv, __uint_as_float(o[8 * e + 2 * i + 1]) * inv) : 0u;
+            y = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+          sts128(mine + (lane * kChunks + (e ^ (lane / (8 / kChunks) % kChunks))) * 16, y);
+        }
+        __syncwarp();
+#pragma unroll
+        for (uint32_t i = 0; i < kChunks; ++i) {
+          const uint32_t r = i * (32 / kChunks) + lane / kChunks, e = lane % kChunks, at = half * 128 + rows32 + r;
+          const uint4 y = lds128(mine + (r * kChunks + (e ^ (r / (8 / kChunks) % kChunks))) * 16);
+          uint32_t head;
+          const uint32_t query = query_of(at, head);
+          if (at < rows_here) {
+            if constexpr (kPart) {
+              if (tiles)
+                *reinterpret_cast<uint4*>(pl.split_out + ((part0 + query) * a.q_heads + hk * group + head) * D + first + q + 4 * e) = y;
+            } else {
+              *reinterpret_cast<uint4*>(a.out + (uint64_t)(w.q0 + query) * a.out_stride + (uint64_t)(hk * group + head) * D + first + q + 8 * e) = y;
+            }
           }
         }
+        __syncwarp();
       }
       fence_before();
     }

@@ -100,6 +100,9 @@ __device__ __forceinline__ void ld32(uint32_t addr, uint32_t* v) {
       : SHN_R8(v, 0), SHN_R8(v, 8), SHN_R8(v, 16), SHN_R8(v, 24)
       : "r"(addr));
 }
+__device__ __forceinline__ void ld8(uint32_t addr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : SHN_R8(v, 0) : "r"(addr));
+}
 // 16 lanes: thread t holds rows t/4 (registers 0, 1) and t/4 + 8 (registers 2, 3) of columns 2(t%4), 2(t%4) + 1 of
 // each 8 columns; 4 registers per 8 columns
 __device__ __forceinline__ void ld_quad32(uint32_t addr, uint32_t* v) {
