@@ -64,61 +64,87 @@ struct Work {
 __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a, uint32_t group, uint32_t tile_from_end,
                                           uint32_t* scan, Work& w) {
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const uint32_t run = (a.n_reqs + kThreads - 1) / kThreads;
-  const uint32_t r0 = min(a.n_reqs, t * run), r1 = min(a.n_reqs, r0 + run);
-  uint32_t own = 0;
-  int32_t kv_len = 0;  // of the run's last request: with up to kThreads requests the one that is meant
-  for (uint32_t r = r0; r < r1; ++r) {
-    const int32_t b = a.cu_q[r], e = a.cu_q[r + 1];
-    kv_len = a.kv_len[r];
-    if (b < 0 || e < b || (uint32_t)e > a.n_tokens) report(a.st, SHN_ERR_INVALID_ARG, r);
-    else own += ((uint32_t)(e - b) * group + kRows - 1) / kRows;
-  }
-  uint32_t inc = own;
+  int32_t len;
+  if (a.n_reqs <= 32) {
+    // every warp finds it by itself, a request to a lane
+    const bool is = lane < a.n_reqs;
+    const int32_t b = is ? a.cu_q[lane] : 0, e = is ? a.cu_q[lane + 1] : 0;
+    len = is ? a.kv_len[lane] : 0;
+    const bool bad = b < 0 || e < b || (uint32_t)e > a.n_tokens;
+    if (bad && warp == 0) report(a.st, SHN_ERR_INVALID_ARG, lane);
+    const uint32_t own = bad ? 0 : ((uint32_t)(e - b) * group + kRows - 1) / kRows;
+    uint32_t inc = own;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t x = __shfl_up_sync(~0u, inc, d);
-    if (lane >= (uint32_t)d) inc += x;
-  }
-  if (lane == 31) scan[warp] = inc;
-  if (t == 0) scan[30] = 0xFFFFFFFFu;
-  __syncthreads();
-  uint32_t before = 0, total = 0;
-#pragma unroll
-  for (uint32_t i = 0; i < kThreads / 32; ++i) {
-    const uint32_t x = scan[i];
-    before += i < warp ? x : 0;
-    total += x;
-  }
-  if (tile_from_end >= total) return false;
-  const uint32_t tile = total - 1 - tile_from_end;
-  before += inc - own;
-  if (tile >= before && tile < before + own) {
-    uint32_t left = tile - before;
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t x = __shfl_up_sync(~0u, inc, d);
+      if (lane >= (uint32_t)d) inc += x;
+    }
+    const uint32_t total = __shfl_sync(~0u, inc, 31);
+    if (tile_from_end >= total) return false;
+    const uint32_t tile = total - 1 - tile_from_end;
+    w.req = __ffs(__ballot_sync(~0u, tile < inc)) - 1;  // the first whose tiles reach it
+    w.row0 = (tile - __shfl_sync(~0u, inc - own, w.req)) * kRows;
+    w.q0 = __shfl_sync(~0u, b, w.req);
+    w.nq = __shfl_sync(~0u, e, w.req) - w.q0;
+    len = __shfl_sync(~0u, len, w.req);
+    w.rows = (uint32_t)w.nq * group;
+  } else {
+    const uint32_t run = (a.n_reqs + kThreads - 1) / kThreads;
+    const uint32_t r0 = min(a.n_reqs, t * run), r1 = min(a.n_reqs, r0 + run);
+    uint32_t own = 0;
+    int32_t kv_len = 0;  // of the run's last request: with up to kThreads requests the one that is meant
     for (uint32_t r = r0; r < r1; ++r) {
       const int32_t b = a.cu_q[r], e = a.cu_q[r + 1];
-      if (b < 0 || e < b || (uint32_t)e > a.n_tokens) continue;
-      const uint32_t n = ((uint32_t)(e - b) * group + kRows - 1) / kRows;
-      if (left < n) {
-        scan[28] = (uint32_t)b;
-        scan[29] = (uint32_t)(e - b);
-        scan[30] = r;
-        scan[31] = left;
-        scan[32] = (uint32_t)(run == 1 ? kv_len : a.kv_len[r]);
-        break;
-      }
-      left -= n;
+      kv_len = a.kv_len[r];
+      if (b < 0 || e < b || (uint32_t)e > a.n_tokens) report(a.st, SHN_ERR_INVALID_ARG, r);
+      else own += ((uint32_t)(e - b) * group + kRows - 1) / kRows;
     }
+    uint32_t inc = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t x = __shfl_up_sync(~0u, inc, d);
+      if (lane >= (uint32_t)d) inc += x;
+    }
+    if (lane == 31) scan[warp] = inc;
+    if (t == 0) scan[30] = 0xFFFFFFFFu;
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kThreads / 32; ++i) {
+      const uint32_t x = scan[i];
+      before += i < warp ? x : 0;
+      total += x;
+    }
+    if (tile_from_end >= total) return false;
+    const uint32_t tile = total - 1 - tile_from_end;
+    before += inc - own;
+    if (tile >= before && tile < before + own) {
+      uint32_t left = tile - before;
+      for (uint32_t r = r0; r < r1; ++r) {
+        const int32_t b = a.cu_q[r], e = a.cu_q[r + 1];
+        if (b < 0 || e < b || (uint32_t)e > a.n_tokens) continue;
+        const uint32_t n = ((uint32_t)(e - b) * group + kRows - 1) / kRows;
+        if (left < n) {
+          scan[28] = (uint32_t)b;
+          scan[29] = (uint32_t)(e - b);
+          scan[30] = r;
+          scan[31] = left;
+          scan[32] = (uint32_t)(run == 1 ? kv_len : a.kv_len[r]);
+          break;
+        }
+        left -= n;
+      }
+    }
+    __syncthreads();
+    w.req = scan[30];
+    if (w.req >= a.n_reqs) return false;
+    w.row0 = scan[31] * kRows;
+    w.q0 = (int32_t)scan[28];
+    w.nq = (int32_t)scan[29];
+    w.rows = (uint32_t)w.nq * group;
+    len = (int32_t)scan[32];
   }
-  __syncthreads();
-  w.req = scan[30];
-  if (w.req >= a.n_reqs) return false;
-  w.row0 = scan[31] * kRows;
-  w.q0 = (int32_t)scan[28];
-  w.nq = (int32_t)scan[29];
-  w.rows = (uint32_t)w.nq * group;
   const int64_t holds = (int64_t)a.max_blocks << c.log2_pt;
-  int32_t len = (int32_t)scan[32];
   if (len < 0 || len > holds) {
     if (t == 0) report(a.st, SHN_ERR_INVALID_ARG, w.req);
     len = len < 0 ? 0 : (int32_t)holds;
@@ -158,8 +184,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   Work w;
   if constexpr (kPart) find_part(c, a, pl, group, w);
   else if (!find_work(c, a, group, blockIdx.x / c.kv_heads, reinterpret_cast<uint32_t*>(smem + L::scan), w)) return;
-  // after a wait that gave up the call has failed: the other blocks do not start on it
-  if (__syncthreads_or(status == SHN_ERR_TIMEOUT)) return;
   const uint32_t rows_here = min(kRows, w.rows - w.row0);
   // tokens the block's last row sees; every row of the block sees at most as many
   // row i of the block is query base_q + x and head y of the group, x = (rest + i) / group: with i + rest < 320 and group <= 64 that
@@ -200,15 +224,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
-  __syncthreads();
+  // after a wait that gave up the call has failed: the other blocks do not start on it
+  const bool failed = __syncthreads_or(status == SHN_ERR_TIMEOUT);
   fence_after();
+  if (failed) {
+    if (warp == kIssueWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(lds32(stop + 4)));
+    return;
+  }
   // all 512 columns are this block's, so its addresses begin at 0 (nothing that follows has to carry the base)
   const uint32_t tmem = 0;
   if (lds32(stop + 4) != 0) sts32(stop, 1);
 
   if (warp < kSoftWarps) {
     // ---- softmax -------------------------------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // the queries of the block as an operand, zeros behind the last row
     const uint16_t* q_src = a.q + (uint64_t)w.q0 * a.q_stride + (uint64_t)hk * group * D;
     uint4 qx[kRows * D / 8 / kSoftThreads];  // all loads first: one wait for them
@@ -222,14 +251,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     }
     // One power of two brings the block's largest query value just below 2^15; fp16 then holds every bf16 down to 2^-32
     // of it exactly. (Values that are not finite set no size and stay what they are.)
-    uint32_t top = 0;
+    uint32_t top2 = 0;
 #pragma unroll
     for (uint32_t i = 0; i < kRows * D / 8 / kSoftThreads; ++i) {
-      const uint32_t x[4] = {qx[i].x, qx[i].y, qx[i].z, qx[i].w};
+      top2 = __vmaxu2(__vmaxu2(top2, qx[i].x & 0x7FFF7FFFu), qx[i].y & 0x7FFF7FFFu);
+      top2 = __vmaxu2(__vmaxu2(top2, qx[i].z & 0x7FFF7FFFu), qx[i].w & 0x7FFF7FFFu);
+    }
+    uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+    if (top >= 0x7F80u) {
+      top = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = x[e] & 0x7FFFu, hi = x[e] >> 16 & 0x7FFFu;
-        top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+      for (uint32_t i = 0; i < kRows * D / 8 / kSoftThreads; ++i) {
+        const uint32_t x[4] = {qx[i].x, qx[i].y, qx[i].z, qx[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = x[e] & 0x7FFFu, hi = x[e] >> 16 & 0x7FFFu;
+          top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+        }
       }
     }
     top = __reduce_max_sync(~0u, top);
@@ -502,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     }
   } else if (warp < kIssueWarp) {
     // ---- fetch and convert ---------------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     constexpr int kLoads = D / 32;  // 16-byte loads of a thread per operand
     const uint32_t t = tid - kSoftThreads, cw = t >> 5;
     // A warp's load: 4 lanes on 64 values of a row, 8 rows. For D = 128 even warps take the rows' first 64 values.
@@ -619,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     }
   } else {
     // ---- products: a warp for each row tile runs the loop as one, an elected thread issues ---------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp < kIssueWarp + 2 && tiles) {
       const uint32_t i = warp - kIssueWarp;
       constexpr uint32_t kS = instr_desc(128, 64, false, false), kO = instr_desc(128, D, false, true);

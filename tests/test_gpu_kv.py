@@ -318,6 +318,17 @@ def test_prompt(h, hk, d, pt, new, ctx):
     run_prompt(cache, table, new, kv_lens, h, d, seed=6, scale=0.5, strided=True)  # a sharper softmax
 
 
+@pytest.mark.parametrize("n", [32, 33, 900, 1800])
+def test_prompt_of_many_requests(n):
+    """As many requests as a warp has lanes, one more, more than a block has threads and two for each of them."""
+    rng = random.Random(n)
+    new = [rng.choice([0, 1, 2, 5]) for _ in range(n)]
+    kv_lens = [m + rng.choice([0, 0, 3, 40]) for m in new]
+    table, pages = tables(kv_lens, 16, 1)
+    cache = filled_cache(pages, 1, 16, 64, seed=2)
+    run_prompt(cache, table, new, kv_lens, 2, 64, seed=3, padding=1)
+
+
 def test_prompt_rows_that_see_nothing():
     """More queries than tokens: the first ones see nothing and are zero; a request without tokens; padding requests."""
     new, kv_lens = [40, 5, 0, 0, 150], [10, 0, 0, 7, 149]
