@@ -17,8 +17,8 @@ __global__ void kv_begin_kernel(DeviceStatus* st) {
 // magnitude are log2(D/8) shuffles away. A lane covers the same dimensions in every row it takes, so the token's cosines and
 // sines and the weights are loaded once, and a block's rows are asked for before anything else is waited for.
 // All arithmetic is float32 (two values an instruction); the query is rounded once to bf16, key and value once to INT8:
-// what is bound by issuing instructions before it is bound by memory has no division in its inner part, and rounds
-// y / scale by adding 1.5 * 2^23, which leaves the integer in the last byte.
+// issuing instructions bounds this about as much as memory, so a row has one division and one reciprocal, and y / scale is
+// rounded by adding 1.5 * 2^23, which leaves the integer in the last byte.
 constexpr int kStoreThreads = 256;
 constexpr int kAtOnce = 4;  // query rows of a lane that are on their way together
 
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_kernel(KvPages c, K
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float f[4];
-        unpack2(fma2(v.x[2 * e], by, round), f[0], f[1]);
-        unpack2(fma2(v.x[2 * e + 1], by, round), f[2], f[3]);
+        unpack2(n[2 * e], f[0], f[1]);
+        unpack2(n[2 * e + 1], f[2], f[3]);
         w[e] = __byte_perm(__byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040),
                            __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040), 0x5410);
       }

@@ -85,8 +85,8 @@ int shn_kv_plan(const int32_t* d_ctx_len, const int32_t* d_new_len, uint32_t n_r
  *     pairs = 0: (y_i, y_{i + rot/2}) by angle i;  pairs = 1: (y_2i, y_2i+1) by angle i:
  *     (a, b) -> (a cos - b sin, b cos + a sin)
  *   query: bfloat16(y);  key, and value with y = x: scale = max(|y|max, 1e-30) / 127,
- *     int8 = round_half_even(y / scale) in [-127, 127], the quotient to 2^-22 of itself. A row with an infinity or NaN
- *     gets that as its scale, so that it reads as values that are not finite.
+ *     int8 = round_half_even(y / scale) in [-127, 127]. A row with an infinity or NaN gets that as its scale, so
+ *     that it reads as values that are not finite.
  *  d_q, d_k, d_v  device, [n_tokens][heads][head_dim], heads contiguous, tokens *_stride values apart (a
  *                 multiple of 8); 16-byte aligned. d_q may be NULL (q_heads 0: keys and values only).
  *  d_q_out        device, [n_tokens][q_heads][head_dim], tokens q_out_stride values apart; may be d_q with the same
@@ -125,11 +125,16 @@ int shn_kv_load(const shn_kv_cache* cache, const int32_t* d_slots, uint32_t n_to
  *  d_q, d_out  device, [n_tokens][q_heads][head_dim] bfloat16, tokens *_stride values apart (a multiple of 8),
  *              16-byte aligned; they do not overlap
  *  q_heads     a multiple of kv_heads, at most 64 * kv_heads
- * Keys and values enter the products as the exact integers; the scales are applied to the float32 scores and
- * weights, and a weight times its value's scale is rounded to bfloat16 (2^-9) before the second product.
+ * Arithmetic: queries and keys enter the products exactly (parts of a query 2^-32 of the largest of its block of 256 rows
+ * aside), scores, their scalings, the softmax and the sums are float32. Before the second product a weight is rounded to
+ * fp16, and a value is fp16(int8 * fp16(scale)): 2^-11 each. Weights below 2^-24 times the ratio of the largest value scale of the
+ * sequence to the token's are lost, so results are exact to 2^-24 of the sequence's largest value.
+ * A token whose value scale is not finite (or 1e36 and more) makes the rows that see it NaN; rows that do not see a token are
+ * not touched by what stands there, nor by what stands behind a sequence's end in its last page.
  * Device errors: SHN_ERR_INVALID_ARG for a page id outside the cache (detail = the request; that page counts as zeros),
  * a d_kv_len that the table row cannot hold (taken as what it holds) or a d_cu_q that decreases or leaves
- * [0, n_tokens] (those queries are left out).
+ * [0, n_tokens] (those queries are left out); SHN_ERR_TIMEOUT if a wait inside a kernel gave up (a quarter of a second; the
+ * result is not complete).
  */
 int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32_t q_heads,
                        const shn_kv_cache* cache, const int32_t* d_block_table, uint32_t max_blocks,
@@ -144,8 +149,10 @@ int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens
  * but are not read). With *d_prefix_len = 0 this is plain decoding attention. kv_len 0 gives zeros.
  *  d_prefix_pages  device, [n_prefix_pages] (NULL if n_prefix_pages is 0); d_prefix_len: device, one value
  *  d_work          shn_kv_attn_shared_workspace_bytes, 256-byte aligned
- * Other arguments, arithmetic and device errors as shn_kv_attn_prompt; *d_prefix_len that the pages cannot hold is taken
- * as what they hold (SHN_ERR_INVALID_ARG).
+ * Other arguments and device errors as shn_kv_attn_prompt; *d_prefix_len that the pages cannot hold is taken as what they
+ * hold (SHN_ERR_INVALID_ARG). Arithmetic: as there for a prefix with 32 or more query rows per key head (n_reqs *
+ * q_heads / kv_heads); for a smaller one and for the requests' own tokens values enter exactly too, their scales with the
+ * weights (which are rounded to fp16 once), and parts of a query below 2^-25 of its largest are lost.
  */
 size_t shn_kv_attn_shared_workspace_bytes(const shn_kv_cache* cache, uint32_t n_reqs, uint32_t q_heads);
 int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, uint32_t q_heads,

@@ -5,8 +5,11 @@ import random
 import pytest
 import torch
 
-from entropy_coded_lossless_b200 import kv, shn
-from tests import kv_spec as spec
+from entropy_coded_lossless_b200 import build as shn_build
+
+shn_build.build()  # the binding is an extension module: it is there before it is imported
+from entropy_coded_lossless_b200 import kv, shn  # noqa: E402
+from tests import kv_spec as spec  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -441,6 +444,7 @@ def shared_tables(own, prefix, pt, seed):
 @pytest.mark.parametrize("h,hk,d,pt,prefix,own", [
     (8, 2, 128, 16, 0, [1]),
     (8, 2, 128, 16, 0, [0, 1, 700, 64, 65]),
+    (8, 2, 128, 16, 0, [n % 50 for n in range(20)]),
     (32, 8, 128, 16, 1008, [3, 200, 0, 17]),
     (4, 4, 64, 32, 64, [1, 2, 3, 300, 31, 33]),
     (24, 4, 64, 32, 4096, [n * 7 % 300 for n in range(33)]),

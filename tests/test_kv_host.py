@@ -6,7 +6,9 @@ import pytest
 import torch
 
 from entropy_coded_lossless_b200 import build as shn_build
-from entropy_coded_lossless_b200 import kv, shn
+
+shn_build.build()  # the binding is an extension module: it is there before it is imported
+from entropy_coded_lossless_b200 import kv, shn  # noqa: E402
 
 BAD, UNSUP, WORK = shn.SHN_ERR_INVALID_ARG, shn.SHN_ERR_UNSUPPORTED, shn.SHN_ERR_WORKSPACE
 P = 1 << 20  # 256-byte aligned
