@@ -192,7 +192,15 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_kernel(KvPages c, K
       for (int d = kLanes / 2; d; d >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
       if (row >= kv1) continue;
       const float scale = max_nan(top, 1e-30f) / 127.f, inverse = 1.f / scale;
-      const uint64_t by = pack2(inverse, inverse), round = pack2(12582912.f, 12582912.f);
+      // y / scale in float32: times the reciprocal, and one residual step that leaves it correctly rounded but for rare
+      // last-bit cases (P. Markstein, IBM J. Res. Dev. 34, 1990)
+      const uint64_t by = pack2(inverse, inverse), minus = pack2(-scale, -scale), round = pack2(12582912.f, 12582912.f);
+      uint64_t n[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t near = mul2(v.x[e], by);
+        n[e] = add2(fma2(fma2(near, minus, v.x[e]), by, near), round);
+      }
       uint32_t w[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
