@@ -63,8 +63,12 @@ int check_attn(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32
   return SHN_OK;
 }
 
-// From this many query rows per key head on, the prefix goes to the tensor core kernel.
-constexpr uint64_t kPrefixRows = 32;
+// Which kernel the prefix goes to. The single-token kernel reads it once for each 8 (16) query rows, about 1.5 ns a unit of 32
+// tokens; the tensor core kernel serves 256 rows at once but takes some 12 us to start and end. Measured (32 query and 8
+// key heads of 128, microseconds of a call with 16 own tokens each, single-token kernel / tensor cores): 8 requests 1024 tokens
+// 18.4 / 26.6, 8192 tokens 28.7 / 34.8; 16 requests 1024 tokens 20.5 / 26.7, 8192 tokens 41.0 / 36.8. So tensor cores from
+// kPrefixUnits units on, and for more row groups than the workspace keeps places for.
+constexpr uint64_t kPrefixUnits = 12288, kPrefixGroups = 64;
 constexpr uint64_t kSplitBlocks = 148;
 
 // How shn_kv_attn_shared is cut up, and its workspace: [status 256][pieces' sums][pieces' (mt, ms, l)].
@@ -76,16 +80,16 @@ struct SharedLayout {
 SharedLayout shared_layout(const shn_kv_cache* c, uint32_t n_reqs, uint32_t q_heads) {
   SharedLayout x = {};
   const uint32_t group = q_heads / c->kv_heads;
-  x.pl.rows = group <= 8 ? 8 : 16;  // the rows of one mma are 8; 16 share what is done for a token's bytes
+  // The rows of one mma are 8; 16 share what is done for a token's bytes (groups of 16, 32 requests of 2048 tokens: 36.9 us
+  // against 41.0 with two groups of 8 each).
+  x.pl.rows = group <= 8 ? 8 : 16;
   x.pl.own_groups = (group + x.pl.rows - 1) / x.pl.rows;
   const uint64_t rows = (uint64_t)n_reqs * group;
-  if (rows >= kPrefixRows) {
-    // as many parts as give every SM one block of the tensor core kernel
-    const uint64_t blocks = (rows + 255) / 256 * c->kv_heads;
-    x.pl.splits = blocks >= kSplitBlocks ? 1 : (uint32_t)(kSplitBlocks / blocks);
-  } else {
-    x.pl.prefix_groups = (uint32_t)((rows + x.pl.rows - 1) / x.pl.rows);
-  }
+  // for the tensor cores: as many parts as give every SM one block
+  const uint64_t blocks = (rows + 255) / 256 * c->kv_heads;
+  x.pl.splits = blocks >= kSplitBlocks ? 1 : (uint32_t)(kSplitBlocks / blocks);
+  const uint64_t groups = (rows + x.pl.rows - 1) / x.pl.rows;
+  x.pl.prefix_groups = groups <= kPrefixGroups ? (uint32_t)groups : 0;
   const uint64_t segs = (uint64_t)c->kv_heads * (x.pl.prefix_groups + (uint64_t)n_reqs * x.pl.own_groups);
   const uint64_t pieces = (kDecodeMaxWarps + segs) * x.pl.rows;
   const uint64_t parts = (uint64_t)x.pl.splits * n_reqs * q_heads;
@@ -242,9 +246,16 @@ int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, 
   x.pl.ml = reinterpret_cast<float4*>(wb + x.ml_off);
   x.pl.split_out = reinterpret_cast<float*>(wb + x.split_off);
   x.pl.split_ml = reinterpret_cast<float4*>(wb + x.split_ml_off);
-  // no more parts than the prefix can have tiles of 128 tokens
-  const uint64_t tiles = ((uint64_t)n_prefix_pages * cache->page_tokens + 127) / 128;
-  if (x.pl.splits > tiles) x.pl.splits = (uint32_t)tiles;
+  const uint64_t prefix_cap = (uint64_t)n_prefix_pages * cache->page_tokens;
+  const uint64_t prefix_units = x.pl.prefix_groups * (uint64_t)cache->kv_heads * ((prefix_cap + kUnit - 1) / kUnit);
+  if (prefix_cap && (!x.pl.prefix_groups || prefix_units >= kPrefixUnits)) {
+    x.pl.prefix_groups = 0;
+    // no more parts than the prefix can have tiles of 128 tokens
+    if (x.pl.splits > (prefix_cap + 127) / 128) x.pl.splits = (uint32_t)((prefix_cap + 127) / 128);
+  } else {
+    x.pl.splits = 0;
+    if (!prefix_cap) x.pl.prefix_groups = 0;
+  }
   // warps: two blocks on each SM (one for 16 rows, which takes more registers), but no more than there can be units
   const uint64_t units = (uint64_t)cache->kv_heads * x.pl.prefix_groups * (((uint64_t)n_prefix_pages * cache->page_tokens + kUnit - 1) / kUnit) +
                          (uint64_t)n_reqs * cache->kv_heads * x.pl.own_groups * (((uint64_t)max_blocks * cache->page_tokens + kUnit - 1) / kUnit + 1);

@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t s) {
-  // one block up to 2 tokens a thread: a second launch costs about what they do
+  // one block up to 2 tokens a thread: a second launch costs about what they do (4.7 against 5.5 us at 900 tokens, 5.6 both at
+  // 1900, 7.8 against 5.5 at 3900)
   if (a.max_tokens <= 2 * kThreads) {
     kv_plan_kernel<true><<<1, kThreads, 0, s>>>(a);
     return cudaGetLastError();

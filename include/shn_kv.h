@@ -150,8 +150,8 @@ int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens
  *  d_prefix_pages  device, [n_prefix_pages] (NULL if n_prefix_pages is 0); d_prefix_len: device, one value
  *  d_work          shn_kv_attn_shared_workspace_bytes, 256-byte aligned
  * Other arguments and device errors as shn_kv_attn_prompt; *d_prefix_len that the pages cannot hold is taken as what they
- * hold (SHN_ERR_INVALID_ARG). Arithmetic: as there for a prefix with 32 or more query rows per key head (n_reqs *
- * q_heads / kv_heads); for a smaller one and for the requests' own tokens values enter exactly too, their scales with the
+ * hold (SHN_ERR_INVALID_ARG). Arithmetic: as there for a large prefix (many query rows, many tokens); for a
+ * smaller one and for the requests' own tokens values enter exactly too, their scales with the
  * weights (which are rounded to fp16 once), and parts of a query below 2^-25 of its largest are lost.
  */
 size_t shn_kv_attn_shared_workspace_bytes(const shn_kv_cache* cache, uint32_t n_reqs, uint32_t q_heads);

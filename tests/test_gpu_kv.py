@@ -475,6 +475,61 @@ def test_shared_prefix_inside_a_page_and_shorter_requests():
         assert (out[6] == 0).all()
 
 
+@pytest.mark.parametrize("d,pt,prefix", [(128, 32, 1), (64, 32, 127), (128, 32, 129), (64, 16, 1000), (128, 1024, 3000), (64, 1024, 2049)])
+def test_shared_prefix_of_many_rows(d, pt, prefix):
+    """Over a thousand query rows to a key head (the tensor core kernel, in parts that may begin inside a long page): a prefix that
+    ends inside a page or a tile, requests shorter than it, empty ones, and one part without a token."""
+    hk, h, n = 2, 32, 70
+    rng = random.Random(prefix)
+    own = [rng.choice([0, prefix // 3, prefix, prefix + rng.randint(1, 300)]) for _ in range(n)]
+    own[3], own[4] = prefix + 310, 0
+    table, pages = tables(own, pt, 5)
+    cache = filled_cache(pages, hk, pt, d, seed=6)
+    out = run_shared(cache, table, own, prefix, h, d, seed=prefix)
+    assert (out[4] == 0).all()
+    run_shared(cache, table, own, prefix, h, d, seed=prefix + 1, scale=0.5, strided=True)
+
+
+@pytest.mark.parametrize("n", [4, 70])
+def test_shared_prefix_with_scales_that_are_not_finite(n):
+    """Infinite and NaN value scales: in tokens of the prefix that only the longer requests see, and behind everyone's end."""
+    hk, h, d, pt, prefix = 2, 32, 128, 32, 300
+    own = [prefix + 5 if r % 2 else 200 for r in range(n)]
+    table, pages = tables(own, pt, 5)
+    cache = filled_cache(pages, hk, pt, d, seed=6)
+    clean = run_shared(cache, table, own, prefix, h, d, seed=1)
+    long = next(r for r in range(n) if own[r] > prefix)
+    for t in (250, 299):  # behind the short ones' end
+        s = spec.token_slots(table[long], pt, 300)[t].item()
+        cache.v_scale[s // pt, :, s % pt] = math.inf if t == 250 else math.nan
+    for r in range(n):
+        last = own[r] % pt
+        cache.v_scale[table[r, own[r] // pt].item(), :, last] = math.nan  # behind the end, in the last page
+    q, out, w = bf16(n, h, d, seed=1), torch.zeros(n, h, d, dtype=torch.bfloat16, device=DEV), work(kv.attn_shared_workspace_bytes(cache, n, h))
+    kv.shn_kv_attn_shared(q, cache, table[long, :10].contiguous(), ints([prefix]), table, ints(own), 1 / math.sqrt(d), out, w)
+    assert status(w) == (0, 0)
+    for r in range(n):
+        if own[r] < prefix:
+            assert torch.equal(out[r], clean[r])
+        else:
+            assert not torch.isfinite(out[r].float()).any()
+
+
+def test_shared_bad_pages_of_a_prefix_of_many_rows():
+    hk, h, d, pt, n, prefix = 2, 32, 128, 32, 70, 320
+    own = [prefix + 3] * n
+    table, pages = tables(own, pt, 5)
+    cache = filled_cache(pages, hk, pt, d, seed=6)
+    q, out, w = bf16(n, h, d, seed=1), torch.zeros(n, h, d, dtype=torch.bfloat16, device=DEV), work(kv.attn_shared_workspace_bytes(cache, n, h))
+    for bad in (-1, pages, 2**31 - 1):
+        front = table[0, :10].clone()
+        front[4] = bad
+        kv.shn_kv_attn_shared(q, cache, front, ints([prefix]), table, ints(own), 0.1, out, w)
+        assert status(w)[0] == shn.SHN_ERR_INVALID_ARG and torch.isfinite(out.float()).all()
+    kv.shn_kv_attn_shared(q, cache, table[0, :10].contiguous(), ints([prefix]), table, ints(own), 0.1, out, w)
+    assert status(w) == (0, 0)
+
+
 def test_shared_equals_prompt_of_one_token():
     own = [77, 1, 260]
     table, pages = tables(own, 16, 1)
