@@ -1,28 +1,38 @@
 // kv_attn_tc.cu — attention of many query rows over the paged INT8 cache on the tensor cores: packed causal
-// prompts (shn_kv_attn_prompt).
+// prompts (shn_kv_attn_prompt), and parts of a prefix that many single-token requests share (shn_kv_attn_shared).
 //
 // A block takes 256 rows of one key head: row = (query, head of the group), so every key and value it reads serves all
 // heads of the group, whatever their number. It walks the sequence in tiles of 128 tokens:
 //   S = Q K^T      tcgen05.mma, fp16, M = 128 rows, N = 64 tokens, for rows 0-127 and 128-255 and both halves, into TMEM
 //   s = S * k_scale_j * softmax_scale * log2(e);  p = 2^(s - m);  l += p;  P = fp16(p)
 //   O += P V       tcgen05.mma, fp16, P read from TMEM (it takes the place of S)
-// Keys enter as the integers, which bf16 holds exactly, and their scales are applied to the float32 scores: scores have
-// float32's error. Values enter as fp16(int8 * v_scale * 2^-e), e the exponent of the largest value scale of 32 tokens, the
-// product formed to more than fp16's 11 bits and rounded once; the weights are rounded to fp16 (2^-11 each, where bf16 operands
-// would cost 2^-8 twice). The power of two goes into the weights: P = p 2^(e - E), with E the exponent O is held in, raised
-// like the softmax's reference when a tile's values are more than 2^7 larger. A weight smaller than 2^-24 of that range is
-// lost, so O is exact to 2^-24 of the largest value of the sequence, or 2^-11 of what is summed.
+// Queries enter with one power of two for the block taken out, which fp16 then holds exactly down to 2^-32 of the largest;
+// keys as the integers, and their scales are applied to the float32 scores: scores have float32's error. Values enter as
+// fp16(int8 * fp16(v_scale * 2^-e)), e the exponent of the largest value scale of 32 tokens; weights, values and their
+// scales are rounded to fp16's 11 bits each (with bf16's 8 the results, rounded to bf16 themselves, were off by 0.0024 instead
+// of 0.0017 in the mean). The power of two goes into the weights: P = p 2^(e - E), with E the exponent O is held in, raised
+// like the softmax's reference when values are more than 2^7 larger. A weight smaller than 2^-24 of that range is
+// lost, so O is exact to 2^-24 of the largest value of the sequence.
 //
-// Softmax in one pass: m is a running maximum in units of log2. It is only raised when a row's maximum grows by more
-// than 8, i.e. a weight may reach 2^8 before the sums are scaled down: that is exact in float32 and bf16 alike
-// (a power-of-two range, no rounding) and spares almost every rescaling of O after a row's first tiles.
+// Softmax in one pass over the scores, without a search for the maximum: m is the maximum of a row's first 64 scores, and a
+// thread's sum of 16 weights shows whether one of the later ones is above it by 2^8; only then m is raised, and what is
+// summed scaled down. Sums of weights are float32.
 //
 // Roles (896 threads): warps 0-7 and 8-15 the softmax of the two row tiles (16 rows to a warp, so that each scheduler
-// has four of them to hide their latencies), warps 16-23 fetch the tiles and turn INT8 into bf16 operands in shared memory,
-// warps 24 and 25 issue the products of a row tile each. While the softmax of one row tile works, the
-// products of the other run. Two K and two V buffers; the next tile's bytes are on their way in registers while the present
-// one is converted.
-// TMEM (512 columns): S0, S1 (128 each; P in their first 64), O0, O1 (D each).
+// has four of them to hide their latencies), warps 16-23 fetch the tiles and turn INT8 into fp16 operands in shared memory,
+// warps 24 and 25 issue the products of a row tile each. Two K and two V buffers; the next operand's bytes are on their
+// way in registers while the present one is converted. TMEM (512 columns): O0, O1 (D each) and for each row tile 128
+// columns in which a tile's two halves of S, the weights in their place and the next tile's first half take turns.
+//
+// What bounds it. 8192 causal tokens, 32 query and 8 key heads of 128: 700 us in a run of calls, 785 TFLOP/s, 48 % of the
+// measured bf16 rate (630 us and 53 % for the call alone in a graph). A tile of 256 x 128 scores costs a block about 4400
+// cycles; the products would take 2048 of them (1024 at D = 64) and so would the exponentials, at 16 a cycle; issuing the
+// instructions of softmax, conversion and waits takes some 3000 of each scheduler. So the softmax sets the pace, by its
+// instructions and their latency, and products and fetches run behind it.
+// The steps, same case: a thread per row with its 128 scores in registers 1458 us; a row shared by four threads, so that a
+// column's scale is read for two rows, 1193; 16 softmax warps 759; two issuing warps, halves with scores formed ahead and no
+// search for the maximum 716; whole lines out and a shorter block start 700. Tried and not kept: 8 softmax warps of 32
+// rows, and blocks of all requests in the order of their lengths.
 #include <type_traits>
 
 #include "kv_decode.cuh"
@@ -42,11 +52,11 @@ constexpr uint32_t kRows = 256;      // query rows of a block
 constexpr float kRise = 256.f;       // how far a weight may pass 1 before the reference is raised,
 constexpr float kValueRise = 7.f;    // and (log2) the values the range O is held in: 2^15 together, within fp16
 constexpr float kValueFall = -60.f, kValueFall2 = 1ull << 60;  // a tile this far below adds nothing to O in fp16
-constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows of 64 bf16
+constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows of 64 fp16
 
 template <int D>
 struct Layout {
-  static constexpr uint32_t kOperand = 128 * D * 2;  // one 128 x D bf16 operand
+  static constexpr uint32_t kOperand = 128 * D * 2;  // one 128 x D fp16 operand
   static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, info = scale + 4 * 512, row_sum = info + 128, bars = row_sum + 8 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
 };
 // barriers
@@ -355,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         const bool edge = __any_sync(~0u, first - (int32_t)col + 64 > min(seen[0], seen[1]));
         float sum[2];
         // Weights against the reference that stands; no maximum is searched first. A thread's sum of a row's 16 weights shows
-        // whether one of them has passed the limit, which almost never happens: this one pass is all then. (Two versions: only tiles at the end of what a row
-        // sees look at the columns' places.)
+        // whether one of them has passed the limit, which almost never happens: this one pass is all then. (Two versions:
+        // only tiles at the end of what a row sees look at the columns' places.)
         auto weights = [&](auto edge_tag) {
           constexpr bool kEdge = decltype(edge_tag)::value;
 #pragma unroll
@@ -660,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp < kIssueWarp + 2 && tiles) {
       const uint32_t i = warp - kIssueWarp;
-      constexpr uint32_t kS = instr_desc(128, 64, false, false), kO = instr_desc(128, D, false, true);
+      constexpr uint32_t kS = instr_desc(128, 64, false), kO = instr_desc(128, D, true);
       const bool lead = elect_one();
       // Both for the tokens 64 h .. 64 h + 63 of tile j.
       auto scores = [&](uint32_t j, uint32_t h) {

@@ -184,9 +184,14 @@ PyObject* store(PyObject*, PyObject* const* v, Py_ssize_t n) {
       n_pos = t.size(0), rot = t.size(1);
     }
     if (k.tokens > UINT32_MAX || n_pos > UINT32_MAX || rot > UINT32_MAX || q.heads > UINT32_MAX) throw std::invalid_argument("a tensor is too long");
+    const int pairs = PyObject_IsTrue(a.v[13]);
+    if (pairs < 0) {
+      PyErr_Clear();
+      throw std::invalid_argument("pairs must be true or false");
+    }
     const On on(a, 14);
     return shn_kv_store(q.p, q.stride, (uint32_t)q.heads, k.p, k.stride, x.p, x.stride, (uint32_t)k.tokens, pos, slots, wq, wk, a.f(11), cs,
-                        (uint32_t)n_pos, (uint32_t)rot, PyObject_IsTrue(a.v[13]) ? 1 : 0, c, o.p, o.stride, w, bytes, on.stream);
+                        (uint32_t)n_pos, (uint32_t)rot, (uint32_t)pairs, c, o.p, o.stride, w, bytes, on.stream);
   });
 }
 

@@ -121,6 +121,7 @@ int shn_kv_plan(const int32_t* d_ctx_len, const int32_t* d_new_len, uint32_t n_r
   if (max_tokens && (!d_positions || !d_slots)) return SHN_ERR_INVALID_ARG;
   const int e = check_work(d_work, work_bytes, SHN_KV_WORKSPACE_BYTES);
   if (e != SHN_OK) return e;
+  if (n_reqs && (d_kv_len == d_ctx_len || d_kv_len == d_new_len)) return SHN_ERR_INVALID_ARG;  // every block reads these
   KvPlanArgs a;
   a.ctx = d_ctx_len, a.fresh = d_new_len, a.n = n_reqs, a.log2_pt = log2_of(page_tokens);
   a.max_blocks = max_blocks, a.n_free = n_free, a.max_tokens = max_tokens;
@@ -200,6 +201,7 @@ int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens
   if (n_reqs && !d_cu_q) return SHN_ERR_INVALID_ARG;
   e = check_work(d_work, work_bytes, SHN_KV_WORKSPACE_BYTES);
   if (e != SHN_OK) return e;
+  if (n_tokens && d_q == d_out) return SHN_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   KvAttnArgs a = {};
   a.q = d_q, a.q_stride = q_stride, a.n_tokens = n_tokens, a.q_heads = q_heads;
@@ -232,6 +234,7 @@ int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, 
   SharedLayout x = shared_layout(cache, n_reqs, q_heads);
   e = check_work(d_work, work_bytes, x.total);
   if (e != SHN_OK) return e;
+  if (n_reqs && d_q == d_out) return SHN_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   KvAttnArgs a = {};
   a.q = d_q, a.q_stride = q_stride, a.n_tokens = n_reqs, a.q_heads = q_heads;

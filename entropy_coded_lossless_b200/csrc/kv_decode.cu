@@ -14,6 +14,9 @@
 // The reference m is raised only when a score passes it by 8, and E, the exponent the sums are held in, when a value scale
 // is more than 2^7 above it (2^15 together, within fp16): almost every step does without a reduction across lanes. A
 // weight below 2^-25 of that range is lost, so the sums are exact to 2^-24 of the sequence's largest value.
+//
+// Measured (32 query and 8 key heads of 128, 128 requests with 1024 own tokens each): 53 us for 282 MB, 5.3 TB/s, 81 % of
+// the measured copy rate. The join then reads what the parts of the prefix and the pieces left for each row: 15 us.
 #include <type_traits>
 
 #include "kv_decode.cuh"
@@ -554,13 +557,16 @@ cudaError_t launch(const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, 
   e = pl.rows == 8 ? launch_behind(kv_decode_kernel<D, 1>, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl)
                    : launch_behind(kv_decode_kernel<D, 2>, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl);
   if (e != cudaSuccess) return e;
-  // few rows may have hundreds of pieces each: as many warps to a row as make twice the warps that ran before, 8 at most
-  const uint32_t items = a.n_reqs * a.q_heads;
-  const uint64_t twice = items;
-  if (twice > pl.warps) return launch_behind(kv_join_kernel<D, 1>, dim3((items + 7) / 8), kDecodeThreads, 0, s, c, a, pl);
-  if (2 * twice > pl.warps) return launch_behind(kv_join_kernel<D, 2>, dim3((items + 3) / 4), kDecodeThreads, 0, s, c, a, pl);
-  if (4 * twice > pl.warps) return launch_behind(kv_join_kernel<D, 4>, dim3((items + 1) / 2), kDecodeThreads, 0, s, c, a, pl);
-  return launch_behind(kv_join_kernel<D, 8>, dim3(items), kDecodeThreads, 0, s, c, a, pl);
+  // Few rows may have hundreds of pieces each, many rows only a few. A row gets 2, 4 or 8 warps while fewer than that share of
+  // the decoding warps' number is asked for: so the join has about the warps that the decode had, up to twice as many.
+  // Measured: 128 rows, a call 11.5 us against 21.6 with one warp to a row; 792 rows 25.2, one warp 33.8, eight 27.6; 4096
+  // rows 126 (one warp), eight 145.
+  const uint64_t rows = (uint64_t)a.n_reqs * a.q_heads;
+  const uint32_t n = (uint32_t)rows;
+  if (rows > pl.warps) return launch_behind(kv_join_kernel<D, 1>, dim3((n + 7) / 8), kDecodeThreads, 0, s, c, a, pl);
+  if (2 * rows > pl.warps) return launch_behind(kv_join_kernel<D, 2>, dim3((n + 3) / 4), kDecodeThreads, 0, s, c, a, pl);
+  if (4 * rows > pl.warps) return launch_behind(kv_join_kernel<D, 4>, dim3((n + 1) / 2), kDecodeThreads, 0, s, c, a, pl);
+  return launch_behind(kv_join_kernel<D, 8>, dim3(n), kDecodeThreads, 0, s, c, a, pl);
 }
 
 }  // namespace

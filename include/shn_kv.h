@@ -63,6 +63,7 @@ int shn_kv_check_cache(const shn_kv_cache* c);
  *  d_kv_len       device, [n_reqs]: ctx + new
  *  d_positions, d_slots  device, [max_tokens]: position and slot of each new token, requests one after
  *                 another; behind the last token position 0 and slot -1
+ * Outputs overlap neither each other nor inputs, but for d_free_next (d_kv_len that is d_ctx_len or d_new_len is refused).
  * A page that is shared with another request must not be extended: let shared prefixes end with a page.
  * Device errors: SHN_ERR_CAPACITY (more than max_tokens new tokens, a row of more than max_blocks pages,
  * too few free pages), SHN_ERR_INVALID_ARG (a negative length, a head outside [0, n_free]). After these no
@@ -123,14 +124,15 @@ int shn_kv_load(const shn_kv_cache* cache, const int32_t* d_slots, uint32_t n_to
  *   s_j = softmax_scale * (q . k_j);  out = sum_j softmax(s)_j v_j, k_j and v_j = int8 * scale
  * A query that sees nothing (kv_len < n) gives zeros. Rows of d_out behind d_cu_q[n_reqs] stay as they were.
  *  d_q, d_out  device, [n_tokens][q_heads][head_dim] bfloat16, tokens *_stride values apart (a multiple of 8),
- *              16-byte aligned; they do not overlap
+ *              16-byte aligned; they do not overlap (one
+ *              that is the other is refused)
  *  q_heads     a multiple of kv_heads, at most 64 * kv_heads
  * Arithmetic: queries and keys enter the products exactly (parts of a query 2^-32 of the largest of its block of 256 rows
  * aside), scores, their scalings, the softmax and the sums are float32. Before the second product a weight is rounded to
  * fp16, and a value is fp16(int8 * fp16(scale)): 2^-11 each. Weights below 2^-24 times the ratio of the largest value scale of the
  * sequence to the token's are lost, so results are exact to 2^-24 of the sequence's largest value.
- * A token whose value scale is not finite (or 1e36 and more) makes the rows that see it NaN; rows that do not see a token are
- * not touched by what stands there, nor by what stands behind a sequence's end in its last page.
+ * A token whose value scale is not finite (or 1e36 and more) makes the rows that see it NaN; rows that do not see a
+ * token are not touched by what stands there, nor by what stands behind a sequence's end in its last page.
  * Device errors: SHN_ERR_INVALID_ARG for a page id outside the cache (detail = the request; that page counts as zeros),
  * a d_kv_len that the table row cannot hold (taken as what it holds) or a d_cu_q that decreases or leaves
  * [0, n_tokens] (those queries are left out); SHN_ERR_TIMEOUT if a wait inside a kernel gave up (a quarter of a second; the
@@ -152,7 +154,9 @@ int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens
  * Other arguments and device errors as shn_kv_attn_prompt; *d_prefix_len that the pages cannot hold is taken as what they
  * hold (SHN_ERR_INVALID_ARG). Arithmetic: as there for a large prefix (many query rows, many tokens); for a
  * smaller one and for the requests' own tokens values enter exactly too, their scales with the
- * weights (which are rounded to fp16 once), and parts of a query below 2^-25 of its largest are lost.
+ * weights (which are rounded to fp16 once), and parts of a query below 2^-25 of its largest are lost. The parts of a row meet
+ * in float32 before they are divided by the sum of the weights: a sum of weights times values above 3.4e38 is infinite. A
+ * token whose value scale is not finite makes the rows that see it NaN or infinite.
  */
 size_t shn_kv_attn_shared_workspace_bytes(const shn_kv_cache* cache, uint32_t n_reqs, uint32_t q_heads);
 int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, uint32_t q_heads,

@@ -110,6 +110,14 @@ def test_shared_refusals(lib, over, code):
     assert lib.shn_kv_attn_shared(*f.values()) == code
 
 
+def test_calls_refuse_outputs_that_are_inputs(lib):
+    a, b = P + 4096, P + 8192
+    assert plan(lib, new=a) == BAD and plan(lib, ctx=a) == BAD  # kv_len is the other one
+    c = ctypes.byref(cache())
+    assert lib.shn_kv_attn_prompt(a, 4096, 50, 32, c, P, 16, P, P, 3, 0.1, a, 4096, b, 1 << 40, None) == BAD
+    assert lib.shn_kv_attn_shared(a, 4096, 3, 32, c, P, 16, P, P, 16, P, 0.1, a, 4096, b, 1 << 40, None) == BAD
+
+
 def test_shared_workspace_query(lib):
     c = cache()
     one, many = (lib.shn_kv_attn_shared_workspace_bytes(ctypes.byref(c), n, 32) for n in (1, 300))
