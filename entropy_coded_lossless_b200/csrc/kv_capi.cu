@@ -162,9 +162,8 @@ int shn_kv_store(const uint16_t* d_q, uint64_t q_stride, uint32_t q_heads, const
   a.q_weight = d_q_weight, a.k_weight = d_k_weight, a.eps = eps;
   a.cos_sin = d_cos_sin, a.n_positions = n_positions, a.rot = rot_dim, a.pairs = pairs;
   a.q_out = d_q_out, a.q_out_stride = q_out_stride;
-  a.st = clear_status(d_work, s);
-  if (!a.st) return SHN_ERR_CUDA;
-  if (n_tokens == 0) return SHN_OK;
+  a.st = static_cast<DeviceStatus*>(d_work);  // set or cleared by the launches
+  if (n_tokens == 0) return clear_status(d_work, s) ? SHN_OK : SHN_ERR_CUDA;
   return launch_kv_store(pages_of(cache), d, a, sm_count_for_launch(), s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
 }
 
@@ -185,9 +184,8 @@ int shn_kv_load(const shn_kv_cache* cache, const int32_t* d_slots, uint32_t n_to
   KvLoadArgs a;
   a.slots = d_slots, a.n_tokens = n_tokens, a.k_out = d_k_out, a.v_out = d_v_out;
   a.k_stride = k_stride, a.v_stride = v_stride;
-  a.st = clear_status(d_work, s);
-  if (!a.st) return SHN_ERR_CUDA;
-  if (n_tokens == 0 || (!d_k_out && !d_v_out)) return SHN_OK;
+  a.st = static_cast<DeviceStatus*>(d_work);  // as above
+  if (n_tokens == 0 || (!d_k_out && !d_v_out)) return clear_status(d_work, s) ? SHN_OK : SHN_ERR_CUDA;
   return launch_kv_load(pages_of(cache), cache->head_dim, a, s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
 }
 

@@ -10,6 +10,49 @@ __global__ void kv_begin_kernel(DeviceStatus* st) {
   if (threadIdx.x == 0) st->status = 0, st->detail = 0;
 }
 
+// The status of a call whose errors its indexes alone show. Up to kOneTokens tokens (kOne) one block looks at all of them in
+// one turn and is the only one to write the status, so no kernel has to clear it first: 64 tokens stored and loaded again
+// 4.97 us against 6.25 with one in front of each (in a run of calls 8.2 and 10.6), 8191 of them 63.7 against 64.9. With more
+// tokens that block would need more turns than others do, and its registers cost the others places (65,536 tokens loaded in
+// 88.7 us against 75.9): then the kernel in front clears the status and every block reports what it finds.
+constexpr int kThreads = 256, kAhead = 8;  // (16-byte loads of a thread on their way together)
+constexpr uint32_t kOneTokens = 4 * kAhead * kThreads;
+// The first of the n indexes that is outside [0, end); negative ones are fine where kNone.
+template <bool kNone>
+__device__ __forceinline__ uint32_t first_outside(const int32_t* p, uint32_t n, uint32_t end) {
+  const uint32_t t = threadIdx.x;
+  const uint32_t lead = min(n, (uint32_t)(-(reinterpret_cast<uintptr_t>(p) >> 2) & 3)), quads = (n - lead) / 4, tail = lead + 4 * quads;
+  uint32_t first = 0xFFFFFFFFu;
+  auto look = [&](int32_t x, uint32_t at) {
+    if (!(kNone && x < 0) && (uint32_t)x >= end) first = min(first, at);
+  };
+  if (t < lead) look(p[t], t);
+  if (tail + t < n) look(p[tail + t], tail + t);
+  const int4* v = reinterpret_cast<const int4*>(p + lead);
+  int4 x[kAhead];
+#pragma unroll
+  for (int e = 0; e < kAhead; ++e) {
+    const uint32_t i = e * kThreads + t;
+    if (i < quads) x[e] = v[i];
+  }
+#pragma unroll
+  for (int e = 0; e < kAhead; ++e) {
+    const uint32_t i = e * kThreads + t, at = lead + 4 * i;
+    if (i < quads) look(x[e].x, at), look(x[e].y, at + 1), look(x[e].z, at + 2), look(x[e].w, at + 3);
+  }
+  return first;
+}
+__device__ __forceinline__ void write_status(DeviceStatus* st, uint32_t first) {
+  __shared__ uint32_t least[kThreads / 32];
+  first = __reduce_min_sync(~0u, first);
+  if ((threadIdx.x & 31) == 0) least[threadIdx.x >> 5] = first;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int i = 1; i < kThreads / 32; ++i) first = min(first, least[i]);
+  st->status = first == 0xFFFFFFFFu ? SHN_OK : SHN_ERR_INVALID_ARG;
+  st->detail = first == 0xFFFFFFFFu ? 0 : first;
+}
+
 // ---- shn_kv_store -------------------------------------------------------------------------------
 // HBM-bound: every value is read and written once. A head row of D values is held by D/8 lanes, 8 values each: 4
 // consecutive ones twice, the second 4 where the rotation's partners of the first are (half the rotated part further on), so a
@@ -21,7 +64,6 @@ __global__ void kv_begin_kernel(DeviceStatus* st) {
 // rounded by adding 1.5 * 2^23, which leaves the integer in the last byte.
 // Measured (8191 tokens, 32 query and 8 key heads of 128): 54 us for 190 MB, 3.5 TB/s, with 62 % of the issue slots taken. With
 // the tokens dealt out by a division, a block each, a call and the load behind it took 89 us; like this 68.
-constexpr int kStoreThreads = 256;
 constexpr int kAtOnce = 4;  // query rows of a lane that are on their way together
 
 // A lane's 8 values of a row, two by two: [0], [1] the first 4, [2], [3] the other 4.
@@ -68,10 +110,17 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kStoreThreads, 3) kv_store_kernel(KvPages c, KvStoreArgs a) {
+template <int D, bool kOne>
+__global__ void __launch_bounds__(kThreads, 3) kv_store_kernel(KvPages c, KvStoreArgs a) {
   using namespace tc;
-  constexpr uint32_t kLanes = D / 8, kGroups = kStoreThreads / kLanes;
+  constexpr uint32_t kLanes = D / 8, kGroups = kThreads / kLanes;
+  if (kOne && blockIdx.x == 0) {
+    if (blockIdx.y) return;
+    uint32_t first = first_outside<true>(a.slots, a.n_tokens, c.n_pages << c.log2_pt);
+    if (a.rot) first = min(first, first_outside<false>(a.positions, a.n_tokens, a.n_positions));
+    return write_status(a.st, first);
+  }
+  const uint32_t block = blockIdx.x - kOne, blocks = gridDim.x - kOne;
   const uint32_t lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   // The block's share of the query rows, and of the key and value rows (keys first); all lanes of a warp run the same
   // number of turns (the shuffles are full).
@@ -125,20 +174,20 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_kernel(KvPages c, K
     }
   };
   // a block's tokens one after another; the next one's slot and position are read a turn ahead
-  int32_t slot = blockIdx.x < a.n_tokens ? a.slots[blockIdx.x] : -1, pos = a.rot && blockIdx.x < a.n_tokens ? a.positions[blockIdx.x] : 0;
-  after_previous();
-  for (uint32_t token = blockIdx.x; token < a.n_tokens; token += gridDim.x) {
+  int32_t slot = a.slots[block], pos = a.rot ? a.positions[block] : 0;
+  if constexpr (!kOne) after_previous();
+  for (uint32_t token = block; token < a.n_tokens; token += blocks) {
     q_src = a.q + (uint64_t)token * a.q_stride + d_lo;
     k_src = a.k + (uint64_t)token * a.k_stride + d_lo, v_src = a.v + (uint64_t)token * a.v_stride + d_lo;
     ask_q(q0);
     ask_kv(kv0 + sub);
     const int32_t slot_now = slot, pos_now = pos;
-    if (token + gridDim.x < a.n_tokens) {
-      slot = a.slots[token + gridDim.x];
-      if (a.rot) pos = a.positions[token + gridDim.x];
+    if (token + blocks < a.n_tokens) {
+      slot = a.slots[token + blocks];
+      if (a.rot) pos = a.positions[token + blocks];
     }
-    if ((slot_now >= 0 && ((uint32_t)slot_now >> c.log2_pt) >= c.n_pages) || (a.rot && (pos_now < 0 || (uint32_t)pos_now >= a.n_positions))) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) report(a.st, SHN_ERR_INVALID_ARG, token);
+    if ((slot_now >= 0 && ((uint32_t)slot_now >> c.log2_pt) >= c.n_pages) || (a.rot && (uint32_t)pos_now >= a.n_positions)) {
+      if (!kOne && threadIdx.x == 0 && blockIdx.y == 0) report(a.st, SHN_ERR_INVALID_ARG, token);
       continue;
     }
     Turn turn = {};
@@ -226,25 +275,27 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_kernel(KvPages c, K
 // the row together. A token's rows are a block's neighbours, so its slot is read from L1 by all but the first.
 // Measured (65,536 tokens, 8 heads of 128): 78 us for 407 MB, 5.2 TB/s, 80 % of the measured copy rate; a loop over rows with one
 // of them on its way took 97.
-constexpr int kLoadThreads = 256;
-
 __device__ __forceinline__ float int8_of(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
 
-template <int D>
-__global__ void __launch_bounds__(kLoadThreads) kv_load_kernel(KvPages c, KvLoadArgs a) {
+template <int D, bool kOne>
+__global__ void __launch_bounds__(kThreads) kv_load_kernel(KvPages c, KvLoadArgs a) {
   constexpr uint32_t kLanes = D / 16;
+  if (kOne && blockIdx.x == 0) {
+    if (blockIdx.y == 0) write_status(a.st, first_outside<true>(a.slots, a.n_tokens, c.n_pages << c.log2_pt));
+    return;
+  }
   const uint32_t lane = threadIdx.x % kLanes;
-  // rows of the block: tokens from blockIdx.x * tokens on, `parts` blocks to a token with more rows than a block has
-  const uint32_t sub = threadIdx.x / kLanes, kSubs = kLoadThreads / kLanes;
+  // rows of the block: so many tokens, or a part of one token's rows where it has more than a block
+  const uint32_t sub = threadIdx.x / kLanes, kSubs = kThreads / kLanes;
   const uint32_t tokens = max(1u, kSubs / c.kv_heads);
-  const uint32_t token = blockIdx.x * tokens + (tokens > 1 ? sub / c.kv_heads : 0);
+  const uint32_t token = (blockIdx.x - kOne) * tokens + (tokens > 1 ? sub / c.kv_heads : 0);
   const uint32_t h = tokens > 1 ? sub % c.kv_heads : blockIdx.y * kSubs + sub;
   const bool real = token < a.n_tokens && h < c.kv_heads && (tokens == 1 || sub / c.kv_heads < tokens);
   const int32_t slot = real ? a.slots[token] : -1;
-  after_previous();
+  if constexpr (!kOne) after_previous();
   if (slot < 0) return;
   if (((uint32_t)slot >> c.log2_pt) >= c.n_pages) {
-    if (lane == 0) report(a.st, SHN_ERR_INVALID_ARG, token);
+    if (!kOne && lane == 0) report(a.st, SHN_ERR_INVALID_ARG, token);
     return;
   }
   const uint64_t at = kv_row_of_slot(c, (uint32_t)slot, h);
@@ -277,23 +328,38 @@ cudaError_t launch_kv_begin(DeviceStatus* st, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_store(const KvPages& c, uint32_t head_dim, const KvStoreArgs& a, int sm_count, cudaStream_t s) {
-  const uint32_t groups = kStoreThreads * 8 / head_dim, rows = a.q_heads > 2 * c.kv_heads ? a.q_heads : 2 * c.kv_heads;
+  const uint32_t groups = kThreads * 8 / head_dim, rows = a.q_heads > 2 * c.kv_heads ? a.q_heads : 2 * c.kv_heads;
   // few tokens: their rows over several blocks, until the SMs have two blocks each or a block has one row per group (64 tokens,
   // 32 query and 8 key heads of 128, the load behind it counted: 6.25 us; 6.53 with a block for all of a token's rows)
   uint32_t parts = 1;
   while ((uint64_t)parts * a.n_tokens < 2ull * sm_count && parts * groups < rows) ++parts;
-  // three blocks to an SM, each with its tokens
-  const uint32_t most = 3u * sm_count;
-  const dim3 grid(a.n_tokens < most ? a.n_tokens : most, parts);
-  return head_dim == 128 ? launch_behind(kv_store_kernel<128>, grid, kStoreThreads, 0, s, c, a)
-                         : launch_behind(kv_store_kernel<64>, grid, kStoreThreads, 0, s, c, a);
+  // three blocks to an SM, each with its tokens (or the status)
+  if (a.n_tokens > kOneTokens) {
+    const cudaError_t e = launch_kv_begin(a.st, s);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(a.n_tokens < 3u * sm_count ? a.n_tokens : 3u * sm_count, parts);
+    return head_dim == 128 ? launch_behind(kv_store_kernel<128, false>, grid, kThreads, 0, s, c, a)
+                           : launch_behind(kv_store_kernel<64, false>, grid, kThreads, 0, s, c, a);
+  }
+  const uint32_t most = 3u * sm_count - 1;
+  const dim3 grid(1 + (a.n_tokens < most ? a.n_tokens : most), parts);
+  if (head_dim == 128) kv_store_kernel<128, true><<<grid, kThreads, 0, s>>>(c, a);
+  else kv_store_kernel<64, true><<<grid, kThreads, 0, s>>>(c, a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_kv_load(const KvPages& c, uint32_t head_dim, const KvLoadArgs& a, cudaStream_t s) {
-  const uint32_t subs = kLoadThreads / (head_dim / 16), tokens = c.kv_heads < subs ? subs / c.kv_heads : 1;
-  const dim3 grid((a.n_tokens + tokens - 1) / tokens, tokens > 1 ? 1 : (c.kv_heads + subs - 1) / subs);
-  return head_dim == 128 ? launch_behind(kv_load_kernel<128>, grid, kLoadThreads, 0, s, c, a)
-                         : launch_behind(kv_load_kernel<64>, grid, kLoadThreads, 0, s, c, a);
+  const uint32_t subs = kThreads / (head_dim / 16), tokens = c.kv_heads < subs ? subs / c.kv_heads : 1;
+  const uint32_t blocks = (a.n_tokens + tokens - 1) / tokens, parts = tokens > 1 ? 1 : (c.kv_heads + subs - 1) / subs;
+  if (a.n_tokens > kOneTokens) {
+    const cudaError_t e = launch_kv_begin(a.st, s);
+    if (e != cudaSuccess) return e;
+    return head_dim == 128 ? launch_behind(kv_load_kernel<128, false>, dim3(blocks, parts), kThreads, 0, s, c, a)
+                           : launch_behind(kv_load_kernel<64, false>, dim3(blocks, parts), kThreads, 0, s, c, a);
+  }
+  if (head_dim == 128) kv_load_kernel<128, true><<<dim3(1 + blocks, parts), kThreads, 0, s>>>(c, a);
+  else kv_load_kernel<64, true><<<dim3(1 + blocks, parts), kThreads, 0, s>>>(c, a);
+  return cudaGetLastError();
 }
 
 }  // namespace shn

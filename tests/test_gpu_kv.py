@@ -268,6 +268,34 @@ def test_store_and_load_report_bad_slots_and_positions():
     assert status(w) == (0, 0)  # every call clears the word
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 255, 1030, 8191, 8192, 8197, 40000])
+def test_a_bad_index_anywhere_is_reported(n):
+    """Slots and positions that start at any place within 16 bytes, bad ones at both ends and between. Of several bad ones a
+    call of up to 8192 tokens reports the first."""
+    cache = filled_cache(2, 1, 16, 64)
+    k, w, cs = bf16(n, 1, 64, seed=n), work(), angles(6, 64, 1)
+    out, none = torch.zeros_like(k), torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    was = cache.k.clone()
+    for lead in range(4):
+        slots, positions = (torch.zeros(lead + n, dtype=torch.int32, device=DEV)[lead:] for _ in range(2))
+        slots -= 1
+        for at in sorted({0, n // 2, n - 1}):
+            last = n - 1 if n <= 8192 else at  # the later one is bad as well
+            slots[at], slots[last] = 32, 33
+            kv.shn_kv_load(cache, slots, out, None, w)
+            assert status(w) == (shn.SHN_ERR_INVALID_ARG, at)
+            kv.shn_kv_store(None, k, k, positions, slots, cache, None, w, cos_sin=cs)
+            assert status(w) == (shn.SHN_ERR_INVALID_ARG, at)
+            slots[at] = slots[last] = -1
+            positions[at], positions[last] = -1, 6
+            kv.shn_kv_store(None, k, k, positions, none, cache, None, w, cos_sin=cs)
+            assert status(w) == (shn.SHN_ERR_INVALID_ARG, at)
+            positions[at] = positions[last] = 0
+        kv.shn_kv_store(None, k, k, positions, slots, cache, None, w, cos_sin=cs)
+        assert status(w) == (0, 0)
+    assert torch.equal(cache.k, was) and not out.any()
+
+
 # ---- attention -------------------------------------------------------------------------------------
 
 
