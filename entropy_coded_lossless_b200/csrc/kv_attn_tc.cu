@@ -24,6 +24,9 @@
 // way in registers while the present one is converted. TMEM (512 columns): O0, O1 (D each) and for each row tile 128
 // columns in which a tile's two halves of S, the weights in their place and the next tile's first half take turns.
 //
+// Where a call has too few rows to fill the SMs, up to 8 blocks of a cluster share a row tile's tokens and join their sums in
+// each other's shared memory (join_parts): no workspace, no second launch.
+//
 // What bounds it. 8192 causal tokens, 32 query and 8 key heads of 128: 700 us in a run of calls, 785 TFLOP/s, 48 % of the
 // measured bf16 rate (630 us and 53 % for the call alone in a graph). A tile of 256 x 128 scores costs a block about 4400
 // cycles; the products would take 2048 of them (1024 at D = 64) and so would the exponentials, at 16 a cycle; issuing the
@@ -178,7 +181,72 @@ __device__ __forceinline__ void find_part(const KvPages& c, const KvAttnArgs& a,
   w.len = min(prefix, (int32_t)((uint64_t)(split + 1) * tiles / pl.splits * kTile)) - (int32_t)w.t0;
 }
 
-template <int D, bool kPart>
+// A sequence's tiles over the blocks of a cluster. Joining costs about as much as a tile, so three tiles stay with one block (4
+// requests of 55 to 262 tokens 17.1 us, 18.8 when they are shared) and from four on a block may have one (3 requests of 83 to
+// 673 tokens 17.1 us; 19.2 with two tiles to a block at least, 21.8 with all in one).
+__device__ __forceinline__ uint32_t parts_of(uint32_t tiles, uint32_t most) { return tiles > 3 ? min(most, tiles) : 1; }
+__device__ __forceinline__ uint32_t first_tile(uint32_t tiles, uint32_t parts, uint32_t rank) { return min(rank, parts) * tiles / parts; }
+
+// The parts' sums, sums of weights l, references m and exponents E lie in their blocks' shared memory. Each block of the cluster
+// joins 256 / ranks rows, a warp 16 / ranks of them, half of these at a time: 8 loads of 32 lanes (a row of a block each) are on
+// their way together.
+//   out = sum O_i 2^(m_i - m + E_i - E) 2^E / sum l_i 2^(m_i - m)
+template <int D, typename F>
+__device__ __forceinline__ void join_parts(uint32_t base, uint32_t ranks, uint32_t parts, uint32_t tiles, uint32_t rank, uint32_t warp,
+                                           uint32_t lane, F put) {
+  using L = Layout<D>;
+  const uint32_t mask = ranks - 1, log2 = 31 - __clz(ranks), each = 8 >> log2;  // rows at a time
+  const uint32_t from = lane & mask;  // the block whose row a lane looks at: row (lane & 7) >> log2
+  const bool has = first_tile(tiles, parts, from + 1) > first_tile(tiles, parts, from);
+#pragma unroll 1
+  for (uint32_t i = 0; i < 2; ++i) {
+    const uint32_t row0 = rank * (kRows >> log2) + (warp * 2 + i) * each, row = row0 + ((lane & 7) >> log2);
+    float l = 0.f, m = -INFINITY, size = -INFINITY;
+    if (has) {
+      l = __uint_as_float(ld_cluster32(base + L::row_sum + 4 * row, from));
+      m = __uint_as_float(ld_cluster32(base + L::row_sum + 4 * (kRows + row), from));
+      size = __uint_as_float(ld_cluster32(base + L::misc + 12, from));
+    }
+    uint4 v[8];
+#pragma unroll
+    for (uint32_t e = 0; e < 8; ++e) {
+      const uint32_t r = row0 + (e >> log2), of = e & mask;
+      v[e] = make_uint4(0, 0, 0, 0);
+      if (first_tile(tiles, parts, of + 1) > first_tile(tiles, parts, of)) {
+        if constexpr (D == 128) {
+          v[e] = ld_cluster128(base + L::q + r * 512 + ((lane ^ (r & 7)) << 4), of);
+        } else {
+          const uint2 x = ld_cluster64(base + L::q + r * 256 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8, of);
+          v[e].x = x.x, v[e].y = x.y;
+        }
+      }
+    }
+    float top = m, held = size;
+    for (uint32_t d = 1; d < ranks; d <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      held = fmaxf(held, __shfl_xor_sync(~0u, held, d));
+    }
+    float by = exp2_approx(m - top);
+    float sum = has ? l * by : 0.f;
+    by = has ? exp2_approx(m - top + (size - held)) : 0.f;
+    for (uint32_t d = 1; d < ranks; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    const float inv = pow2(held) / sum;
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (uint32_t e = 0; e < 8; ++e) {
+      const float f = __shfl_sync(~0u, by, e), g = __shfl_sync(~0u, inv, e);
+      o[0] = fmaf(__uint_as_float(v[e].x), f, o[0]), o[1] = fmaf(__uint_as_float(v[e].y), f, o[1]);
+      o[2] = fmaf(__uint_as_float(v[e].z), f, o[2]), o[3] = fmaf(__uint_as_float(v[e].w), f, o[3]);
+      if ((e & mask) == mask) {
+        put(row0 + (e >> log2), o, g);
+        o[0] = o[1] = o[2] = o[3] = 0.f;
+      }
+    }
+  }
+}
+
+// kSplit: pl.splits blocks of a cluster share the tokens of 256 rows, and the rows of the result (join_parts).
+template <int D, bool kPart, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAttnArgs a, DecodePlan pl) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using L = Layout<D>;
@@ -186,14 +254,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   // Roles are counted from the second warpgroup on: the issuing warp is the block's first, which the schedulers serve
   // before younger ones.
   const uint32_t lane = threadIdx.x & 31, warp = ((threadIdx.x >> 5) + kIssueWarp) % (kThreads / 32), tid = warp * 32 + lane;
-  const uint32_t group = a.q_heads / c.kv_heads, hk = blockIdx.x % c.kv_heads;
+  const uint32_t place = kSplit ? blockIdx.x / pl.splits : blockIdx.x, rank = kSplit ? blockIdx.x % pl.splits : 0;
+  const uint32_t group = a.q_heads / c.kv_heads, hk = place % c.kv_heads;
 
   after_previous();
   let_next();
   const uint32_t status = *reinterpret_cast<volatile uint32_t*>(&a.st->status);
   Work w;
   if constexpr (kPart) find_part(c, a, pl, group, w);
-  else if (!find_work(c, a, group, blockIdx.x / c.kv_heads, reinterpret_cast<uint32_t*>(smem + L::scan), w)) return;
+  else if (!find_work(c, a, group, place / c.kv_heads, reinterpret_cast<uint32_t*>(smem + L::scan), w)) return;
   const uint32_t rows_here = min(kRows, w.rows - w.row0);
   // tokens the block's last row sees; every row of the block sees at most as many
   // row i of the block is query base_q + x and head y of the group, x = (rest + i) / group: with i + rest < 320 and group <= 64 that
@@ -205,8 +274,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     return base_q + x;
   };
   const int32_t shift = w.len - w.nq + 1;  // query i sees shift + i tokens
-  const int32_t most = kPart ? max(0, w.len) : max(0, min(w.len, shift + (int32_t)((w.row0 + rows_here - 1) / group)));
-  const uint32_t tiles = ((uint32_t)most + kTile - 1) / kTile;
+  int32_t most = kPart ? max(0, w.len) : max(0, min(w.len, shift + (int32_t)((w.row0 + rows_here - 1) / group)));
+  uint32_t tiles = ((uint32_t)most + kTile - 1) / kTile;
+  const uint32_t all_tiles = tiles;
+  const uint32_t parts = kSplit ? parts_of(all_tiles, pl.splits) : 1;
+  if constexpr (kSplit) {
+    if (parts == 1 && rank > 0) return;  // (with one part no block waits for another or looks at its memory)
+    if (parts > 1) {
+      const uint32_t first = first_tile(all_tiles, parts, rank);
+      tiles = first_tile(all_tiles, parts, rank + 1) - first;
+      w.t0 = first * kTile;
+      most = max(0, min(most - (int32_t)w.t0, (int32_t)(tiles * kTile)));
+    }
+  }
 
   if (tid == 0) {
     bar_init(bars + kQFull, kSoftThreads);
@@ -237,7 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   // after a wait that gave up the call has failed: the other blocks do not start on it
   const bool failed = __syncthreads_or(status == SHN_ERR_TIMEOUT);
   fence_after();
-  if (failed) {
+  if (kSplit && parts > 1) {
+    if (failed) tiles = 0;  // (the cluster's barriers need every block)
+  } else if (failed) {
     if (warp == kIssueWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(lds32(stop + 4)));
     return;
   }
@@ -311,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         bool bad;
         return max(0, min(w.len, decode_len(c, a, (int32_t)w.t0 + w.len, q, bad) - (int32_t)w.t0));
       }
+      if constexpr (kSplit) return max(0, min(most, min(w.len, shift + (int32_t)q) - (int32_t)w.t0));
       return max(0, min(w.len, shift + (int32_t)q));
     };
     int32_t seen[2];
@@ -476,11 +559,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
       if ((lane & 3) == 0) sts32(sums + 4 * (lanes + quad + 8 * r), __float_as_uint(l[r]));
-      if (kPart && (lane & 3) == 0) sts32(refs + 4 * (lanes + quad + 8 * r), __float_as_uint(m[r]));
+      if ((kPart || kSplit) && (lane & 3) == 0) sts32(refs + 4 * (lanes + quad + 8 * r), __float_as_uint(m[r]));
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(kSoftThreads / 2) : "memory");
     if (ok && tiles) ok = __all_sync(~0u, bar_wait(bars + kOFull + 16 * half + 8, (tiles - 1) & 1, stop));
-    if (ok) {
+    if (kSplit && parts > 1) {
+      fence_after();
+      asm volatile("bar.sync 3, %0;" ::"n"(kSoftThreads) : "memory");  // all products are done with shared memory
+      // O where the queries and keys were, a row's 16-byte chunks exchanged so that 8 lanes' rows meet no bank twice
+      const uint32_t row = half * 128 + rows32 + lane, first = (warp >> 2 & 1) * (D / 2);
+      if (tid == 0) sts32(base + L::misc + 12, __float_as_uint(held));
+#pragma unroll 1
+      for (uint32_t q = 0; ok && tiles && q < D / 2; q += 32) {
+        uint32_t o[32];
+        ld32(tmem + (rows32 << 16) + 256 + half * D + first + q, o);
+        wait_ld();
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e)
+          sts128(base + L::q + row * (4 * D) + ((((first + q) / 4 + e) ^ (row & 7)) << 4), make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+      }
+      fence_before();
+      cluster_sync();
+      join_parts<D>(base, pl.splits, parts, all_tiles, rank, warp, lane, [&](uint32_t at, const float* o, float inv) {
+        if (at >= rows_here) return;
+        uint32_t head;
+        const uint32_t query = query_of(at, head);
+        const bool any = min(w.len, shift + (int32_t)query) > 0;  // no token seen: zeros
+        uint32_t x[D / 64];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) x[i] = any ? bf16_pack(o[2 * i] * inv, o[2 * i + 1] * inv) : 0u;
+        uint16_t* dst = a.out + (uint64_t)(w.q0 + query) * a.out_stride + (uint64_t)(hk * group + head) * D + lane * (D / 32);
+        if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(x[0], x[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = x[0];
+      });
+      cluster_sync();  // nobody leaves while its memory is read
+    } else if (ok) {
       fence_after();
       // Each warp takes half the columns of its 32 rows, 32 at a time: a thread has a row, and a row a thread is written as lines
       // would be, so the values change hands in shared memory (the queries' place, which no product reads any more: 4 KB a warp).
@@ -556,8 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     // A warp's load: 4 lanes on 64 values of a row, 8 rows. For D = 128 even warps take the rows' first 64 values.
     const uint32_t part = D == 128 ? (cw & 1) : 0, first = (cw >> (D == 128 ? 1 : 0)) * kLoads * 8;
     const uint32_t chunk = lane & 3, sub = lane >> 2;
-    const int32_t* table = kPart ? a.prefix_pages + (w.t0 >> c.log2_pt) : a.table + (uint64_t)w.req * a.max_blocks;
-    const uint32_t skip = kPart ? w.t0 & ((1u << c.log2_pt) - 1) : 0;  // (pages longer than a tile: the part begins inside one)
+    const int32_t* table = (kPart ? a.prefix_pages : a.table + (uint64_t)w.req * a.max_blocks) + (kPart || kSplit ? w.t0 >> c.log2_pt : 0);
+    const uint32_t skip = kPart || kSplit ? w.t0 & ((1u << c.log2_pt) - 1) : 0;  // (pages longer than a tile: the part begins inside one)
     const uint32_t pt_mask = (1u << c.log2_pt) - 1;
 
     // page of the tile's 16-token group `lane` (lanes 0-7), -1 where there are no tokens
@@ -665,6 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       turn(std::true_type{}, row_scale, base + L::v + buf * L::kOperand, c.k, off);
       if (lane == 0) bar_arrive(bars + kVFull + 8 * buf);
     }
+    if (kSplit && parts > 1) cluster_sync(), cluster_sync();
   } else {
     // ---- products: a warp for each row tile runs the loop as one, an elected thread issues ---------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
@@ -725,6 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         }
       }
     }
+    if (kSplit && parts > 1) cluster_sync(), cluster_sync();
   }
   fence_before();
   __syncthreads();
@@ -735,28 +850,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
 
 // More shared memory than the default 48 KB: an attribute of the kernel on each device, so it is set for the one that is
 // current on every call.
-template <int D, bool kPart>
+template <int D, bool kPart, bool kSplit>
 cudaError_t launch(uint64_t blocks, const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s) {
   if (blocks >= (1ull << 31)) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D, kPart>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::total);
+  const auto kernel = kv_prompt_kernel<D, kPart, kSplit>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::total);
   if (e != cudaSuccess) return e;
-  return launch_behind(kv_prompt_kernel<D, kPart>, dim3((uint32_t)blocks), kThreads, Layout<D>::total, s, c, a, pl);
+  if constexpr (kSplit) return launch_behind_in_clusters(kernel, pl.splits, dim3((uint32_t)blocks * pl.splits), kThreads, Layout<D>::total, s, c, a, pl);
+  else return launch_behind(kernel, dim3((uint32_t)blocks), kThreads, Layout<D>::total, s, c, a, pl);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, cudaStream_t s) {
+cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, int sm_count, cudaStream_t s) {
   const uint64_t group = a.q_heads / c.kv_heads;
   // at most so many tiles, however the queries are spread over the requests
   const uint64_t blocks = ((uint64_t)a.n_tokens * group / kRows + (a.n_reqs < a.n_tokens ? a.n_reqs : a.n_tokens)) * c.kv_heads;
-  const DecodePlan none = {};
-  return head_dim == 128 ? launch<128, false>(blocks, c, a, none, s) : launch<64, false>(blocks, c, a, none, s);
+  DecodePlan pl = {};
+  pl.splits = 1;
+  // Few blocks, and requests that may be long: several blocks to the same rows, as many as the SMs have places and the longest
+  // sequence tiles. Measured, with and without: one query after 5102 tokens (8 heads on one) 29.6 / 118.8 us, 700 after 2551 (8 on
+  // 2) 33.8 / 74.6, 40 after 5102 (32 on 8, of 64) 26.9 / 102.1. With 4 blocks to a row at most they take 42.4, 34.2 and
+  // 37.8, with up to twice the blocks that have places 29.7, 49.1 and 27.0.
+  const uint64_t tokens = (uint64_t)a.max_blocks << c.log2_pt;  // what a request can have
+  while (pl.splits < 8 && blocks * pl.splits * 2 <= (uint64_t)sm_count && tokens > 2 * pl.splits * kTile) pl.splits *= 2;
+  if (pl.splits > 1) return head_dim == 128 ? launch<128, false, true>(blocks, c, a, pl, s) : launch<64, false, true>(blocks, c, a, pl, s);
+  return head_dim == 128 ? launch<128, false, false>(blocks, c, a, pl, s) : launch<64, false, false>(blocks, c, a, pl, s);
 }
 
 cudaError_t launch_kv_prefix(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s) {
   const uint64_t group = a.q_heads / c.kv_heads;
   const uint64_t blocks = (a.n_reqs * group + kRows - 1) / kRows * c.kv_heads * pl.splits;
-  return head_dim == 128 ? launch<128, true>(blocks, c, a, pl, s) : launch<64, true>(blocks, c, a, pl, s);
+  return head_dim == 128 ? launch<128, true, false>(blocks, c, a, pl, s) : launch<64, true, false>(blocks, c, a, pl, s);
 }
 
 }  // namespace shn

@@ -208,7 +208,7 @@ int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens
   a.st = clear_status(d_work, s);
   if (!a.st) return SHN_ERR_CUDA;
   if (n_tokens == 0 || n_reqs == 0) return SHN_OK;
-  return launch_kv_prompt(pages_of(cache), cache->head_dim, a, s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
+  return launch_kv_prompt(pages_of(cache), cache->head_dim, a, sm_count_for_launch(), s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
 }
 
 size_t shn_kv_attn_shared_workspace_bytes(const shn_kv_cache* cache, uint32_t n_reqs, uint32_t q_heads) {

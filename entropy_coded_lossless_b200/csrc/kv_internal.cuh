@@ -44,18 +44,25 @@ __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, uint32_t threads, size_t smem, cudaStream_t s, const A&... args) {
+cudaError_t launch_behind_in_clusters(void (*kernel)(P...), uint32_t cluster, dim3 grid, uint32_t threads, size_t smem, cudaStream_t s,
+                                      const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster, at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, uint32_t threads, size_t smem, cudaStream_t s, const A&... args) {
+  return launch_behind_in_clusters(kernel, 1, grid, threads, smem, s, args...);
 }
 cudaError_t launch_kv_begin(DeviceStatus* st, cudaStream_t s);
 
@@ -110,6 +117,6 @@ struct KvAttnArgs {
   uint64_t out_stride;
   DeviceStatus* st;
 };
-cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, cudaStream_t s);
+cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnArgs& a, int sm_count, cudaStream_t s);
 
 }  // namespace shn

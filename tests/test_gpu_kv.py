@@ -417,6 +417,66 @@ def test_attention_extreme_scores(d):
     run_shared(cache, table, [n], 0, h, d, seed=4)
 
 
+@pytest.mark.parametrize("h,hk,d,pt,new,ctx", [
+    (2, 1, 64, 16, [1], [511]),  # a few tiles: two parts
+    (2, 1, 128, 16, [1], [640]),
+    (8, 1, 128, 64, [1], [2900]),  # 8 parts of 2 or 3 tiles
+    (5, 1, 64, 128, [3, 1, 0], [3000, 0, 700]),  # short requests beside a long one: parts without tiles
+    (4, 4, 128, 1024, [9], [2040]),  # parts that begin inside a page
+    (12, 3, 64, 32, [70, 130], [1500, 900]),  # rows of several blocks, the last one odd
+    (32, 8, 128, 16, [7], [1283]),
+    (16, 2, 64, 64, [400], [1000]),  # the causal end lies in several parts
+    (1, 1, 128, 32, [300], [500]),
+    (64, 1, 64, 16, [5], [1200]),
+])
+def test_prompt_of_few_rows(h, hk, d, pt, new, ctx):
+    """Few rows and many tokens: the tokens are shared by several blocks."""
+    kv_lens = [n + c for n, c in zip(new, ctx)]
+    table, pages = tables(kv_lens, pt, 3, extra=1)
+    cache = filled_cache(pages, hk, pt, d, seed=4)
+    run_prompt(cache, table, new, kv_lens, h, d, seed=5, padding=2)
+    run_prompt(cache, table, new, kv_lens, h, d, seed=6, scale=0.5, strided=True)
+    # value scales that grow and fall along the sequence: the parts hold their sums in different ranges
+    grow = torch.logspace(-9, 9, cache.v_scale.numel(), device=DEV).view_as(cache.v_scale)
+    cache.v_scale *= grow
+    run_prompt(cache, table, new, kv_lens, h, d, seed=7)
+    cache.v_scale /= grow * grow
+    run_prompt(cache, table, new, kv_lens, h, d, seed=8)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_of_few_rows_masked_and_empty(d):
+    """Rows that see no token, or none of the later parts, and what masked places of those hold; wide tables of short
+    requests; a bad page in a later part; all of it captured and replayed."""
+    new, kv_lens, pt, hk, h = [20, 1], [1024, 9], 32, 1, 4
+    table, pages = tables(kv_lens, pt, 8, extra=2)
+    cache = filled_cache(pages, hk, pt, d, seed=9)
+    clean, scale = run_prompt(cache, table, new, kv_lens, h, d, seed=5), 1 / math.sqrt(d)
+    last = spec.token_slots(table[0], pt, 1024)[1010:].tolist()
+    for x in last:
+        cache.v_scale[x // pt, :, x % pt] = math.inf
+        cache.k_scale[x // pt, :, x % pt] = math.nan
+    q, out, w = bf16(21, h, d, seed=5), torch.zeros(21, h, d, dtype=torch.bfloat16, device=DEV), work()
+    args = (q, cache, table, ints([0, 20, 21]), ints(kv_lens), scale, out, w)
+    kv.shn_kv_attn_prompt(*args)
+    assert status(w) == (0, 0)
+    # Weights enter fp16 times a power of two that the value scales of 32 tokens give, masked ones among them: below fp16's
+    # normal numbers a weight's rounding depends on it, by no more than the tolerance's part for lost weights.
+    ref, tol = spec.cache_attention(q, filled_cache(pages, hk, pt, d, seed=9), lambda r: table[r], kv_lens, [0, 20, 21], scale)
+    assert ((out[:6].double() - ref[:6]).abs() <= tol[:6]).all() and torch.isnan(out[6:20]).all() and torch.equal(out[20], clean[20])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv.shn_kv_attn_prompt(*args)
+    first = out.clone()
+    out.zero_()
+    graph.replay()
+    assert torch.equal(out.view(torch.int16), first.view(torch.int16))
+    run_prompt(filled_cache(pages, hk, pt, d, seed=9), table, [1100, 1], [1024, 9], 1, d, seed=2)  # 76 rows see nothing
+    table[0, 30] = pages
+    kv.shn_kv_attn_prompt(*args)
+    assert status(w) == (shn.SHN_ERR_INVALID_ARG, 0) and torch.equal(out[20], clean[20])
+
+
 def test_prompt_far_slots():
     """A cache whose bytes pass 2^32: pages at its end are read where they are."""
     hk, pt, d = 8, 64, 128
