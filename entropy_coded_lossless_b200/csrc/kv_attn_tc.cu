@@ -257,9 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   const uint32_t place = kSplit ? blockIdx.x / pl.splits : blockIdx.x, rank = kSplit ? blockIdx.x % pl.splits : 0;
   const uint32_t group = a.q_heads / c.kv_heads, hk = place % c.kv_heads;
 
-  after_previous();
+  if constexpr (!kPart) after_previous();  // (parts of a prefix: the call's first kernel)
   let_next();
-  const uint32_t status = *reinterpret_cast<volatile uint32_t*>(&a.st->status);
+  const uint32_t status = kPart ? 0 : *reinterpret_cast<volatile uint32_t*>(&a.st->status);
   Work w;
   if constexpr (kPart) find_part(c, a, pl, group, w);
   else if (!find_work(c, a, group, place / c.kv_heads, reinterpret_cast<uint32_t*>(smem + L::scan), w)) return;
@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     for (uint32_t i = 0; i < 4; ++i) bar_init(bars + kScaleFull + 8 * i, kConvertWarps);
     sts32(stop, 0);
     sts32(base + L::misc + 8, 0);
+    if (kPart) sts32(base + L::misc + 16, kNoError);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssueWarp) {
@@ -680,7 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if (j < tiles && tok < most) {
         p = table[(tok + skip) >> c.log2_pt];
         if (p < 0 || (uint32_t)p >= c.n_pages) {
-          if (lane < 8) report(a.st, SHN_ERR_INVALID_ARG, w.req);
+          if (kPart) sts32(base + L::misc + 16, 0);
+          else if (lane < 8) report(a.st, SHN_ERR_INVALID_ARG, w.req);
           p = -1;
         }
       }
@@ -845,7 +847,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   __syncthreads();
   fence_after();
   if (warp == kIssueWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-  if (tid == 0 && lds32(stop) != 0) report(a.st, SHN_ERR_TIMEOUT, w.req);
+  if constexpr (kPart) {
+    if (tid == 0) pl.errors[blockIdx.x] = lds32(stop) != 0 ? kGaveUp : lds32(base + L::misc + 16);
+  } else {
+    if (tid == 0 && lds32(stop) != 0) report(a.st, SHN_ERR_TIMEOUT, w.req);
+  }
 }
 
 // More shared memory than the default 48 KB: an attribute of the kernel on each device, so it is set for the one that is
@@ -857,6 +863,7 @@ cudaError_t launch(uint64_t blocks, const KvPages& c, const KvAttnArgs& a, const
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::total);
   if (e != cudaSuccess) return e;
   if constexpr (kSplit) return launch_behind_in_clusters(kernel, pl.splits, dim3((uint32_t)blocks * pl.splits), kThreads, Layout<D>::total, s, c, a, pl);
+  else if constexpr (kPart) return launch_first(kernel, dim3((uint32_t)blocks), kThreads, Layout<D>::total, s, c, a, pl);
   else return launch_behind(kernel, dim3((uint32_t)blocks), kThreads, Layout<D>::total, s, c, a, pl);
 }
 

@@ -71,10 +71,12 @@ int check_attn(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32
 constexpr uint64_t kPrefixUnits = 12288, kPrefixGroups = 64;
 constexpr uint64_t kSplitBlocks = 148;
 
-// How shn_kv_attn_shared is cut up, and its workspace: [status 256][pieces' sums][pieces' (mt, ms, l)].
+// How shn_kv_attn_shared is cut up, and its workspace: [status 256][pieces' sums][pieces' (mt, ms, l)][the same of the prefix's
+// parts][blocks' errors].
 struct SharedLayout {
   DecodePlan pl;
-  size_t out_off, ml_off, split_off, split_ml_off, total;
+  size_t out_off, ml_off, split_off, split_ml_off, errors_off, total;
+  uint64_t prefix_tiles;  // of 256 rows, all key heads'
 };
 
 SharedLayout shared_layout(const shn_kv_cache* c, uint32_t n_reqs, uint32_t q_heads) {
@@ -97,7 +99,9 @@ SharedLayout shared_layout(const shn_kv_cache* c, uint32_t n_reqs, uint32_t q_he
   x.ml_off = x.out_off + round_up(pieces * c->head_dim * sizeof(float), 256);
   x.split_off = x.ml_off + round_up(pieces * sizeof(float4), 256);
   x.split_ml_off = x.split_off + round_up(parts * c->head_dim * sizeof(float), 256);
-  x.total = x.split_ml_off + round_up(parts * sizeof(float4), 256);
+  x.errors_off = x.split_ml_off + round_up(parts * sizeof(float4), 256);
+  x.prefix_tiles = blocks;
+  x.total = x.errors_off + round_up((blocks * x.pl.splits + kDecodeMaxWarps / (kDecodeThreads / 32)) * sizeof(uint32_t), 256);
   return x;
 }
 
@@ -239,14 +243,14 @@ int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, 
   a.table = d_block_table, a.max_blocks = max_blocks, a.kv_len = d_kv_len, a.n_reqs = n_reqs;
   a.prefix_pages = d_prefix_pages, a.n_prefix_pages = n_prefix_pages, a.prefix_len = d_prefix_len;
   a.scale = softmax_scale, a.out = d_out, a.out_stride = out_stride;
-  a.st = clear_status(d_work, s);
-  if (!a.st) return SHN_ERR_CUDA;
-  if (n_reqs == 0) return SHN_OK;
+  a.st = static_cast<DeviceStatus*>(d_work);  // the last kernel sets it
+  if (n_reqs == 0) return clear_status(d_work, s) ? SHN_OK : SHN_ERR_CUDA;
   uint8_t* wb = static_cast<uint8_t*>(d_work);
   x.pl.out = reinterpret_cast<float*>(wb + x.out_off);
   x.pl.ml = reinterpret_cast<float4*>(wb + x.ml_off);
   x.pl.split_out = reinterpret_cast<float*>(wb + x.split_off);
   x.pl.split_ml = reinterpret_cast<float4*>(wb + x.split_ml_off);
+  x.pl.errors = reinterpret_cast<uint32_t*>(wb + x.errors_off);
   const uint64_t prefix_cap = (uint64_t)n_prefix_pages * cache->page_tokens;
   const uint64_t prefix_units = x.pl.prefix_groups * (uint64_t)cache->kv_heads * ((prefix_cap + kUnit - 1) / kUnit);
   if (prefix_cap && (!x.pl.prefix_groups || prefix_units >= kPrefixUnits)) {
@@ -265,6 +269,7 @@ int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, 
   if (blocks > (units + per_block - 1) / per_block) blocks = (units + per_block - 1) / per_block;
   if (blocks > kDecodeMaxWarps / per_block) blocks = kDecodeMaxWarps / per_block;
   x.pl.warps = (uint32_t)(blocks * per_block);
+  x.pl.n_errors = (uint32_t)(x.prefix_tiles * x.pl.splits + blocks);
   if (x.pl.splits && launch_kv_prefix(pages_of(cache), cache->head_dim, a, x.pl, s) != cudaSuccess) return SHN_ERR_CUDA;
   return launch_kv_decode(pages_of(cache), cache->head_dim, a, x.pl, s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
 }

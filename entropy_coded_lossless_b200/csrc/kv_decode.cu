@@ -59,17 +59,19 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
   constexpr int kKLoads = D / 64;  // 16-byte loads of a token's keys per lane
   constexpr uint32_t kStages = Ring<D>::kStages, kStage = Ring<D>::kStage;
   __shared__ UnitScan scan;
+  __shared__ uint32_t error;
   const uint32_t lane = threadIdx.x & 31, g = lane >> 2, cc = lane & 3;
   const uint32_t w = blockIdx.x * (kDecodeThreads / 32) + (threadIdx.x >> 5);
   const uint32_t group = a.q_heads / c.kv_heads;
-  // Nothing here reads what the kernel before writes. Where that is the prefix's, the status word is cleared already, and only
-  // the end of this kernel has to come after it (the join is behind both); else the clearing comes first.
-  if (!pl.splits) after_previous();
+  // Nothing here reads what the prefix's kernel writes, if there is one before; only the end of this kernel has to come after
+  // it (the join is behind both).
   let_next();
+  if (threadIdx.x == 0) error = kNoError;
+  __syncthreads();
   bool bad;
   const int32_t prefix = decode_prefix(c, a, bad);
-  if (bad && blockIdx.x == 0 && threadIdx.x == 0) report(a.st, SHN_ERR_INVALID_ARG, 0);
-  scan_units(c, a, prefix, scan, blockIdx.x == 0);
+  if (bad && threadIdx.x == 0) error = 0;
+  scan_units(c, a, prefix, scan, blockIdx.x == 0 ? &error : nullptr);
 
   const uint32_t prefix_units = pl.prefix_groups ? ((uint32_t)prefix + kUnit - 1) / kUnit : 0;
   const uint32_t prefix_segs = c.kv_heads * pl.prefix_groups, seg_per_req = c.kv_heads * pl.own_groups;
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
     auto row_of = [&](uint32_t t, int32_t p) -> uint64_t {
       if (t >= t_last) return ~0ull;
       if (p < 0 || (uint32_t)p >= c.n_pages) {
-        if (lane == 0) report(a.st, SHN_ERR_INVALID_ARG, r);
+        if (lane == 0) atomicMin(&error, r);
         return ~0ull;
       }
       return kv_row(c, (uint32_t)p, hk, t & ((1u << c.log2_pt) - 1));
@@ -414,6 +416,8 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
         while (own_units(prefix, decode_len(c, a, prefix, r, bad)) == 0) ++r;  // ends: there are units left
     }
   }
+  __syncthreads();
+  if (threadIdx.x == 0) pl.errors[pl.n_errors - gridDim.x + blockIdx.x] = error;
   if (pl.splits) after_previous();
 }
 
@@ -425,9 +429,29 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
   __shared__ float sum_o[kWarps][D], sum_m[kWarps], sum_l[kWarps];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t group = a.q_heads / c.kv_heads;
+  if (blockIdx.x == gridDim.x - 1) {  // the call's status
+    __shared__ uint32_t first;
+    if (threadIdx.x == 0) first = kNoError;
+    __syncthreads();
+    after_previous();
+    uint32_t least = kNoError;
+    bool gave_up = false;
+    for (uint32_t i = threadIdx.x; i < pl.n_errors; i += kDecodeThreads) {
+      const uint32_t x = pl.errors[i];
+      gave_up |= x == kGaveUp;
+      least = min(least, x);
+    }
+    if (least < kGaveUp) atomicMin(&first, least);
+    gave_up = __syncthreads_or(gave_up);
+    if (threadIdx.x == 0) {
+      a.st->status = gave_up ? SHN_ERR_TIMEOUT : first != kNoError ? SHN_ERR_INVALID_ARG : SHN_OK;
+      a.st->detail = !gave_up && first != kNoError ? first : 0;
+    }
+    return;
+  }
   bool bad;
   const int32_t prefix = decode_prefix(c, a, bad);
-  scan_units(c, a, prefix, scan, false);
+  scan_units(c, a, prefix, scan, nullptr);
   const uint32_t wanted = blockIdx.x * (kWarps / kTeam) + warp / kTeam, items = a.n_reqs * a.q_heads;
   const uint32_t item = min(wanted, items - 1);  // (no warp leaves: there is a barrier ahead)
   const uint32_t r = item / a.q_heads, head = item % a.q_heads, hk = head / group, g = head % group;
@@ -551,11 +575,11 @@ __global__ void __launch_bounds__(kDecodeThreads) kv_join_kernel(KvPages c, KvAt
 template <int D>
 cudaError_t launch(const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, cudaStream_t s) {
   const dim3 blocks(pl.warps / (kDecodeThreads / 32));
-  cudaError_t e = cudaFuncSetAttribute(pl.rows == 8 ? kv_decode_kernel<D, 1> : kv_decode_kernel<D, 2>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes);
+  const auto kernel = pl.rows == 8 ? kv_decode_kernel<D, 1> : kv_decode_kernel<D, 2>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes);
   if (e != cudaSuccess) return e;
-  e = pl.rows == 8 ? launch_behind(kv_decode_kernel<D, 1>, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl)
-                   : launch_behind(kv_decode_kernel<D, 2>, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl);
+  e = pl.splits ? launch_behind(kernel, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl)
+                : launch_first(kernel, blocks, kDecodeThreads, Ring<D>::kBytes, s, c, a, pl);
   if (e != cudaSuccess) return e;
   // Few rows may have hundreds of pieces each, many rows only a few. A row gets 2, 4 or 8 warps while fewer than that share of
   // the decoding warps' number is asked for: so the join has about the warps that the decode had, up to twice as many.
@@ -563,10 +587,11 @@ cudaError_t launch(const KvPages& c, const KvAttnArgs& a, const DecodePlan& pl, 
   // rows 126 (one warp), eight 145.
   const uint64_t rows = (uint64_t)a.n_reqs * a.q_heads;
   const uint32_t n = (uint32_t)rows;
-  if (rows > pl.warps) return launch_behind(kv_join_kernel<D, 1>, dim3((n + 7) / 8), kDecodeThreads, 0, s, c, a, pl);
-  if (2 * rows > pl.warps) return launch_behind(kv_join_kernel<D, 2>, dim3((n + 3) / 4), kDecodeThreads, 0, s, c, a, pl);
-  if (4 * rows > pl.warps) return launch_behind(kv_join_kernel<D, 4>, dim3((n + 1) / 2), kDecodeThreads, 0, s, c, a, pl);
-  return launch_behind(kv_join_kernel<D, 8>, dim3(n), kDecodeThreads, 0, s, c, a, pl);
+  // (one block more, for the status)
+  if (rows > pl.warps) return launch_behind(kv_join_kernel<D, 1>, dim3((n + 7) / 8 + 1), kDecodeThreads, 0, s, c, a, pl);
+  if (2 * rows > pl.warps) return launch_behind(kv_join_kernel<D, 2>, dim3((n + 3) / 4 + 1), kDecodeThreads, 0, s, c, a, pl);
+  if (4 * rows > pl.warps) return launch_behind(kv_join_kernel<D, 4>, dim3((n + 1) / 2 + 1), kDecodeThreads, 0, s, c, a, pl);
+  return launch_behind(kv_join_kernel<D, 8>, dim3(n + 1), kDecodeThreads, 0, s, c, a, pl);
 }
 
 }  // namespace

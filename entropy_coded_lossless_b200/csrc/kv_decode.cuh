@@ -27,7 +27,12 @@ struct DecodePlan {
   float4* ml;              // [pieces][rows] (mt, ms, l, -)
   float* split_out;        // [splits][n_reqs * q_heads][head_dim]
   float4* split_ml;
+  uint32_t* errors;        // [n_errors], what each block found: the prefix kernel's blocks, then the single-token kernel's
+  uint32_t n_errors;
 };
+// A block's error: none, a wait that gave up, or the (first) request with something invalid. Every block writes its word, and
+// the last kernel makes the status of them: nothing has to be cleared in front of the first.
+constexpr uint32_t kNoError = 0xFFFFFFFFu, kGaveUp = 0xFFFFFFFEu;
 
 // Effective lengths: what the tables can hold. `bad` is set where the caller's value is not that.
 __device__ __forceinline__ int32_t decode_prefix(const KvPages& c, const KvAttnArgs& a, bool& bad) {
@@ -53,7 +58,8 @@ struct UnitScan {
   unsigned long long before[kDecodeThreads + 1];
   unsigned long long warp_sum[kDecodeThreads / 32];
 };
-__device__ __forceinline__ void scan_units(const KvPages& c, const KvAttnArgs& a, int32_t prefix, UnitScan& s, bool say) {
+// first_bad: where the first request with a bad length goes (shared memory), or null.
+__device__ __forceinline__ void scan_units(const KvPages& c, const KvAttnArgs& a, int32_t prefix, UnitScan& s, uint32_t* first_bad) {
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint32_t run = (a.n_reqs + kDecodeThreads - 1) / kDecodeThreads;
   const uint32_t r0 = min(a.n_reqs, t * run), r1 = min(a.n_reqs, r0 + run);
@@ -61,7 +67,7 @@ __device__ __forceinline__ void scan_units(const KvPages& c, const KvAttnArgs& a
   for (uint32_t r = r0; r < r1; ++r) {
     bool bad;
     const int32_t len = decode_len(c, a, prefix, r, bad);
-    if (bad && say) report(a.st, SHN_ERR_INVALID_ARG, r);
+    if (bad && first_bad) atomicMin(first_bad, r);
     own += own_units(prefix, len);
   }
   unsigned long long inc = own;

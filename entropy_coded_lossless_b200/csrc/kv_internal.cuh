@@ -37,9 +37,9 @@ __device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
   return r;
 }
 
-// A call's first kernel clears the status word; the next ones are launched so that they start while the one before still
+// A call's first kernel is launched as any other; the next ones are launched so that they start while the one before still
 // runs (programmatic dependent launch) and hide their start behind it. A kernel launched so reads nothing that the one
-// before writes, and reports nothing, until after_previous(); let_next() lets the one after it start.
+// before writes, and writes nothing that it reads, until after_previous(); let_next() lets the one after it start.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -59,6 +59,11 @@ cudaError_t launch_behind_in_clusters(void (*kernel)(P...), uint32_t cluster, di
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_first(void (*kernel)(P...), dim3 grid, uint32_t threads, size_t smem, cudaStream_t s, const A&... args) {
+  kernel<<<grid, threads, smem, s>>>(P(args)...);
+  return cudaGetLastError();
 }
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, uint32_t threads, size_t smem, cudaStream_t s, const A&... args) {
