@@ -4,8 +4,9 @@
 // token and per new page, each finding its request by a search in the sums. Little is read or written
 // (about 16 bytes per request and 8 per token), so the call is bound by latency. Every block forms the sums
 // for itself, which costs less than handing them around, and takes a token per thread. A step that one block
-// covers is one launch; for more a small kernel in front keeps the free-list head as it was before the call, since
-// the caller may have it updated in place. Measured: 256 requests with a token each 4.4 us, 1000 with 131,072 in all 6.8 us; one
+// covers is one launch. With more blocks the first of them looks at everything that can be wrong and is the only one to
+// write the status; only where the caller has the free-list head updated in place a small kernel in front keeps it
+// as it was before the call. Measured: 256 requests with a token each 4.1 us, 1000 with 131,072 in all 6.4 us; one
 // cluster of 8 blocks with 16 tokens a thread took 24.6 for the latter.
 #include "kv_internal.cuh"
 
@@ -22,19 +23,21 @@ __device__ __forceinline__ long long pages_of(long long tokens, uint32_t log2_pt
   return (tokens + (1ll << log2_pt) - 1) >> log2_pt;
 }
 
-// Clears the status and keeps the head (behind the status word) for the kernel that follows.
-__global__ void kv_plan_begin_kernel(KvPlanArgs a) {
+// Keeps the head (behind the status word) for the kernel that follows.
+__global__ void kv_plan_begin_kernel(KvPlanArgs a, int32_t* kept) {
   let_next();
-  if (threadIdx.x == 0) a.st->status = 0, a.st->detail = 0, reinterpret_cast<int32_t*>(a.st)[2] = *a.free_head;
+  if (threadIdx.x == 0) *kept = *a.free_head;
 }
 
-template <bool kOne>  // one block, no kernel in front
+template <bool kOne>  // one block
 __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
   __shared__ Sum2 before[kThreads + 1];  // sums in front of each thread's run of requests
   __shared__ Sum2 warp_sum[32];
   __shared__ uint32_t bad_code, bad_detail;
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const uint32_t rank = blockIdx.x, ranks = gridDim.x;
+  // (several blocks: the first is for the status)
+  const bool looks = !kOne && blockIdx.x == 0;
+  const uint32_t rank = kOne ? 0 : blockIdx.x - 1, ranks = kOne ? 1 : gridDim.x - 1;
   const uint32_t run = (a.n + kThreads - 1) / kThreads;
   const uint32_t r0 = min(a.n, t * run), r1 = min(a.n, r0 + run);
   if (t == 0) bad_code = 0, bad_detail = 0xFFFFFFFFu;
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
 
   if constexpr (!kOne) {
     after_previous();
-    head = reinterpret_cast<const volatile int32_t*>(a.st)[2];
+    head = *reinterpret_cast<const volatile int32_t*>(a.free_head);
   }
   uint32_t code = bad_code == 2 ? SHN_ERR_INVALID_ARG : bad_code == 1 ? SHN_ERR_CAPACITY : SHN_OK;
   uint32_t detail = code ? bad_detail : 0;
@@ -96,8 +99,44 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
   if constexpr (kOne) {
     if (t == 0) a.st->status = code, a.st->detail = detail;
     __syncthreads();  // the head is read and the status set before anything is written
-  } else if (rank == 0 && t == 0 && code) {
-    report(a.st, code, detail);
+  }
+  const int32_t page_limit = (int32_t)(0x7FFFFFFFu >> a.log2_pt);
+  const uint32_t pt_mask = (1u << a.log2_pt) - 1;
+  if (looks) {
+    // pages that are begun, and new ones
+    if (ok) {
+      for (uint32_t r = r0; r < r1; ++r) {
+        const int32_t c = a.ctx[r];
+        if (a.fresh[r] > 0 && (c & pt_mask)) {
+          const int32_t p = a.table[(uint64_t)r * a.max_blocks + (c >> a.log2_pt)];
+          if (p < 0 || p >= page_limit) atomicMin(&bad_detail, r);
+        }
+      }
+      constexpr int kAhead = 8;
+      for (long long i0 = t; i0 < total.pages; i0 += kAhead * kThreads) {
+        int32_t p[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) p[e] = i0 + e * kThreads < total.pages ? a.free_pages[head + i0 + e * kThreads] : 0;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          if (p[e] >= 0 && p[e] < page_limit) continue;
+          const long long i = i0 + e * kThreads;
+          uint32_t r = 0;  // the request that takes it
+          while (before[r / run + 1].pages <= i) r += run;
+          for (long long j = i - before[r / run].pages;; ++r) {
+            j -= pages_of((long long)a.ctx[r] + a.fresh[r], a.log2_pt) - pages_of(a.ctx[r], a.log2_pt);
+            if (j < 0) break;
+          }
+          atomicMin(&bad_detail, r);
+        }
+      }
+      __syncthreads();
+      detail = bad_detail;
+      if (detail != 0xFFFFFFFFu) code = SHN_ERR_INVALID_ARG;
+      else detail = 0;
+    }
+    if (t == 0) a.st->status = code, a.st->detail = detail;
+    return;
   }
   if (rank == 0 && t == 0) {
     *a.free_next = (int32_t)(ok ? head + total.pages : head);
@@ -111,8 +150,6 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
       tok += a.fresh[r];
     }
   }
-  const int32_t page_limit = (int32_t)(0x7FFFFFFFu >> a.log2_pt);
-  const uint32_t pt_mask = (1u << a.log2_pt) - 1;
   // new pages into the table
   if (ok) {
     for (long long i = rank * kThreads + t; i < total.pages; i += (long long)ranks * kThreads) {
@@ -128,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
         if (j < need) {
           const int32_t p = a.free_pages[head + i];
           a.table[(uint64_t)r * a.max_blocks + have + j] = p;
-          if (p < 0 || p >= page_limit) report(a.st, SHN_ERR_INVALID_ARG, r);
+          if (kOne && (p < 0 || p >= page_limit)) report(a.st, SHN_ERR_INVALID_ARG, r);
           break;
         }
         j -= need;
@@ -151,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
           const long long b = pos >> a.log2_pt;
           const int32_t p = b < have ? a.table[(uint64_t)r * a.max_blocks + b] : a.free_pages[head + pages + b - have];
           if (p >= 0 && p < page_limit) slot = (int32_t)(((uint32_t)p << a.log2_pt) + (pos & pt_mask));
-          else report(a.st, SHN_ERR_INVALID_ARG, r);
+          else if (kOne) report(a.st, SHN_ERR_INVALID_ARG, r);
           break;
         }
         j -= f;
@@ -166,17 +203,21 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t s) {
-  // one block up to 2 tokens a thread: a second launch costs about what they do (4.7 against 5.5 us at 900 tokens, 5.6 both at
-  // 1900, 7.8 against 5.5 at 3900)
-  if (a.max_tokens <= 2 * kThreads) {
+  // one block up to a token a thread (256 tokens 4.1 us, 4.4 with a block more for the status; 900 tokens 4.5 and 4.8; with two
+  // tokens a thread 1500 tokens 5.5 and 4.7)
+  if (a.max_tokens <= kThreads) {
     kv_plan_kernel<true><<<1, kThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
-  kv_plan_begin_kernel<<<1, 32, 0, s>>>(a);
+  const uint32_t most = 2u * sm_count_for_launch() - 1, blocks = (a.max_tokens + kThreads - 1) / kThreads;
+  const dim3 grid(1 + (blocks < most ? blocks : most));
+  if (a.free_head != a.free_next) return launch_first(kv_plan_kernel<false>, grid, kThreads, 0, s, a);
+  KvPlanArgs b = a;
+  int32_t* kept = reinterpret_cast<int32_t*>(a.st) + 2;
+  b.free_head = kept;
+  kv_plan_begin_kernel<<<1, 32, 0, s>>>(a, kept);
   const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const uint32_t most = 2u * sm_count_for_launch(), blocks = (a.max_tokens + kThreads - 1) / kThreads;
-  return launch_behind(kv_plan_kernel<false>, dim3(blocks < most ? blocks : most), kThreads, 0, s, a);
+  return e == cudaSuccess ? launch_behind(kv_plan_kernel<false>, grid, kThreads, 0, s, b) : e;
 }
 
 }  // namespace shn

@@ -141,6 +141,37 @@ def test_plan_reports_a_bad_page():
     assert slots.tolist() == [-1, -1, 3 * 16 + 14, 3 * 16 + 15, -1, -1, -1, -1]
 
 
+@pytest.mark.parametrize("n,new", [(40, 100), (1500, 3)])
+def test_plan_of_many_tokens_reports_the_first_bad_page(n, new):
+    """Pages that are begun and pages from the list, those of a request that takes no token aside; the head in place or not."""
+    pt = 16
+    ctx = [5 if r % 3 else 0 for r in range(n)]
+    fresh = [new if r % 5 else 0 for r in range(n)]
+    pages = [-(-(c + m) // pt) - -(-c // pt) for c, m in zip(ctx, fresh)]
+    begun = [r for r in range(n) if ctx[r] and fresh[r]]
+    takes = [r for r in range(n) if pages[r]]
+    far = (2**31 - 1) // pt
+    width = max(pages) + 1
+    for bad_begun, bad_new in ((begun[3], None), (None, takes[1]), (None, takes[-1]), (begun[-1], takes[2]), (begun[1], takes[-2]), (None, None)):
+        for in_place in (False, True):
+            table = [[r] + [-1] * (width - 1) if c else [-1] * width for r, c in enumerate(ctx)]
+            table[5][0] = -3  # (request 5 takes no token)
+            if bad_begun is not None:
+                table[bad_begun][0] = -2
+            free = [n + i for i in range(sum(pages) + 2)]
+            if bad_new is not None:
+                free[1 + sum(pages[:bad_new])] = far
+            nxt, cu, kv_len, pos, slots = plan_buffers(n, sum(fresh) + 9)
+            head, w = ints([1]), work()
+            kv.shn_kv_plan(ints(ctx), ints(fresh), pt, ints(table), ints(free), head, head if in_place else nxt, cu, kv_len, pos, slots, w)
+            bad = [r for r in (bad_begun, bad_new) if r is not None]
+            assert status(w) == ((shn.SHN_ERR_INVALID_ARG, min(bad)) if bad else (0, 0))
+            assert (head if in_place else nxt).item() == 1 + sum(pages)
+            none = sum(min(fresh[r], pt - ctx[r]) for r in bad[:1] if r == bad_begun) + sum(
+                min(pt, fresh[r] - (pt - ctx[r]) % pt) for r in bad if r == bad_new)
+            assert (slots[:sum(fresh)] < 0).sum().item() == none
+
+
 def test_plan_of_nothing():
     w = work()
     e = ints([])
