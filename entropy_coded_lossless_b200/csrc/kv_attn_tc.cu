@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   const uint32_t place = kSplit ? blockIdx.x / pl.splits : blockIdx.x, rank = kSplit ? blockIdx.x % pl.splits : 0;
   const uint32_t group = a.q_heads / c.kv_heads, hk = place % c.kv_heads;
 
-  if constexpr (!kPart) after_previous();  // (parts of a prefix: the call's first kernel)
-  let_next();
+  if constexpr (kPart) let_next();  // the call's first kernel
+  else after_previous();            // the last
   const uint32_t status = kPart ? 0 : *reinterpret_cast<volatile uint32_t*>(&a.st->status);
   Work w;
   if constexpr (kPart) find_part(c, a, pl, group, w);

@@ -11,10 +11,10 @@
  * Conventions are those of shn.h: caller-owned memory, asynchronous on `stream`, on the device that is
  * current for the calling thread; errors the host can see are returned and nothing is enqueued; errors
  * only the device can see (a page id outside the cache, more tokens than a buffer holds) go to the
- * status word at the start of the caller's workspace (d_work), which every call clears first. A workspace
- * serves one call at a time: calls whose GPU work may overlap (other streams, replays of other
- * graphs) need one each. Everything can be captured into a CUDA graph: lengths, tables and counts are
- * read on the device, the host arguments are sizes of buffers.
+ * status word at the start of the caller's workspace (d_work), which every call sets (0: no error, and what
+ * stood in the workspace before does not matter). A workspace serves one call at a time: calls whose GPU work
+ * may overlap (other streams, replays of other graphs) need one each. Everything can be captured into a CUDA
+ * graph: lengths, tables and counts are read on the device, the host arguments are sizes of buffers.
  * Results do not depend on timing: the same inputs give the same bits.
  *
  * Token t of request r lies in page block_table[r][t / page_tokens], at t % page_tokens. A slot is
@@ -131,9 +131,9 @@ int shn_kv_load(const shn_kv_cache* cache, const int32_t* d_slots, uint32_t n_to
  * aside), scores, their scalings, the softmax and the sums are float32. Before the second product a weight is rounded to
  * fp16, and a value is fp16(int8 * fp16(scale)): 2^-11 each. Weights below 2^-24 times the ratio of the largest value scale of the
  * sequence to the token's are lost, so results are exact to 2^-24 of the sequence's largest value.
- * (The sequence: all tokens up to the last query's of 128 rows, in whole tiles of 128; so the size of a finite value scale counts for
- * rows of a few earlier queries too.) A token whose value scale is not finite (or 1e36 and more) makes the rows that see it
- * NaN; rows that do not see it are not touched, nor by what stands behind a sequence's end in its last page.
+ * (The sequence: the tokens that the last of 256 rows sees, so the size of a value scale counts for rows of a few
+ * earlier queries too.) A token whose value scale is not finite (or 1e36 and more) makes the rows that see it NaN and
+ * leaves the others alone, and so does what stands behind a sequence's end in its last page.
  * Device errors: SHN_ERR_INVALID_ARG for a page id outside the cache (detail = the request; that page counts as zeros),
  * a d_kv_len that the table row cannot hold (taken as what it holds) or a d_cu_q that decreases or leaves
  * [0, n_tokens] (those queries are left out); SHN_ERR_TIMEOUT if a wait inside a kernel gave up (a quarter of a second; the
