@@ -10,15 +10,15 @@ __global__ void kv_begin_kernel(DeviceStatus* st) {
   if (threadIdx.x == 0) st->status = 0, st->detail = 0;
 }
 
-// The status of a call whose errors its indexes alone show. Up to kOneTokens tokens (kOne) one block looks at all of them in
-// one turn and is the only one to write the status, so no kernel has to clear it first: 64 tokens stored and loaded again
-// 4.97 us against 6.25 with one in front of each (in a run of calls 8.2 and 10.6), 8191 of them 63.7 against 64.9. With more
-// tokens that block would need more turns than others do, and its registers cost the others places (65,536 tokens loaded in
-// 88.7 us against 75.9): then the kernel in front clears the status and every block reports what it finds.
-constexpr int kThreads = 256, kAhead = 8;  // (16-byte loads of a thread on their way together)
-constexpr uint32_t kOneTokens = 4 * kAhead * kThreads;
+// The status of a call whose errors its indexes alone show. Up to kOneTokens tokens (kOne) one block looks at all of them
+// and is the only one to write the status, so no kernel has to clear it first: 64 tokens stored and loaded again 4.97 us
+// against 6.25 with one in front of each (in a run of calls 8.2 and 10.6), 8191 of them 63.7 against 64.9. With more tokens
+// that block would be the last to end, and its registers cost the others places (65,536 tokens loaded in 88.7 us against
+// 75.9): then the kernel in front clears the status and every block reports what it finds.
+constexpr uint32_t kOneTokens = 8192;
+constexpr int kAhead = 8;  // 16-byte loads of a thread on their way together
 // The first of the n indexes that is outside [0, end); negative ones are fine where kNone.
-template <bool kNone>
+template <bool kNone, int kThreads>
 __device__ __forceinline__ uint32_t first_outside(const int32_t* p, uint32_t n, uint32_t end) {
   const uint32_t t = threadIdx.x;
   const uint32_t lead = min(n, (uint32_t)(-(reinterpret_cast<uintptr_t>(p) >> 2) & 3)), quads = (n - lead) / 4, tail = lead + 4 * quads;
@@ -29,19 +29,23 @@ __device__ __forceinline__ uint32_t first_outside(const int32_t* p, uint32_t n, 
   if (t < lead) look(p[t], t);
   if (tail + t < n) look(p[tail + t], tail + t);
   const int4* v = reinterpret_cast<const int4*>(p + lead);
-  int4 x[kAhead];
+#pragma unroll 1
+  for (uint32_t i0 = t; i0 < quads; i0 += kAhead * kThreads) {
+    int4 x[kAhead];
 #pragma unroll
-  for (int e = 0; e < kAhead; ++e) {
-    const uint32_t i = e * kThreads + t;
-    if (i < quads) x[e] = v[i];
-  }
+    for (int e = 0; e < kAhead; ++e) {
+      const uint32_t i = i0 + e * kThreads;
+      if (i < quads) x[e] = v[i];
+    }
 #pragma unroll
-  for (int e = 0; e < kAhead; ++e) {
-    const uint32_t i = e * kThreads + t, at = lead + 4 * i;
-    if (i < quads) look(x[e].x, at), look(x[e].y, at + 1), look(x[e].z, at + 2), look(x[e].w, at + 3);
+    for (int e = 0; e < kAhead; ++e) {
+      const uint32_t i = i0 + e * kThreads, at = lead + 4 * i;
+      if (i < quads) look(x[e].x, at), look(x[e].y, at + 1), look(x[e].z, at + 2), look(x[e].w, at + 3);
+    }
   }
   return first;
 }
+template <int kThreads>
 __device__ __forceinline__ void write_status(DeviceStatus* st, uint32_t first) {
   __shared__ uint32_t least[kThreads / 32];
   first = __reduce_min_sync(~0u, first);
@@ -62,8 +66,11 @@ __device__ __forceinline__ void write_status(DeviceStatus* st, uint32_t first) {
 // All arithmetic is float32 (two values an instruction); the query is rounded once to bf16, key and value once to INT8:
 // issuing instructions bounds this about as much as memory, so a row has one division and one reciprocal, and y / scale is
 // rounded by adding 1.5 * 2^23, which leaves the integer in the last byte.
-// Measured (8191 tokens, 32 query and 8 key heads of 128): 54 us for 190 MB, 3.5 TB/s, with 62 % of the issue slots taken. With
-// the tokens dealt out by a division, a block each, a call and the load behind it took 89 us; like this 68.
+// Measured (8191 tokens, 32 query and 8 key heads of 128): 43 us for 190 MB, 4.4 TB/s, 67 % of the measured copy rate.
+// Small blocks, each with its token: what a warp does once for a token (rotation, addresses) then serves more rows, and
+// tokens of few rows leave no warp idle. 64 threads, 14 blocks to an SM: 42.9 us, and 8191 tokens of 8 query and 8 key heads
+// of 64 11.8; 128 threads, 6 blocks 44.4 and 14.3; 256 threads, 3 blocks 53.5 and 23.0; 32 threads, 24 blocks 48.5 and 9.6.
+constexpr int kStoreThreads = 64, kStoreBlocks = 14;
 constexpr int kAtOnce = 4;  // query rows of a lane that are on their way together
 
 // A lane's 8 values of a row, two by two: [0], [1] the first 4, [2], [3] the other 4.
@@ -111,14 +118,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 template <int D, bool kOne>
-__global__ void __launch_bounds__(kThreads, 3) kv_store_kernel(KvPages c, KvStoreArgs a) {
+__global__ void __launch_bounds__(kStoreThreads, kStoreBlocks) kv_store_kernel(KvPages c, KvStoreArgs a) {
   using namespace tc;
-  constexpr uint32_t kLanes = D / 8, kGroups = kThreads / kLanes;
+  constexpr uint32_t kLanes = D / 8, kGroups = kStoreThreads / kLanes;
   if (kOne && blockIdx.x == 0) {
     if (blockIdx.y) return;
-    uint32_t first = first_outside<true>(a.slots, a.n_tokens, c.n_pages << c.log2_pt);
-    if (a.rot) first = min(first, first_outside<false>(a.positions, a.n_tokens, a.n_positions));
-    return write_status(a.st, first);
+    uint32_t first = first_outside<true, kStoreThreads>(a.slots, a.n_tokens, c.n_pages << c.log2_pt);
+    if (a.rot) first = min(first, first_outside<false, kStoreThreads>(a.positions, a.n_tokens, a.n_positions));
+    return write_status<kStoreThreads>(a.st, first);
   }
   const uint32_t block = blockIdx.x - kOne, blocks = gridDim.x - kOne;
   const uint32_t lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
@@ -277,16 +284,18 @@ __global__ void __launch_bounds__(kThreads, 3) kv_store_kernel(KvPages c, KvStor
 // of them on its way took 97.
 __device__ __forceinline__ float int8_of(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
 
+constexpr int kLoadThreads = 256;
+
 template <int D, bool kOne>
-__global__ void __launch_bounds__(kThreads) kv_load_kernel(KvPages c, KvLoadArgs a) {
+__global__ void __launch_bounds__(kLoadThreads) kv_load_kernel(KvPages c, KvLoadArgs a) {
   constexpr uint32_t kLanes = D / 16;
   if (kOne && blockIdx.x == 0) {
-    if (blockIdx.y == 0) write_status(a.st, first_outside<true>(a.slots, a.n_tokens, c.n_pages << c.log2_pt));
+    if (blockIdx.y == 0) write_status<kLoadThreads>(a.st, first_outside<true, kLoadThreads>(a.slots, a.n_tokens, c.n_pages << c.log2_pt));
     return;
   }
   const uint32_t lane = threadIdx.x % kLanes;
   // rows of the block: so many tokens, or a part of one token's rows where it has more than a block
-  const uint32_t sub = threadIdx.x / kLanes, kSubs = kThreads / kLanes;
+  const uint32_t sub = threadIdx.x / kLanes, kSubs = kLoadThreads / kLanes;
   const uint32_t tokens = max(1u, kSubs / c.kv_heads);
   const uint32_t token = (blockIdx.x - kOne) * tokens + (tokens > 1 ? sub / c.kv_heads : 0);
   const uint32_t h = tokens > 1 ? sub % c.kv_heads : blockIdx.y * kSubs + sub;
@@ -328,37 +337,37 @@ cudaError_t launch_kv_begin(DeviceStatus* st, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_store(const KvPages& c, uint32_t head_dim, const KvStoreArgs& a, int sm_count, cudaStream_t s) {
-  const uint32_t groups = kThreads * 8 / head_dim, rows = a.q_heads > 2 * c.kv_heads ? a.q_heads : 2 * c.kv_heads;
-  // few tokens: their rows over several blocks, until the SMs have two blocks each or a block has one row per group (64 tokens,
-  // 32 query and 8 key heads of 128, the load behind it counted: 6.25 us; 6.53 with a block for all of a token's rows)
+  const uint32_t groups = kStoreThreads * 8 / head_dim, rows = a.q_heads > 2 * c.kv_heads ? a.q_heads : 2 * c.kv_heads;
+  // few tokens: their rows over several blocks, until the SMs have 8 blocks each or a block has one row per group (a token, 32
+  // query and 8 key heads of 128, 2.3 us; 2.5 with fewer and larger blocks)
   uint32_t parts = 1;
-  while ((uint64_t)parts * a.n_tokens < 2ull * sm_count && parts * groups < rows) ++parts;
-  // three blocks to an SM, each with its tokens (or the status)
+  while ((uint64_t)parts * a.n_tokens < 8ull * sm_count && parts * groups < rows) ++parts;
+  // as many blocks as the SMs have places, each with its tokens (or the status)
   if (a.n_tokens > kOneTokens) {
     const cudaError_t e = launch_kv_begin(a.st, s);
     if (e != cudaSuccess) return e;
-    const dim3 grid(a.n_tokens < 3u * sm_count ? a.n_tokens : 3u * sm_count, parts);
-    return head_dim == 128 ? launch_behind(kv_store_kernel<128, false>, grid, kThreads, 0, s, c, a)
-                           : launch_behind(kv_store_kernel<64, false>, grid, kThreads, 0, s, c, a);
+    const dim3 grid(a.n_tokens < kStoreBlocks * (uint32_t)sm_count ? a.n_tokens : kStoreBlocks * (uint32_t)sm_count, parts);
+    return head_dim == 128 ? launch_behind(kv_store_kernel<128, false>, grid, kStoreThreads, 0, s, c, a)
+                           : launch_behind(kv_store_kernel<64, false>, grid, kStoreThreads, 0, s, c, a);
   }
-  const uint32_t most = 3u * sm_count - 1;
+  const uint32_t most = kStoreBlocks * (uint32_t)sm_count - 1;
   const dim3 grid(1 + (a.n_tokens < most ? a.n_tokens : most), parts);
-  if (head_dim == 128) kv_store_kernel<128, true><<<grid, kThreads, 0, s>>>(c, a);
-  else kv_store_kernel<64, true><<<grid, kThreads, 0, s>>>(c, a);
+  if (head_dim == 128) kv_store_kernel<128, true><<<grid, kStoreThreads, 0, s>>>(c, a);
+  else kv_store_kernel<64, true><<<grid, kStoreThreads, 0, s>>>(c, a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_load(const KvPages& c, uint32_t head_dim, const KvLoadArgs& a, cudaStream_t s) {
-  const uint32_t subs = kThreads / (head_dim / 16), tokens = c.kv_heads < subs ? subs / c.kv_heads : 1;
+  const uint32_t subs = kLoadThreads / (head_dim / 16), tokens = c.kv_heads < subs ? subs / c.kv_heads : 1;
   const uint32_t blocks = (a.n_tokens + tokens - 1) / tokens, parts = tokens > 1 ? 1 : (c.kv_heads + subs - 1) / subs;
   if (a.n_tokens > kOneTokens) {
     const cudaError_t e = launch_kv_begin(a.st, s);
     if (e != cudaSuccess) return e;
-    return head_dim == 128 ? launch_behind(kv_load_kernel<128, false>, dim3(blocks, parts), kThreads, 0, s, c, a)
-                           : launch_behind(kv_load_kernel<64, false>, dim3(blocks, parts), kThreads, 0, s, c, a);
+    return head_dim == 128 ? launch_behind(kv_load_kernel<128, false>, dim3(blocks, parts), kLoadThreads, 0, s, c, a)
+                           : launch_behind(kv_load_kernel<64, false>, dim3(blocks, parts), kLoadThreads, 0, s, c, a);
   }
-  if (head_dim == 128) kv_load_kernel<128, true><<<dim3(1 + blocks, parts), kThreads, 0, s>>>(c, a);
-  else kv_load_kernel<64, true><<<dim3(1 + blocks, parts), kThreads, 0, s>>>(c, a);
+  if (head_dim == 128) kv_load_kernel<128, true><<<dim3(1 + blocks, parts), kLoadThreads, 0, s>>>(c, a);
+  else kv_load_kernel<64, true><<<dim3(1 + blocks, parts), kLoadThreads, 0, s>>>(c, a);
   return cudaGetLastError();
 }
 
