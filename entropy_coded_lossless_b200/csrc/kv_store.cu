@@ -12,9 +12,9 @@ __global__ void kv_begin_kernel(DeviceStatus* st) {
 
 // The status of a call whose errors its indexes alone show. Up to kOneTokens tokens (kOne) one block looks at all of them
 // and is the only one to write the status, so no kernel has to clear it first: 64 tokens stored and loaded again 4.97 us
-// against 6.25 with one in front of each (in a run of calls 8.2 and 10.6), 8191 of them 63.7 against 64.9. With more tokens
-// that block would be the last to end, and its registers cost the others places (65,536 tokens loaded in 88.7 us against
-// 75.9): then the kernel in front clears the status and every block reports what it finds.
+// against 5.99 with one in front of each, 8000 53.5 against 54.8. With more tokens that block would be the last to end (65,536
+// tokens of one head of 64 loaded in 21.2 us against 7.8): then the kernel in front clears the status and every block
+// reports what it finds.
 constexpr uint32_t kOneTokens = 8192;
 constexpr int kAhead = 8;  // 16-byte loads of a thread on their way together
 // The first of the n indexes that is outside [0, end); negative ones are fine where kNone.
@@ -280,11 +280,12 @@ __global__ void __launch_bounds__(kStoreThreads, kStoreBlocks) kv_store_kernel(K
 // ---- shn_kv_load --------------------------------------------------------------------------------
 // HBM-bound copy with a scale: 16 INT8 values (16 bytes) in and 32 bytes out per lane, D/16 lanes to a row, keys and values of
 // the row together. A token's rows are a block's neighbours, so its slot is read from L1 by all but the first.
-// Measured (65,536 tokens, 8 heads of 128): 78 us for 407 MB, 5.2 TB/s, 80 % of the measured copy rate; a loop over rows with one
-// of them on its way took 97.
-__device__ __forceinline__ float int8_of(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
+// Read and written once, so as streaming data that leaves the L2 first, and in small blocks, which end and begin more evenly.
+// Measured (65,536 tokens, 8 heads of 128): 67 us for 407 MB, 6.0 TB/s, 92 % of the measured copy rate; blocks of 128 threads
+// 69.5, of 256 70.9, those without the streaming hints 76.1; a loop over rows with one of them on its way 97.
+constexpr int kLoadThreads = 64;
 
-constexpr int kLoadThreads = 256;
+__device__ __forceinline__ float int8_of(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
 
 template <int D, bool kOne>
 __global__ void __launch_bounds__(kLoadThreads) kv_load_kernel(KvPages c, KvLoadArgs a) {
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kLoadThreads) kv_load_kernel(KvPages c, KvLoad
   float s[2];
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    raw[kv] = *reinterpret_cast<const uint4*>((kv ? c.v : c.k) + at * D + lane * 16);
+    raw[kv] = __ldcs(reinterpret_cast<const uint4*>((kv ? c.v : c.k) + at * D + lane * 16));
     s[kv] = (kv ? c.v_scale : c.k_scale)[at];
   }
 #pragma unroll
@@ -324,8 +325,8 @@ __global__ void __launch_bounds__(kLoadThreads) kv_load_kernel(KvPages c, KvLoad
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = bf16_pack(int8_of(w[j / 2], 2 * (j % 2)) * s[kv], int8_of(w[j / 2], 2 * (j % 2) + 1) * s[kv]);
     uint4* dst = reinterpret_cast<uint4*>(out + (uint64_t)token * (kv ? a.v_stride : a.k_stride) + (uint64_t)h * D + lane * 16);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+    __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
   }
 }
 
