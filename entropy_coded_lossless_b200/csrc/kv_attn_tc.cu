@@ -245,7 +245,8 @@ __device__ __forceinline__ void join_parts(uint32_t base, uint32_t ranks, uint32
   }
 }
 
-// kSplit: pl.splits blocks of a cluster share the tokens of 256 rows, and the rows of the result (join_parts).
+// kSplit (grids of no more blocks than SMs): pl.splits blocks of a cluster, or one, share the tokens of 256 rows, and the rows
+// of the result (join_parts).
 template <int D, bool kPart, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAttnArgs a, DecodePlan pl) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -407,6 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       seen[r] = seen_by(half * 128 + lanes + quad + 8 * r);
       m[r] = -INFINITY, l[r] = 0.f, neg[r] = 0.f, limit[r] = seen[r] ? -1.f : INFINITY;  // (no reference yet: any sum passes)
     }
+    // A warp whose rows are all behind the last one keeps step and does no more: its places in TMEM hold anything, and so do
+    // these rows' sums, which nobody reads (one query after 5102 tokens 29.6 -> 25.8 us, 24 short requests 14.4 -> 12.8). Not for
+    // full grids, whose blocks have few such rows: there the question alone costs 7 % (8192 tokens 627 -> 673 us).
+    if (kSplit && half * 128 + lanes >= rows_here) seen[0] = -1;
     bool ok = true;
     for (uint32_t j = 0; j < tiles && ok; ++j) {
       ok = __all_sync(~0u, bar_wait(bars + kScaleFull + 8 * (j & 3), (j >> 2) & 1, stop));
@@ -432,6 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       for (int h = 0; h < 2; ++h) {
         ok = __all_sync(~0u, bar_wait(bars + kSFull + 16 * half + 8 * h, j & 1, stop));
         if (!ok) break;
+        if (kSplit && seen[0] < 0) {  // (see above)
+          if (lane == 0 && h == 1) bar_arrive(bars + kPFull + 16 * half);
+          continue;
+        }
         fence_after();
         // s[4n + 2r + e]: row quad + 8r, column 64h + 8n + col + e
         uint32_t s[32];
@@ -788,12 +797,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       const uint32_t i = warp - kIssueWarp;
       constexpr uint32_t kS = instr_desc(128, 64, false), kO = instr_desc(128, D, true);
       const bool lead = elect_one();
+      const bool real = !kSplit || i * 128 < rows_here;  // (a row tile without rows has no products, only their barriers)
       // Both for the tokens 64 h .. 64 h + 63 of tile j.
       auto scores = [&](uint32_t j, uint32_t h) {
         const uint32_t q = smem_desc(base + L::q + i * L::kOperand, 16), k = smem_desc(base + L::k + (j & 1) * L::kOperand + h * 8192, 16);
         const uint32_t d = tmem + 128 * i + 64 * ((j + h) & 1);
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) {
+        for (int e = 0; real && e < D / 16; ++e) {
           const uint32_t off = ((e / 4) * kHalf + (e % 4) * 32) >> 4;
           if (e == 0) mma_ss<false>(d, q + off, k + off, kS, lead);
           else mma_ss<true>(d, q + off, k + off, kS, lead);
@@ -804,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         const uint32_t v = smem_desc(base + L::v + (j & 1) * L::kOperand, kHalf) + h * (4 * 2048 >> 4);
         const uint32_t p = tmem + 128 * i + 64 * (j & 1) + 32 * h;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mma_ts(tmem + 256 + D * i, p + 8 * e, v + e * (2048 >> 4), kO, j > 0 || h > 0 || e > 0, lead);
+        for (int e = 0; real && e < 4; ++e) mma_ts(tmem + 256 + D * i, p + 8 * e, v + e * (2048 >> 4), kO, j > 0 || h > 0 || e > 0, lead);
         commit(bars + kOFull + 16 * i + 8 * h, lead);
       };
       auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(~0u, bar_wait(bars + bar, parity, stop)); };
@@ -876,12 +886,12 @@ cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnAr
   DecodePlan pl = {};
   pl.splits = 1;
   // Few blocks, and requests that may be long: several blocks to the same rows, as many as the SMs have places and the longest
-  // sequence tiles. Measured, with and without: one query after 5102 tokens (8 heads on one) 29.6 / 118.8 us, 700 after 2551 (8 on
-  // 2) 33.8 / 74.6, 40 after 5102 (32 on 8, of 64) 26.9 / 102.1. With 4 blocks to a row at most they take 42.4, 34.2 and
+  // sequence tiles. Measured, with and without: one query after 5102 tokens (8 heads on one) 25.9 / 118.8 us, 700 after 2551 (8 on
+  // 2) 34.4 / 74.6, 40 after 5102 (32 on 8, of 64) 26.6 / 102.1. With 4 blocks to a row at most they take 42.4, 34.2 and
   // 37.8, with up to twice the blocks that have places 29.7, 49.1 and 27.0.
   const uint64_t tokens = (uint64_t)a.max_blocks << c.log2_pt;  // what a request can have
   while (pl.splits < 8 && blocks * pl.splits * 2 <= (uint64_t)sm_count && tokens > 2 * pl.splits * kTile) pl.splits *= 2;
-  if (pl.splits > 1) return head_dim == 128 ? launch<128, false, true>(blocks, c, a, pl, s) : launch<64, false, true>(blocks, c, a, pl, s);
+  if (blocks <= (uint64_t)sm_count) return head_dim == 128 ? launch<128, false, true>(blocks, c, a, pl, s) : launch<64, false, true>(blocks, c, a, pl, s);
   return head_dim == 128 ? launch<128, false, false>(blocks, c, a, pl, s) : launch<64, false, false>(blocks, c, a, pl, s);
 }
 
