@@ -72,7 +72,7 @@ constexpr uint64_t kPrefixUnits = 12288, kPrefixGroups = 64;
 constexpr uint64_t kSplitBlocks = 148;
 
 // How shn_kv_attn_shared is cut up, and its workspace: [status 256][pieces' sums][pieces' (mt, ms, l)][the same of the prefix's
-// parts][blocks' errors].
+// parts][blocks' errors]. For one request at least: an empty batch has no layout, only a status word.
 struct SharedLayout {
   DecodePlan pl;
   size_t out_off, ml_off, split_off, split_ml_off, errors_off, total;
@@ -219,7 +219,7 @@ size_t shn_kv_attn_shared_workspace_bytes(const shn_kv_cache* cache, uint32_t n_
   if (check_cache(cache) != SHN_OK || q_heads == 0 || q_heads % cache->kv_heads ||
       q_heads / cache->kv_heads > kMaxGroup || n_reqs >= (1u << 31) / q_heads)
     return 0;
-  return shared_layout(cache, n_reqs, q_heads).total;
+  return n_reqs ? shared_layout(cache, n_reqs, q_heads).total : SHN_KV_WORKSPACE_BYTES;
 }
 
 int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, uint32_t q_heads,
@@ -233,18 +233,21 @@ int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, 
   if (!d_prefix_len || (n_prefix_pages && !d_prefix_pages) ||
       (uint64_t)n_prefix_pages * cache->page_tokens >= (1ull << 31))
     return SHN_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n_reqs == 0) {
+    e = check_work(d_work, work_bytes, SHN_KV_WORKSPACE_BYTES);
+    return e != SHN_OK ? e : clear_status(d_work, s) ? SHN_OK : SHN_ERR_CUDA;
+  }
   SharedLayout x = shared_layout(cache, n_reqs, q_heads);
   e = check_work(d_work, work_bytes, x.total);
   if (e != SHN_OK) return e;
-  if (n_reqs && d_q == d_out) return SHN_ERR_INVALID_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d_q == d_out) return SHN_ERR_INVALID_ARG;
   KvAttnArgs a = {};
   a.q = d_q, a.q_stride = q_stride, a.n_tokens = n_reqs, a.q_heads = q_heads;
   a.table = d_block_table, a.max_blocks = max_blocks, a.kv_len = d_kv_len, a.n_reqs = n_reqs;
   a.prefix_pages = d_prefix_pages, a.n_prefix_pages = n_prefix_pages, a.prefix_len = d_prefix_len;
   a.scale = softmax_scale, a.out = d_out, a.out_stride = out_stride;
   a.st = static_cast<DeviceStatus*>(d_work);  // the last kernel sets it
-  if (n_reqs == 0) return clear_status(d_work, s) ? SHN_OK : SHN_ERR_CUDA;
   uint8_t* wb = static_cast<uint8_t*>(d_work);
   x.pl.out = reinterpret_cast<float*>(wb + x.out_off);
   x.pl.ml = reinterpret_cast<float4*>(wb + x.ml_off);
