@@ -92,16 +92,22 @@ SharedLayout shared_layout(const shn_kv_cache* c, uint32_t n_reqs, uint32_t q_he
   x.pl.splits = blocks >= kSplitBlocks ? 1 : (uint32_t)(kSplitBlocks / blocks);
   const uint64_t groups = (rows + x.pl.rows - 1) / x.pl.rows;
   x.pl.prefix_groups = groups <= kPrefixGroups ? (uint32_t)groups : 0;
-  const uint64_t segs = (uint64_t)c->kv_heads * (x.pl.prefix_groups + (uint64_t)n_reqs * x.pl.own_groups);
+  // Places for the most that any number of requests up to this one needs (a workspace serves smaller batches too), although
+  // splits and prefix_groups fall as rows are added: prefix_groups are at most kPrefixGroups; parts' rows are at most
+  // kSplitBlocks * 256 where there are several splits (256 rows to a block), and blocks * splits at most kSplitBlocks.
+  const uint64_t segs = (uint64_t)c->kv_heads * ((groups < kPrefixGroups ? groups : kPrefixGroups) + (uint64_t)n_reqs * x.pl.own_groups);
   const uint64_t pieces = (kDecodeMaxWarps + segs) * x.pl.rows;
-  const uint64_t parts = (uint64_t)x.pl.splits * n_reqs * q_heads;
+  const uint64_t all_rows = (uint64_t)n_reqs * q_heads, most_splits = c->kv_heads < kSplitBlocks ? kSplitBlocks / c->kv_heads : 1;
+  const uint64_t split_rows = all_rows * most_splits < kSplitBlocks * 256 ? all_rows * most_splits : kSplitBlocks * 256;
+  const uint64_t parts = all_rows > split_rows ? all_rows : split_rows;
+  const uint64_t part_blocks = blocks > kSplitBlocks ? blocks : kSplitBlocks;
   x.out_off = 256;
   x.ml_off = x.out_off + round_up(pieces * c->head_dim * sizeof(float), 256);
   x.split_off = x.ml_off + round_up(pieces * sizeof(float4), 256);
   x.split_ml_off = x.split_off + round_up(parts * c->head_dim * sizeof(float), 256);
   x.errors_off = x.split_ml_off + round_up(parts * sizeof(float4), 256);
   x.prefix_tiles = blocks;
-  x.total = x.errors_off + round_up((blocks * x.pl.splits + kDecodeMaxWarps / (kDecodeThreads / 32)) * sizeof(uint32_t), 256);
+  x.total = x.errors_off + round_up((part_blocks + kDecodeMaxWarps / (kDecodeThreads / 32)) * sizeof(uint32_t), 256);
   return x;
 }
 

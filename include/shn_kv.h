@@ -151,7 +151,8 @@ int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens
  * row, which is indexed by the token's position as everywhere (so the pages of the prefix may stand there too,
  * but are not read). With *d_prefix_len = 0 this is plain decoding attention. kv_len 0 gives zeros.
  *  d_prefix_pages  device, [n_prefix_pages] (NULL if n_prefix_pages is 0); d_prefix_len: device, one value
- *  d_work          shn_kv_attn_shared_workspace_bytes, 256-byte aligned
+ *  d_work          shn_kv_attn_shared_workspace_bytes, 256-byte aligned; what holds n_reqs requests holds fewer too
+ *                  (same cache shape and q_heads)
  * Other arguments and device errors as shn_kv_attn_prompt; *d_prefix_len that the pages cannot hold is taken as what they
  * hold (SHN_ERR_INVALID_ARG). Arithmetic: as there for a large prefix (many query rows, many tokens); for a
  * smaller one and for the requests' own tokens values enter exactly too, their scales with the

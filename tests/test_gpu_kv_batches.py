@@ -54,3 +54,21 @@ def test_store_and_load_of_no_tokens():
     w = base.work()
     kv.shn_kv_load(cache, none, rows(0, 2, 64), None, w)
     assert base.status(w) == (0, 0)
+
+
+@pytest.mark.parametrize("h,hk,prefix", [(32, 8, 8192), (8, 2, 64), (6, 1, 4096)])
+def test_a_shrinking_batch_keeps_its_workspace(h, hk, prefix):
+    """The workspace of the largest batch, used again by smaller ones (whose prefix is cut into more parts)."""
+    pt, d, most = 64, 128, 100
+    own = [1 + n * 37 % 150 for n in range(most)]
+    table, pages = base.shared_tables(own, prefix, pt, 3)
+    cache = base.filled_cache(pages, hk, pt, d, seed=4)
+    q, front = base.bf16(most, h, d, seed=5), table[0, :prefix // pt].contiguous()
+    w = base.work(kv.attn_shared_workspace_bytes(cache, most, h))
+    for n in (100, 65, 64, 33, 1, 64, 100):
+        lens, a, b = base.ints([prefix + x for x in own[:n]]), rows(n, h, d), rows(n, h, d)
+        fresh = base.work(kv.attn_shared_workspace_bytes(cache, n, h))
+        for o, x in ((a, w), (b, fresh)):
+            kv.shn_kv_attn_shared(q[:n], cache, front, base.ints([prefix]), table[:n], lens, 0.1, o, x)
+            assert base.status(x) == (0, 0)
+        assert torch.equal(a, b) and torch.isfinite(a).all()

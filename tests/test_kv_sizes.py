@@ -32,3 +32,12 @@ def test_an_empty_batch_still_has_its_arguments_checked():
     for over, code in ((dict(work=None), shn.SHN_ERR_INVALID_ARG), (dict(work=P + 64), shn.SHN_ERR_INVALID_ARG), (dict(plen=None), shn.SHN_ERR_INVALID_ARG),
                        (dict(work_bytes=255), shn.SHN_ERR_WORKSPACE), (dict(h=12), shn.SHN_ERR_INVALID_ARG)):
         assert kv._lib().shn_kv_attn_shared(*{**f, **over}.values()) == code
+
+
+@pytest.mark.parametrize("hk,h,d", [(8, 32, 128), (1, 1, 128), (1, 64, 64), (4, 24, 64), (40, 40, 128), (148, 148, 64), (200, 400, 64), (1024, 1024, 128), (2, 34, 128)])
+def test_a_workspace_serves_smaller_batches_too(hk, h, d):
+    """A server sizes its workspace once, for its largest batch."""
+    c = cache(hk, d)
+    sizes = [size(c, n, h) for n in range(700)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:])), next((n, a, b) for n, (a, b) in enumerate(zip(sizes, sizes[1:])) if a > b)
+    assert size(c, 5000, h) >= sizes[-1]
