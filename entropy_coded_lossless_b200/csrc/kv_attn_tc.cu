@@ -84,7 +84,7 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
     const int32_t b = is ? a.cu_q[lane] : 0, e = is ? a.cu_q[lane + 1] : 0;
     len = is ? a.kv_len[lane] : 0;
     const bool bad = b < 0 || e < b || (uint32_t)e > a.n_tokens;
-    if (bad && warp == 0) report(a.st, SHN_ERR_INVALID_ARG, lane);
+    if (bad && warp == 0) report_first(a.st, SHN_ERR_INVALID_ARG, lane);
     const uint32_t own = bad ? 0 : ((uint32_t)(e - b) * group + kRows - 1) / kRows;
     uint32_t inc = own;
 #pragma unroll
@@ -109,7 +109,7 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
     for (uint32_t r = r0; r < r1; ++r) {
       const int32_t b = a.cu_q[r], e = a.cu_q[r + 1];
       kv_len = a.kv_len[r];
-      if (b < 0 || e < b || (uint32_t)e > a.n_tokens) report(a.st, SHN_ERR_INVALID_ARG, r);
+      if (b < 0 || e < b || (uint32_t)e > a.n_tokens) report_first(a.st, SHN_ERR_INVALID_ARG, r);
       else own += ((uint32_t)(e - b) * group + kRows - 1) / kRows;
     }
     uint32_t inc = own;
@@ -159,7 +159,7 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
   }
   const int64_t holds = (int64_t)a.max_blocks << c.log2_pt;
   if (len < 0 || len > holds) {
-    if (t == 0) report(a.st, SHN_ERR_INVALID_ARG, w.req);
+    if (t == 0) report_first(a.st, SHN_ERR_INVALID_ARG, w.req);
     len = len < 0 ? 0 : (int32_t)holds;
   }
   w.len = len;
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         p = table[(tok + skip) >> c.log2_pt];
         if (p < 0 || (uint32_t)p >= c.n_pages) {
           if (kPart) sts32(base + L::misc + 16, 0);
-          else if (lane < 8) report(a.st, SHN_ERR_INVALID_ARG, w.req);
+          else if (lane < 8) report_first(a.st, SHN_ERR_INVALID_ARG, w.req);
           p = -1;
         }
       }
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   if constexpr (kPart) {
     if (tid == 0) pl.errors[blockIdx.x] = lds32(stop) != 0 ? kGaveUp : lds32(base + L::misc + 16);
   } else {
-    if (tid == 0 && lds32(stop) != 0) report(a.st, SHN_ERR_TIMEOUT, w.req);
+    if (tid == 0 && lds32(stop) != 0) report_first(a.st, SHN_ERR_TIMEOUT, w.req);
   }
 }
 

@@ -37,6 +37,20 @@ __device__ __forceinline__ uint32_t bf16_pack(float lo, float hi) {
   return r;
 }
 
+// An error into the status, which is 0 before: of several of one kind the first request's (token's) stays, whoever comes
+// first, and a wait that gave up stands above what is wrong with the input.
+__device__ __forceinline__ void report_first(DeviceStatus* st, uint32_t code, uint32_t detail) {
+  unsigned long long *word = reinterpret_cast<unsigned long long*>(st), old = 0;
+  const unsigned long long mine = code | (unsigned long long)detail << 32;
+  for (;;) {
+    const unsigned long long now = atomicCAS(word, old, mine);
+    if (now == old) return;
+    const uint32_t is = (uint32_t)now;
+    if (is == code ? (uint32_t)(now >> 32) <= detail : is != 0 && code != SHN_ERR_TIMEOUT) return;
+    old = now;
+  }
+}
+
 // A call's first kernel is launched as any other; the next ones are launched so that they start while the one before still
 // runs (programmatic dependent launch) and hide their start behind it. A kernel launched so reads nothing that the one
 // before writes, and writes nothing that it reads, until after_previous(); let_next() lets the one after it start.

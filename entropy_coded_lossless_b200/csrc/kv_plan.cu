@@ -96,10 +96,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
   if (code == SHN_OK && (total.tokens > (long long)a.max_tokens || head + total.pages > (long long)a.n_free))
     code = SHN_ERR_CAPACITY;
   const bool ok = code == SHN_OK;
-  if constexpr (kOne) {
-    if (t == 0) a.st->status = code, a.st->detail = detail;
-    __syncthreads();  // the head is read and the status set before anything is written
-  }
+  if constexpr (kOne) __syncthreads();  // the head and what was found are read before anything is written
   const int32_t page_limit = (int32_t)(0x7FFFFFFFu >> a.log2_pt);
   const uint32_t pt_mask = (1u << a.log2_pt) - 1;
   if (looks) {
@@ -165,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
         if (j < need) {
           const int32_t p = a.free_pages[head + i];
           a.table[(uint64_t)r * a.max_blocks + have + j] = p;
-          if (kOne && (p < 0 || p >= page_limit)) report(a.st, SHN_ERR_INVALID_ARG, r);
+          if (kOne && (p < 0 || p >= page_limit)) atomicMin(&bad_detail, r);
           break;
         }
         j -= need;
@@ -188,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
           const long long b = pos >> a.log2_pt;
           const int32_t p = b < have ? a.table[(uint64_t)r * a.max_blocks + b] : a.free_pages[head + pages + b - have];
           if (p >= 0 && p < page_limit) slot = (int32_t)(((uint32_t)p << a.log2_pt) + (pos & pt_mask));
-          else if (kOne) report(a.st, SHN_ERR_INVALID_ARG, r);
+          else if (kOne) atomicMin(&bad_detail, r);
           break;
         }
         j -= f;
@@ -197,6 +194,13 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(KvPlanArgs a) {
     }
     a.positions[i] = pos;
     a.slots[i] = slot;
+  }
+  if constexpr (kOne) {
+    __syncthreads();
+    if (t) return;
+    const bool page = ok && bad_detail != 0xFFFFFFFFu;  // (the first request with one that is bad)
+    a.st->status = page ? SHN_ERR_INVALID_ARG : code;
+    a.st->detail = page ? bad_detail : detail;
   }
 }
 

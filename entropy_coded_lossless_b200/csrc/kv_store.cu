@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kStoreThreads, kStoreBlocks) kv_store_kernel(K
       if (a.rot) pos = a.positions[token + blocks];
     }
     if ((slot_now >= 0 && ((uint32_t)slot_now >> c.log2_pt) >= c.n_pages) || (a.rot && (uint32_t)pos_now >= a.n_positions)) {
-      if (!kOne && threadIdx.x == 0 && blockIdx.y == 0) report(a.st, SHN_ERR_INVALID_ARG, token);
+      if (!kOne && threadIdx.x == 0 && blockIdx.y == 0) report_first(a.st, SHN_ERR_INVALID_ARG, token);
       continue;
     }
     Turn turn = {};
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kLoadThreads) kv_load_kernel(KvPages c, KvLoad
   if constexpr (!kOne) after_previous();
   if (slot < 0) return;
   if (((uint32_t)slot >> c.log2_pt) >= c.n_pages) {
-    if (!kOne && lane == 0) report(a.st, SHN_ERR_INVALID_ARG, token);
+    if (!kOne && lane == 0) report_first(a.st, SHN_ERR_INVALID_ARG, token);
     return;
   }
   const uint64_t at = kv_row_of_slot(c, (uint32_t)slot, h);

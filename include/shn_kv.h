@@ -12,8 +12,9 @@
  * current for the calling thread; errors the host can see are returned and nothing is enqueued; errors
  * only the device can see (a page id outside the cache, more tokens than a buffer holds) go to the
  * status word at the start of the caller's workspace (d_work), which every call sets (0: no error, and what
- * stood in the workspace before does not matter). A workspace serves one call at a time: calls whose GPU work
- * may overlap (other streams, replays of other graphs) need one each. Everything can be captured into a CUDA
+ * stood in the workspace before does not matter); of several requests or tokens that are wrong it names the
+ * first. A workspace serves one call at a time: calls whose GPU work may overlap (other streams, replays of
+ * other graphs) need one each. Everything can be captured into a CUDA
  * graph: lengths, tables and counts are read on the device, the host arguments are sizes of buffers.
  * Results do not depend on timing: the same inputs give the same bits.
  *
