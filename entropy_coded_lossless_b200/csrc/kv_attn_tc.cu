@@ -72,10 +72,36 @@ struct Work {
   uint32_t t0;               // first token (in pages) of the block's part of the sequence
 };
 
+// In front of the others, which start beside it: what is wrong with the requests' ranges and lengths into the status. (Asked by every
+// block of the kernel that follows, it cost a call of three short prompts 2 us of 16 and one of 8192 tokens 20 us of 690.)
+__global__ void kv_prompt_begin_kernel(KvPages c, KvAttnArgs a) {
+  let_next();
+  __shared__ uint32_t least[32];
+  const uint32_t t = threadIdx.x;
+  const int64_t holds = (int64_t)a.max_blocks << c.log2_pt;
+  uint32_t first = kNoError;
+  for (uint32_t r = t; r < a.n_reqs; r += blockDim.x) {
+    const int32_t b = a.cu_q[r], e = a.cu_q[r + 1], len = a.kv_len[r];
+    if (b < 0 || e < b || (uint32_t)e > a.n_tokens || (e > b && (len < 0 || len > holds))) first = min(first, r);
+  }
+  first = __reduce_min_sync(~0u, first);
+  if ((t & 31) == 0) least[t >> 5] = first;
+  __syncthreads();
+  if (t) return;
+  for (uint32_t i = 1; i < blockDim.x / 32; ++i) first = min(first, least[i]);
+  a.st->status = first == kNoError ? SHN_OK : SHN_ERR_INVALID_ARG;
+  a.st->detail = first == kNoError ? 0 : first;
+}
+
 // Which request's rows a block takes: tiles of 256 rows, request after request, the last tile first (a
 // prompt's last rows see the most tokens, and long blocks belong in front). False: no such tile.
 __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a, uint32_t group, uint32_t tile_from_end,
-                                          uint32_t* scan, Work& w) {
+                                          uint32_t* scan, Work& w, uint32_t& status) {
+  // The status as the kernel in front left it, asked for behind the first loads: both are on their way together.
+  auto look = [&] {
+    after_previous();
+    status = *reinterpret_cast<volatile uint32_t*>(&a.st->status);
+  };
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
   int32_t len;
   if (a.n_reqs <= 32) {
@@ -83,8 +109,8 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
     const bool is = lane < a.n_reqs;
     const int32_t b = is ? a.cu_q[lane] : 0, e = is ? a.cu_q[lane + 1] : 0;
     len = is ? a.kv_len[lane] : 0;
+    look();
     const bool bad = b < 0 || e < b || (uint32_t)e > a.n_tokens;
-    if (bad && warp == 0) report_first(a.st, SHN_ERR_INVALID_ARG, lane);
     const uint32_t own = bad ? 0 : ((uint32_t)(e - b) * group + kRows - 1) / kRows;
     uint32_t inc = own;
 #pragma unroll
@@ -109,9 +135,9 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
     for (uint32_t r = r0; r < r1; ++r) {
       const int32_t b = a.cu_q[r], e = a.cu_q[r + 1];
       kv_len = a.kv_len[r];
-      if (b < 0 || e < b || (uint32_t)e > a.n_tokens) report_first(a.st, SHN_ERR_INVALID_ARG, r);
-      else own += ((uint32_t)(e - b) * group + kRows - 1) / kRows;
+      if (b >= 0 && e >= b && (uint32_t)e <= a.n_tokens) own += ((uint32_t)(e - b) * group + kRows - 1) / kRows;
     }
+    look();
     uint32_t inc = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -158,11 +184,7 @@ __device__ __forceinline__ bool find_work(const KvPages& c, const KvAttnArgs& a,
     len = (int32_t)scan[32];
   }
   const int64_t holds = (int64_t)a.max_blocks << c.log2_pt;
-  if (len < 0 || len > holds) {
-    if (t == 0) report_first(a.st, SHN_ERR_INVALID_ARG, w.req);
-    len = len < 0 ? 0 : (int32_t)holds;
-  }
-  w.len = len;
+  w.len = len < 0 ? 0 : len > holds ? (int32_t)holds : len;
   w.t0 = 0;
   return true;
 }
@@ -258,12 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   const uint32_t place = kSplit ? blockIdx.x / pl.splits : blockIdx.x, rank = kSplit ? blockIdx.x % pl.splits : 0;
   const uint32_t group = a.q_heads / c.kv_heads, hk = place % c.kv_heads;
 
-  if constexpr (kPart) let_next();  // the call's first kernel
-  else after_previous();            // the last
-  const uint32_t status = kPart ? 0 : *reinterpret_cast<volatile uint32_t*>(&a.st->status);
   Work w;
-  if constexpr (kPart) find_part(c, a, pl, group, w);
-  else if (!find_work(c, a, group, place / c.kv_heads, reinterpret_cast<uint32_t*>(smem + L::scan), w)) return;
+  uint32_t status = 0;
+  if constexpr (kPart) {
+    let_next();  // the call's first kernel
+    find_part(c, a, pl, group, w);
+  } else {  // the last: only the status is the other one's
+    if (!find_work(c, a, group, place / c.kv_heads, reinterpret_cast<uint32_t*>(smem + L::scan), w, status)) return;
+  }
   const uint32_t rows_here = min(kRows, w.rows - w.row0);
   // tokens the block's last row sees; every row of the block sees at most as many
   // row i of the block is query base_q + x and head y of the group, x = (rest + i) / group: with i + rest < 320 and group <= 64 that
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     for (uint32_t i = 0; i < 4; ++i) bar_init(bars + kScaleFull + 8 * i, kConvertWarps);
     sts32(stop, 0);
     sts32(base + L::misc + 8, 0);
-    if (kPart) sts32(base + L::misc + 16, kNoError);
+    sts32(base + L::misc + 16, kNoError);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssueWarp) {
@@ -690,8 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if (j < tiles && tok < most) {
         p = table[(tok + skip) >> c.log2_pt];
         if (p < 0 || (uint32_t)p >= c.n_pages) {
-          if (kPart) sts32(base + L::misc + 16, 0);
-          else if (lane < 8) report_first(a.st, SHN_ERR_INVALID_ARG, w.req);
+          sts32(base + L::misc + 16, 0);
           p = -1;
         }
       }
@@ -860,7 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   if constexpr (kPart) {
     if (tid == 0) pl.errors[blockIdx.x] = lds32(stop) != 0 ? kGaveUp : lds32(base + L::misc + 16);
   } else {
-    if (tid == 0 && lds32(stop) != 0) report_first(a.st, SHN_ERR_TIMEOUT, w.req);
+    const bool gave_up = lds32(stop) != 0;
+    if (tid == 0 && (gave_up || lds32(base + L::misc + 16) != kNoError)) report_first(a.st, gave_up ? SHN_ERR_TIMEOUT : SHN_ERR_INVALID_ARG, w.req);
   }
 }
 
@@ -890,6 +914,9 @@ cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnAr
   // 2) 34.4 / 74.6, 40 after 5102 (32 on 8, of 64) 26.6 / 102.1. With 4 blocks to a row at most they take 42.4, 34.2 and
   // 37.8, with up to twice the blocks that have places 29.7, 49.1 and 27.0.
   const uint64_t tokens = (uint64_t)a.max_blocks << c.log2_pt;  // what a request can have
+  kv_prompt_begin_kernel<<<1, a.n_reqs < 1024 ? (a.n_reqs + 31) / 32 * 32 : 1024, 0, s>>>(c, a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   while (pl.splits < 8 && blocks * pl.splits * 2 <= (uint64_t)sm_count && tokens > 2 * pl.splits * kTile) pl.splits *= 2;
   if (blocks <= (uint64_t)sm_count) return head_dim == 128 ? launch<128, false, true>(blocks, c, a, pl, s) : launch<64, false, true>(blocks, c, a, pl, s);
   return head_dim == 128 ? launch<128, false, false>(blocks, c, a, pl, s) : launch<64, false, false>(blocks, c, a, pl, s);

@@ -215,9 +215,8 @@ int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens
   a.q = d_q, a.q_stride = q_stride, a.n_tokens = n_tokens, a.q_heads = q_heads;
   a.table = d_block_table, a.max_blocks = max_blocks, a.cu_q = d_cu_q, a.kv_len = d_kv_len, a.n_reqs = n_reqs;
   a.scale = softmax_scale, a.out = d_out, a.out_stride = out_stride;
-  a.st = clear_status(d_work, s);
-  if (!a.st) return SHN_ERR_CUDA;
-  if (n_tokens == 0 || n_reqs == 0) return SHN_OK;
+  a.st = static_cast<DeviceStatus*>(d_work);  // set by the first launch
+  if (n_tokens == 0 || n_reqs == 0) return clear_status(d_work, s) ? SHN_OK : SHN_ERR_CUDA;
   return launch_kv_prompt(pages_of(cache), cache->head_dim, a, sm_count_for_launch(), s) == cudaSuccess ? SHN_OK : SHN_ERR_CUDA;
 }
 
