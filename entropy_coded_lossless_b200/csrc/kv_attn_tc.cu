@@ -10,9 +10,14 @@
 // keys as the integers, and their scales are applied to the float32 scores: scores have float32's error. Values enter as
 // fp16(int8 * fp16(v_scale * 2^-e)), e the exponent of the largest value scale of 32 tokens; weights, values and their
 // scales are rounded to fp16's 11 bits each (with bf16's 8 the results, rounded to bf16 themselves, were off by 0.0024 instead
-// of 0.0017 in the mean). The power of two goes into the weights: P = p 2^(e - E), with E the exponent O is held in, raised
-// like the softmax's reference when values are more than 2^7 larger. A weight smaller than 2^-24 of that range is
-// lost, so O is exact to 2^-24 of the largest value of the sequence.
+// of 0.0017 in the mean). The power of two goes into the weights: P = p 2^(e - E), with E the exponent a row's O is held in: 6 below
+// that of the largest value scale it has seen, and raised like the softmax's reference when one is more than 2^6 larger. What
+// fp16 cannot hold of a weight is 2^-25 of that range, so O is exact to n 2^-30 + 2^-24 of the largest value of the n tokens that
+// the row sees.
+// Tokens that a row does not see are nothing to it, whatever their size. So a tile that some row of the block does not see whole
+// has the integers as values and the scales on the float32 weights, P = fp16(p * v_scale 2^-E), and each row's E is of what it sees.
+// (All tiles that way would round once for three times: the mean error stays 0.0017, 8192 tokens take 761 us a call instead
+// of 696.)
 //
 // Softmax in one pass over the scores, without a search for the maximum: m is the maximum of a row's first 64 scores, and a
 // thread's sum of 16 weights shows whether one of the later ones is above it by 2^8; only then m is raised, and what is
@@ -53,14 +58,15 @@ constexpr uint32_t kThreads = 32 * (kIssueWarp + 4);
 constexpr uint32_t kTile = 128;      // tokens of a tile
 constexpr uint32_t kRows = 256;      // query rows of a block
 constexpr float kRise = 256.f;       // how far a weight may pass 1 before the reference is raised,
-constexpr float kValueRise = 7.f;    // and (log2) the values the range O is held in: 2^15 together, within fp16
+constexpr float kValueRise = 6.f;    // and (log2) the exponent of a value scale E: with the scale's own factor 2^15, within fp16
 constexpr float kValueFall = -60.f, kValueFall2 = 1ull << 60;  // a tile this far below adds nothing to O in fp16
+constexpr float kValueClimb = 110.f, kValueClimb2 = 0x1p-110f;  // 32 tokens may be above E as a whole: those that the row does not see
 constexpr uint32_t kHalf = 128 * 128;  // bytes of 128 rows of 64 fp16
 
 template <int D>
 struct Layout {
   static constexpr uint32_t kOperand = 128 * D * 2;  // one 128 x D fp16 operand
-  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, info = scale + 4 * 512, row_sum = info + 128, bars = row_sum + 8 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
+  static constexpr uint32_t q = 0, k = 2 * kOperand, v = 4 * kOperand, scale = 6 * kOperand, info = scale + 4 * 1024, row_sum = info + 128, bars = row_sum + 12 * kRows, misc = bars + 256, scan = misc + 64, total = scan + 192;
 };
 // barriers
 enum : uint32_t { kQFull = 0, kKFull = 8, kKEmpty = 24, kVFull = 40, kVEmpty = 56, kScaleFull = 72, kSFull = 104, kPFull = 136, kOFull = 168, kDrain = 200 };
@@ -209,7 +215,7 @@ __device__ __forceinline__ void find_part(const KvPages& c, const KvAttnArgs& a,
 __device__ __forceinline__ uint32_t parts_of(uint32_t tiles, uint32_t most) { return tiles > 3 ? min(most, tiles) : 1; }
 __device__ __forceinline__ uint32_t first_tile(uint32_t tiles, uint32_t parts, uint32_t rank) { return min(rank, parts) * tiles / parts; }
 
-// The parts' sums, sums of weights l, references m and exponents E lie in their blocks' shared memory. Each block of the cluster
+// The parts' sums, sums of weights l, references m and exponents E of their rows lie in their blocks' shared memory. Each block of the cluster
 // joins 256 / ranks rows, a warp 16 / ranks of them, half of these at a time: 8 loads of 32 lanes (a row of a block each) are on
 // their way together.
 //   out = sum O_i 2^(m_i - m + E_i - E) 2^E / sum l_i 2^(m_i - m)
@@ -227,7 +233,7 @@ __device__ __forceinline__ void join_parts(uint32_t base, uint32_t ranks, uint32
     if (has) {
       l = __uint_as_float(ld_cluster32(base + L::row_sum + 4 * row, from));
       m = __uint_as_float(ld_cluster32(base + L::row_sum + 4 * (kRows + row), from));
-      size = __uint_as_float(ld_cluster32(base + L::misc + 12, from));
+      size = m == -INFINITY ? m : __uint_as_float(ld_cluster32(base + L::row_sum + 4 * (2 * kRows + row), from));  // (no sums: no range)
     }
     uint4 v[8];
 #pragma unroll
@@ -332,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     for (uint32_t i = 0; i < 4; ++i) bar_init(bars + kScaleFull + 8 * i, kConvertWarps);
     sts32(stop, 0);
     sts32(base + L::misc + 8, 0);
+    sts32(base + L::misc + 12, 0x7FFFFFFFu);
     sts32(base + L::misc + 16, kNoError);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -356,6 +363,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
   if (warp < kSoftWarps) {
     // ---- softmax -------------------------------------------------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    // A warp has 16 rows (TMEM lanes); a thread has two of them, `quad` and quad + 8, and of each 8 columns two: a column's
+    // scales, read from shared memory, serve two rows, and a row's maximum is two shuffles away.
+    const uint32_t half = warp >> 3;  // which 128 rows
+    const uint32_t lanes = (warp & 3) * 32 + (warp & 4) * 4, quad = lane >> 2, col = 2 * (lane & 3);
+    const uint32_t at = tmem + (lanes << 16);
+    const uint32_t s_at = at + half * 128, o_at = at + 256 + half * D;
+    auto seen_by = [&](uint32_t row) -> int32_t {
+      if (row >= rows_here) return 0;
+      uint32_t head;
+      const uint32_t q = query_of(row, head);
+      if constexpr (kPart) {
+        bool bad;
+        return max(0, min(w.len, decode_len(c, a, (int32_t)w.t0 + w.len, q, bad) - (int32_t)w.t0));
+      }
+      if constexpr (kSplit) return max(0, min(most, min(w.len, shift + (int32_t)q) - (int32_t)w.t0));
+      return max(0, min(w.len, shift + (int32_t)q));
+    };
     // the queries of the block as an operand, zeros behind the last row
     const uint16_t* q_src = a.q + (uint64_t)w.q0 * a.q_stride + (uint64_t)hk * group * D;
     uint4 qx[kRows * D / 8 / kSoftThreads];  // all loads first: one wait for them
@@ -367,6 +391,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       qx[i] = make_uint4(0, 0, 0, 0);
       if (row < rows_here) qx[i] = *reinterpret_cast<const uint4*>(q_src + (uint64_t)query * a.q_stride + head * D + piece * 8);
     }
+    int32_t seen[2];  // (rows behind the last one: all tokens)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t row = half * 128 + lanes + quad + 8 * r;
+      seen[r] = row < rows_here ? seen_by(row) : 0x7FFFFFFF;
+    }
+    const int32_t least_seen = __reduce_min_sync(~0u, min(seen[0], seen[1]));
+    if (lane == 0) atomicMin(reinterpret_cast<int32_t*>(smem + L::misc + 12), least_seen);
     // One power of two brings the block's largest query value just below 2^15; fp16 then holds every bf16 down to 2^-32
     // of it exactly. (Values that are not finite set no size and stay what they are.)
     uint32_t top2 = 0;
@@ -405,31 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     fence_smem();
     bar_arrive(bars + kQFull);
 
-    // A warp has 16 rows (TMEM lanes); a thread has two of them, `quad` and quad + 8, and of each 8 columns two: a column's
-    // scales, read from shared memory, serve two rows, and a row's maximum is two shuffles away.
-    const uint32_t half = warp >> 3;  // which 128 rows
-    const uint32_t lanes = (warp & 3) * 32 + (warp & 4) * 4, quad = lane >> 2, col = 2 * (lane & 3);
-    const uint32_t at = tmem + (lanes << 16);
-    const uint32_t s_at = at + half * 128, o_at = at + 256 + half * D;
-    auto seen_by = [&](uint32_t row) -> int32_t {
-      if (row >= rows_here) return 0;
-      uint32_t head;
-      const uint32_t q = query_of(row, head);
-      if constexpr (kPart) {
-        bool bad;
-        return max(0, min(w.len, decode_len(c, a, (int32_t)w.t0 + w.len, q, bad) - (int32_t)w.t0));
-      }
-      if constexpr (kSplit) return max(0, min(most, min(w.len, shift + (int32_t)q) - (int32_t)w.t0));
-      return max(0, min(w.len, shift + (int32_t)q));
-    };
-    int32_t seen[2];
+    // Tiles that all rows of the block see whole come first: all rows hold their sums in the same range, and no column's place is
+    // looked at. In the others a row has its own.
+    const uint32_t whole = min(tiles, lds32(base + L::misc + 12) / kTile);
     float m[2], l[2];
     float neg[2];    // minus the reference (0 while there is none)
     float limit[2];  // how large a sum of weights may be before it is raised
-    float held = 0.f, held2 = 1.f;  // E and 2^E: O is in units of it
+    float held[2] = {-300.f, -300.f}, held2[2] = {1.f, 1.f};  // E and 2^E: a row's O is in units of it (none yet)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      seen[r] = seen_by(half * 128 + lanes + quad + 8 * r);
       m[r] = -INFINITY, l[r] = 0.f, neg[r] = 0.f, limit[r] = seen[r] ? -1.f : INFINITY;  // (no reference yet: any sum passes)
     }
     // A warp whose rows are all behind the last one keeps step and does no more: its places in TMEM hold anything, and so do
@@ -437,162 +453,225 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     // full grids, whose blocks have few such rows: there the question alone costs 7 % (8192 tokens 627 -> 673 us).
     if (kSplit && half * 128 + lanes >= rows_here) seen[0] = -1;
     bool ok = true;
-    for (uint32_t j = 0; j < tiles && ok; ++j) {
-      ok = __all_sync(~0u, bar_wait(bars + kScaleFull + 8 * (j & 3), (j >> 2) & 1, stop));
-      if (!ok) break;
-      // the size (log2) of the value scales, 32 tokens a time
-      const uint32_t info = after_here(base + L::info + (j & 3) * 32);
-      const uint4 sizes = lds128(info);
-      const float size[4] = {__uint_as_float(sizes.x), __uint_as_float(sizes.y), __uint_as_float(sizes.z), __uint_as_float(sizes.w)};
-      const float largest = fmaxf(fmaxf(size[0], size[1]), fmaxf(size[2], size[3]));
-      const bool larger = j > 0 && largest > held + kValueRise;
-      float lower = 1.f;  // what O is scaled by then
-      if (j == 0 || larger) {
-        lower = pow2(fmaxf(held - largest, -126.f));
-        held = largest;
-        held2 = pow2(held);
-      }
-      // Half a tile (64 tokens) at a time. The first half's scores lie in the 64 columns `here`, the second's in the other 64; both
-      // halves' weights go into `here` (32 columns each). So the columns of the second half are free as soon as its scores
-      // are in registers, and the next tile's first half is put there while this one is still worked on: next to no scores are
-      // ever waited for.
+    // Half a tile (64 tokens) at a time. The first half's scores lie in the 64 columns `here`, the second's in the other 64; both
+    // halves' weights go into `here` (32 columns each). So the columns of the second half are free as soon as its scores
+    // are in registers, and the next tile's first half is put there while this one is still worked on: next to no scores are
+    // ever waited for. `grows`: some row's range may have to be raised (the same in all threads of the warp).
+    auto half_tile = [&](auto edge_tag, uint32_t j, int h, uint32_t info, bool grows) {
+      constexpr bool kEdge = decltype(edge_tag)::value;
       const uint32_t here = s_at + (j & 1) * 64;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ok = __all_sync(~0u, bar_wait(bars + kSFull + 16 * half + 8 * h, j & 1, stop));
-        if (!ok) break;
-        if (kSplit && seen[0] < 0) {  // (see above)
-          if (lane == 0 && h == 1) bar_arrive(bars + kPFull + 16 * half);
-          continue;
-        }
-        fence_after();
-        // s[4n + 2r + e]: row quad + 8r, column 64h + 8n + col + e
-        uint32_t s[32];
-        ld_quad32(s_at + ((j + h) & 1) * 64, s);
-        wait_ld();
-        if (h == 1) {
-          // the first half's weights are stored and the second's scores loaded
-          wait_st();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(bars + kPFull + 16 * half);
-        }
-        const uint32_t scales = after_here(base + L::scale + (j & 3) * 512 + h * 256 + 4 * col);
-        const int32_t first = (int32_t)(j * kTile + 64 * h + col);
-        const bool edge = __any_sync(~0u, first - (int32_t)col + 64 > min(seen[0], seen[1]));
-        float sum[2];
-        // Weights against the reference that stands; no maximum is searched first. A thread's sum of a row's 16 weights shows
-        // whether one of them has passed the limit, which almost never happens: this one pass is all then. (Two versions:
-        // only tiles at the end of what a row sees look at the columns' places.)
-        auto weights = [&](auto edge_tag) {
-          constexpr bool kEdge = decltype(edge_tag)::value;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) sum[r] = 0.f;
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {  // 32 columns: 16 of packed pairs
-            const float by = fmaxf(lds32_free(info + 8 * h + 4 * b) - held, kValueFall);  // their weights' power of two
-            const float unby = fminf(held2 * lds32_free(info + 16 + 8 * h + 4 * b), kValueFall2);
-            uint64_t part[2] = {0, 0}, ref[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) ref[r] = pack2(neg[r] + by, neg[r] + by);
-            uint32_t p[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int n = 4 * b + i;
-              const uint64_t ks = lds64_free(scales + 32 * n);
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const uint32_t* v = &s[4 * n + 2 * r];
-                float x, y;
-                unpack2(fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), ks, ref[r]), x, y);
-                if constexpr (kEdge) {
-                  x = first + 8 * n < seen[r] ? x : -INFINITY;
-                  y = first + 8 * n + 1 < seen[r] ? y : -INFINITY;
-                }
-                x = exp2_approx(x), y = exp2_approx(y);
-                part[r] = add2(part[r], pack2(x, y));
-                p[2 * i + r] = fp16_pack(x, y);
-              }
-            }
-            st_pairs8(here + 32 * h + 16 * b, p);
+      ok = __all_sync(~0u, bar_wait(bars + kSFull + 16 * half + 8 * h, j & 1, stop));
+      if (!ok) return;
+      if (kSplit && seen[0] < 0) {  // (see above)
+        if (lane == 0 && h == 1) bar_arrive(bars + kPFull + 16 * half);
+        return;
+      }
+      fence_after();
+      // s[4n + 2r + e]: row quad + 8r, column 64h + 8n + col + e
+      uint32_t s[32];
+      ld_quad32(s_at + ((j + h) & 1) * 64, s);
+      wait_ld();
+      if (h == 1) {
+        // the first half's weights are stored and the second's scores loaded
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bars + kPFull + 16 * half);
+      }
+      const uint32_t scales = after_here(base + L::scale + (j & 3) * 1024 + h * 256 + 4 * col);
+      const int32_t first = (int32_t)(j * kTile + 64 * h + col);
+      bool rise = j == 0 && h == 0;  // (there is no reference yet)
+      float lower[2] = {1.f, 1.f};   // what O is scaled by
+      if (grows) {
+        float top[2];  // (log2) the largest value scale of the tile, or of what the row sees of the half
+        if constexpr (!kEdge) {
+          const uint4 sizes = lds128(info);
+          top[0] = top[1] = fmaxf(fmaxf(__uint_as_float(sizes.x), __uint_as_float(sizes.y)), fmaxf(__uint_as_float(sizes.z), __uint_as_float(sizes.w)));
+        } else {
+          float most_v[2] = {0.f, 0.f};
+#pragma unroll 2
+          for (int n = 0; n < 8; ++n) {
+            float x, y;
+            unpack2(lds64_free(scales + 512 + 32 * n), x, y);
+            const float unit = pow2(lds32_free(info + 8 * h + 4 * (n >> 2)));
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              float x, y;
-              unpack2(part[r], x, y);
-              sum[r] = fmaf(x + y, unby, sum[r]);
+              if (first + 8 * n < seen[r]) most_v[r] = fmaxf(most_v[r], fabsf(x) * unit);
+              if (first + 8 * n + 1 < seen[r]) most_v[r] = fmaxf(most_v[r], fabsf(y) * unit);
             }
           }
-        };
-        bool rise = j == 0 && h == 0;  // there is no reference yet
-        if (!rise) {
-          if (edge) weights(std::true_type{});
-          else weights(std::false_type{});
-          rise = __any_sync(~0u, sum[0] > limit[0] || sum[1] > limit[1]) || (larger && h == 0);
-        }
-        if (rise) {
-          // the reference rises to the row's maximum of this half: what is summed is scaled down, and the weights formed again
-          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
+          for (int r = 0; r < 2; ++r) {
+            most_v[r] = fmaxf(most_v[r], __shfl_xor_sync(~0u, most_v[r], 1));
+            most_v[r] = fmaxf(most_v[r], __shfl_xor_sync(~0u, most_v[r], 2));
+            top[r] = (float)((int32_t)(__float_as_uint(most_v[r]) >> 23) - 127);
+          }
+        }
+        bool raised = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (!(top[r] > held[r] + kValueRise)) continue;
+          const float to = fmaxf(top[r] - kValueRise, -126.f);
+          lower[r] = pow2(fmaxf(held[r] - to, -126.f));
+          held[r] = to;
+          held2[r] = pow2(to);
+          raised = true;
+        }
+        rise |= __any_sync(~0u, raised);
+      }
+      float sum[2];
+      // Weights against the reference that stands; no maximum is searched first. A thread's sum of a row's 16 weights shows
+      // whether one of them has passed the limit, which almost never happens: this one pass is all then.
+      auto weights = [&](auto mask_tag) {
+        constexpr bool kMask = decltype(mask_tag)::value;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) sum[r] = 0.f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {  // 32 columns: 16 of packed pairs
+          // their weights' power of two, and its inverse
+          const float size = lds32_free(info + 8 * h + 4 * b), inverse = lds32_free(info + 16 + 8 * h + 4 * b);
+          float by[2], unby[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int of = kMask ? r : 0;
+            by[r] = fmaxf(size - held[of], kValueFall);
+            unby[r] = fminf(held2[of] * inverse, kValueFall2);
+            if constexpr (kMask) by[r] = fminf(by[r], kValueClimb), unby[r] = fmaxf(unby[r], kValueClimb2);
+          }
+          uint64_t part[2] = {0, 0}, ref[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) ref[r] = pack2(neg[r] + by[r], neg[r] + by[r]);
+          uint32_t p[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = 4 * b + i;
             const uint64_t ks = lds64_free(scales + 32 * n);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
+              const uint32_t* v = &s[4 * n + 2 * r];
               float x, y;
-              unpack2(mul2(pack2(__uint_as_float(s[4 * n + 2 * r]), __uint_as_float(s[4 * n + 2 * r + 1])), ks), x, y);
-              if (first + 8 * n < seen[r]) top[r] = fmaxf(top[r], x);
-              if (first + 8 * n + 1 < seen[r]) top[r] = fmaxf(top[r], y);
+              unpack2(fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), ks, ref[r]), x, y);
+              if constexpr (kMask) {
+                x = first + 8 * n < seen[r] ? x : -INFINITY;
+                y = first + 8 * n + 1 < seen[r] ? y : -INFINITY;
+              }
+              x = exp2_approx(x), y = exp2_approx(y);
+              part[r] = add2(part[r], pack2(x, y));
+              if constexpr (kEdge) unpack2(mul2(pack2(x, y), lds64_free(scales + 512 + 32 * n)), x, y);  // (values without their scales)
+              p[2 * i + r] = fp16_pack(x, y);
             }
           }
-          float keep[2];
+          st_pairs8(here + 32 * h + 16 * b, p);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
-            keep[r] = 1.f;
-            if (top[r] > m[r]) {
-              keep[r] = exp2_approx(m[r] - top[r]);
-              m[r] = top[r];
-              neg[r] = -top[r];
-              limit[r] = kRise;
-            }
-            l[r] *= keep[r];
-            if (h == 0) keep[r] *= lower;
+            float x, y;
+            unpack2(part[r], x, y);
+            sum[r] = fmaf(x + y, unby[r], sum[r]);
           }
-          if (j > 0 || h > 0) {
-            ok = __all_sync(~0u, bar_wait(bars + kOFull + 16 * half + 8 * (h ^ 1), (j + h + 1) & 1, stop));  // the part before this one
-            if (!ok) break;
-            fence_after();
-#pragma unroll 1
-            for (uint32_t o_q = o_at; o_q < o_at + D; o_q += 16) {  // few registers a time
-              uint32_t o[8];
-              ld_quad8(o_q, o);
-              wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep[(e >> 1) & 1]);
-              st_quad8(o_q, o);
-            }
-          }
-          if (edge) weights(std::true_type{});
-          else weights(std::false_type{});
         }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) l[r] += sum[r];
+      };
+      bool masked = false;  // some row of the warp does not see the half whole
+      if constexpr (kEdge) masked = __any_sync(~0u, first - (int32_t)col + 64 > min(seen[0], seen[1]));
+      auto form_weights = [&] {
+        if constexpr (kEdge) {
+          if (masked) return weights(std::true_type{});
+        }
+        weights(std::false_type{});
+      };
+      if (!rise) {
+        form_weights();
+        rise = __any_sync(~0u, sum[0] > limit[0] || sum[1] > limit[1]);
       }
-      if (!ok) break;
+      if (rise) {
+        // the reference rises to the row's maximum of this half: what is summed is scaled down, and the weights formed again
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const uint64_t ks = lds64_free(scales + 32 * n);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float x, y;
+            unpack2(mul2(pack2(__uint_as_float(s[4 * n + 2 * r]), __uint_as_float(s[4 * n + 2 * r + 1])), ks), x, y);
+            if (!kEdge || first + 8 * n < seen[r]) top[r] = fmaxf(top[r], x);
+            if (!kEdge || first + 8 * n + 1 < seen[r]) top[r] = fmaxf(top[r], y);
+          }
+        }
+        float keep[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+          top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+          keep[r] = 1.f;
+          if (top[r] > m[r]) {
+            keep[r] = exp2_approx(m[r] - top[r]);
+            m[r] = top[r];
+            neg[r] = -top[r];
+            limit[r] = kRise;
+          }
+          l[r] *= keep[r];
+          keep[r] *= lower[r];
+        }
+        if (j > 0 || h > 0) {
+          ok = __all_sync(~0u, bar_wait(bars + kOFull + 16 * half + 8 * (h ^ 1), (j + h + 1) & 1, stop));  // the part before this one
+          if (!ok) return;
+          fence_after();
+#pragma unroll 1
+          for (uint32_t o_q = o_at; o_q < o_at + D; o_q += 16) {  // few registers a time
+            uint32_t o[8];
+            ld_quad8(o_q, o);
+            wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep[(e >> 1) & 1]);
+            st_quad8(o_q, o);
+          }
+        }
+        form_weights();
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) l[r] += sum[r];
+    };
+    auto end_tile = [&] {
       wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(bars + kPFull + 16 * half + 8);
+    };
+    // The sizes (log2) of a tile's value scales, 32 tokens a time, as an address; and the largest.
+    auto begin_tile = [&](uint32_t j, uint32_t& info) -> float {
+      ok = __all_sync(~0u, bar_wait(bars + kScaleFull + 8 * (j & 3), (j >> 2) & 1, stop));
+      info = after_here(base + L::info + (j & 3) * 32);
+      const uint4 sizes = lds128(info);
+      return fmaxf(fmaxf(__uint_as_float(sizes.x), __uint_as_float(sizes.y)), fmaxf(__uint_as_float(sizes.z), __uint_as_float(sizes.w)));
+    };
+    uint32_t j = 0;
+    for (; j < whole && ok; ++j) {
+      uint32_t info;
+      const bool grows = begin_tile(j, info) > held[0] + kValueRise;
+      if (!ok) break;
+      half_tile(std::false_type{}, j, 0, info, grows);
+      if (ok) half_tile(std::false_type{}, j, 1, info, false);
+      if (ok) end_tile();
+    }
+#pragma unroll 1
+    for (; j < tiles && ok; ++j) {
+      uint32_t info;
+      const float largest = begin_tile(j, info);
+      const bool grows = __any_sync(~0u, largest > fminf(held[0], held[1]) + kValueRise);
+      if (!ok) break;
+      half_tile(std::true_type{}, j, 0, info, grows);
+      if (ok) half_tile(std::true_type{}, j, 1, info, grows);
+      if (ok) end_tile();
     }
     // the rows' sums, through shared memory to the threads that write the rows: warps of the same 32 rows take half of the
     // columns each (the barrier comes first: no warp may miss it)
     const uint32_t rows32 = (warp & 3) * 32;
-    const uint32_t sums = base + L::row_sum + 4 * (half * 128), refs = sums + 4 * kRows;
+    const uint32_t sums = base + L::row_sum + 4 * (half * 128), refs = sums + 4 * kRows, ranges = refs + 4 * kRows;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
       if ((lane & 3) == 0) sts32(sums + 4 * (lanes + quad + 8 * r), __float_as_uint(l[r]));
+      if ((lane & 3) == 0) sts32(ranges + 4 * (lanes + quad + 8 * r), __float_as_uint(held[r]));
       if ((kPart || kSplit) && (lane & 3) == 0) sts32(refs + 4 * (lanes + quad + 8 * r), __float_as_uint(m[r]));
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(kSoftThreads / 2) : "memory");
@@ -602,7 +681,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       asm volatile("bar.sync 3, %0;" ::"n"(kSoftThreads) : "memory");  // all products are done with shared memory
       // O where the queries and keys were, a row's 16-byte chunks exchanged so that 8 lanes' rows meet no bank twice
       const uint32_t row = half * 128 + rows32 + lane, first = (warp >> 2 & 1) * (D / 2);
-      if (tid == 0) sts32(base + L::misc + 12, __float_as_uint(held));
 #pragma unroll 1
       for (uint32_t q = 0; ok && tiles && q < D / 2; q += 32) {
         uint32_t o[32];
@@ -635,7 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       const bool any = seen_by(row) > 0;
       // no token seen: zeros. (A sum that is not positive although tokens were seen is a NaN's or an infinity's.)
       const float sum = __uint_as_float(lds32(sums + 4 * (rows32 + lane)));
-      const float inv = any ? held2 / sum : 0.f;
+      const float range = __uint_as_float(lds32(ranges + 4 * (rows32 + lane)));
+      const float inv = any ? pow2(range) / sum : 0.f;
       const uint32_t first = (warp >> 2 & 1) * (D / 2), mine = base + L::q + half * L::kOperand + (warp & 7) * (L::kOperand / 8);
       const uint64_t part0 = kPart ? (uint64_t)(blockIdx.x / c.kv_heads % pl.splits) * a.n_reqs : 0;
       if constexpr (kPart) {
@@ -643,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         const uint32_t query = query_of(row, head);
         if (row < rows_here && first == 0) {
           const float ref = __uint_as_float(lds32(refs + 4 * (rows32 + lane)));
-          pl.split_ml[(part0 + query) * a.q_heads + hk * group + head] = make_float4(tiles ? ref + held : -INFINITY, ref, tiles ? sum : 0.f, 0.f);
+          pl.split_ml[(part0 + query) * a.q_heads + hk * group + head] = make_float4(tiles ? ref + range : -INFINITY, ref, tiles ? sum : 0.f, 0.f);
         }
       }
       // a row's 32 columns are `kChunks` pieces of 16 bytes; a turn of the warp writes 32 / kChunks rows of them
@@ -778,8 +857,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       for (int i = 0; i < kLoads; ++i) raw[i] = fetch(c.k, off, i);
       fetch_scales(0, pages);
     }
-    if (tiles && __all_sync(~0u, bar_wait(bars + kQFull, 0, stop)))
+    uint32_t whole = 0;
+    if (tiles && __all_sync(~0u, bar_wait(bars + kQFull, 0, stop))) {
+      whole = lds32(base + L::misc + 12) / kTile;
       factor *= pow2i(max(-100, (int32_t)(lds32(base + L::misc + 8) >> 7) - 127) - 14);
+    }
     for (uint32_t j = 0; j < tiles; ++j) {
       const uint32_t buf = j & 1, use = j >> 1;
       pages = pages_of(j + 1);  // -1 behind the last tile: nothing is fetched for it
@@ -792,15 +874,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       const float v = bad ? 0.f : v_scale;
       // 2^(e_v - 127) <= the largest of the 32 < 2^(e_v - 126)
       const uint32_t e_v = max(__reduce_max_sync(~0u, __float_as_uint(fabsf(v))) >> 23, 1u);
+      const float in_range = v * __uint_as_float((254u - e_v) << 23);  // the lane's scale, in (-2, 2)
+      uint32_t row_scale = fp16_pack(in_range, in_range);
+      if (j >= whole) {  // values stay integers, their scales meet the weights
+        row_scale = 0x3C003C00u;
+        if (cw & 1) sts32(base + L::scale + (j & 3) * 1024 + 512 + 4 * own32, __float_as_uint(in_range));
+      }
       if ((cw & 1) == 0) {
-        sts32(base + L::scale + (j & 3) * 512 + 4 * own32, bad ? 0x7FC00000u : __float_as_uint(k_scale * factor));
+        sts32(base + L::scale + (j & 3) * 1024 + 4 * own32, bad ? 0x7FC00000u : __float_as_uint(k_scale * factor));
         if (lane == 0) {
           sts32(base + L::info + (j & 3) * 32 + 2 * cw, __float_as_uint((float)(int32_t)(e_v - 127)));
           sts32(base + L::info + (j & 3) * 32 + 16 + 2 * cw, (254u - e_v) << 23);  // 2^-(e_v - 127)
         }
       }
-      const float in_range = v * __uint_as_float((254u - e_v) << 23);  // the lane's scale, in [0, 2)
-      const uint32_t row_scale = fp16_pack(in_range, in_range);
       turn(std::false_type{}, 0u, base + L::k + buf * L::kOperand, c.v, off);
       if (lane == 0) {
         bar_arrive(bars + kScaleFull + 8 * (j & 3));
