@@ -8,8 +8,8 @@ r: roundings to fp16, 2^-11 each. Prompts and large prefixes round a weight, its
 INT8 value (r = 3 2^-11); single tokens only the product of weight and value scale (r = 2^-11).
 f: fp16 ends at 2^-24, half a step of which is 2^-25. A weight enters as P = p 2^(e - E) with p <= 1 at the sequence's largest, its
 value as v 2^-e below 254, and E is 6 below the exponent of the largest value scale that the query has seen: 2^-25 2^E 254 <=
-2^-30 vmax a token, against a sum of weights of at least 1. (Where values enter as their integers, always for single tokens, 127
-stands for 254: 2^-31.)
+2^-30 vmax a token, against a sum of weights of at least 1. (Single tokens: E is 5 below, and values enter as their integers, so that
+127 stands for 254: the same.)
 2^-24: a value scale relative to the largest of 32 tokens enters as fp16, too, off by at most 2^-25.
 A score is a float32 sum of dim products (at most (dim + 8) 2^-24 of the sum of their magnitudes), which changes a weight's share by at
 most twice that; sums over n tokens add (2 n + 64) 2^-24, which covers the exponential's 2^-22. The result is rounded to bfloat16,
@@ -103,6 +103,12 @@ def shared(cache, table, kv_lens, prefix, h, d, seed, scale, q=None, rounded=PRO
     check(out, *exact(q, cache, lambda i: slots[i], kv_lens, scale, rounded, f))
 
 
+def bounds(h, hk, n):
+    """(rounded, f) of single tokens: these batches' prefixes go to the tensor cores from 65 groups of 8 (16) query rows on."""
+    rows = 8 if h // hk <= 8 else 16
+    return (PROMPT, 2.0**-30) if n * (h // hk) > 64 * rows else (SINGLE, 2.0**-30)
+
+
 # (h, hk, new, kv_lens): one whose row tiles share their tokens among blocks, and one with more row tiles than SMs
 FEW, MANY = (6, 2, [150, 3, 40], [1600, 3, 300]), (16, 16, [700, 900, 33], [700, 1200, 33])
 
@@ -118,7 +124,7 @@ def test_few_tokens_whose_values_cancel(n, d):
     cache.v[:, :, 1::2] = -cache.v[:, :, ::2]  # a token and its opposite
     q = base.bf16(60 * n, h, d, seed=3)
     prompt(cache, table, [n] * 60, [n] * 60, h, d, 0, 0.002, q)
-    shared(cache, table, [n] * 60, 0, h, d, 0, 0.002, q[:60], SINGLE, 2.0**-31)
+    shared(cache, table, [n] * 60, 0, h, d, 0, 0.002, q[:60], SINGLE, 2.0**-30)
     many = base.bf16(4000, h, d, seed=4)
     prompt(cache, table[:40], [100] * 40, [n] * 40, h, d, 0, 0.002, many)  # (most rows see nothing)
 
@@ -137,7 +143,7 @@ def test_single_tokens(h, hk, n, prefix, d):
     lens = [prefix + 1 + r * 53 % 400 for r in range(n)]
     table, pages = base.tables(lens, 32, 5)
     cache = base.filled_cache(pages, hk, 32, d, seed=6)
-    shared(cache, table, lens, prefix, h, d, 7, 1 / math.sqrt(d))
+    shared(cache, table, lens, prefix, h, d, 7, 1 / math.sqrt(d), None, *bounds(h, hk, n))
 
 
 def one_strong_key(cache, table, n, at, d, nats):
@@ -186,7 +192,7 @@ def test_tokens_that_a_row_does_not_see_do_not_touch_it(h, hk, new, kv_lens, d, 
 
 
 @pytest.mark.parametrize("small", [1e-4, 1e-7, 1e-12, 1e-20])
-@pytest.mark.parametrize("h,hk,n,prefix", [(32, 2, 70, 1500)])
+@pytest.mark.parametrize("h,hk,n,prefix", [(8, 2, 5, 700), (16, 1, 6, 300), (64, 1, 4, 90), (32, 2, 70, 1500)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_tokens_of_a_prefix_that_a_request_does_not_see(h, hk, n, prefix, d, small):
     """Requests shorter than the prefix, whose later tokens have far larger values."""
@@ -196,4 +202,4 @@ def test_tokens_of_a_prefix_that_a_request_does_not_see(h, hk, n, prefix, d, sma
     cache = base.filled_cache(pages, hk, pt, d, seed=6)
     for s in base.spec.token_slots(table[0], pt, cut).tolist():
         cache.v_scale[s // pt, :, s % pt] *= small
-    shared(cache, table, lens, prefix, h, d, 7, 1 / math.sqrt(d))
+    shared(cache, table, lens, prefix, h, d, 7, 1 / math.sqrt(d), None, *bounds(h, hk, n))
