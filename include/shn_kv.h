@@ -125,20 +125,19 @@ int shn_kv_load(const shn_kv_cache* cache, const int32_t* d_slots, uint32_t n_to
  *   s_j = softmax_scale * (q . k_j);  out = sum_j softmax(s)_j v_j, k_j and v_j = int8 * scale
  * A query that sees nothing (kv_len < n) gives zeros. Rows of d_out behind d_cu_q[n_reqs] stay as they were.
  *  d_q, d_out  device, [n_tokens][q_heads][head_dim] bfloat16, tokens *_stride values apart (a multiple of 8),
- *              16-byte aligned; they do not overlap (one
- *              that is the other is refused)
+ *              16-byte aligned; they do not overlap (one that is the other is refused)
  *  q_heads     a multiple of kv_heads, at most 64 * kv_heads
  * Arithmetic: queries and keys enter the products exactly (parts of a query 2^-32 of the largest of its block of 256 rows
- * aside), scores, their scalings, the softmax and the sums are float32. Before the second product a weight is rounded to
- * fp16, and a value is fp16(int8 * fp16(scale)): 2^-11 each. Weights below 2^-24 times the ratio of the largest value scale of the
- * sequence to the token's are lost, so results are exact to 2^-24 of the sequence's largest value.
- * (The sequence: the tokens that the last of 256 rows sees, so the size of a value scale counts for rows of a few
- * earlier queries too.) A token whose value scale is not finite (or 1e36 and more) makes the rows that see it NaN and
- * leaves the others alone, and so does what stands behind a sequence's end in its last page.
+ * aside), scores, their scalings, the softmax and the sums are float32. At most three things are rounded to fp16, by 2^-11
+ * of themselves: a weight, its token's value scale (relative to the largest of 32 tokens) and the scale's product with the INT8
+ * value. What fp16 cannot hold adds up over the tokens: a query that sees n tokens, whose largest value scale is s, is exact to
+ * (n 2^-30 + 2^-24) 127 s besides. Tokens that a query does not see have no part in either, whatever stands there.
+ * Tokens whose value scale is not finite (or 1e36 and more) make the rows that see them NaN and leave the others alone, and so
+ * does what stands behind a sequence's end in its last page.
  * Device errors: SHN_ERR_INVALID_ARG for a page id outside the cache (detail = the request; that page counts as zeros),
  * a d_kv_len that the table row cannot hold (taken as what it holds) or a d_cu_q that decreases or leaves
- * [0, n_tokens] (those queries are left out); SHN_ERR_TIMEOUT if a wait inside a kernel gave up (a quarter of a second; the
- * result is not complete).
+ * [0, n_tokens] (those queries are left out; what rows hold that are then in two ranges is not defined);
+ * SHN_ERR_TIMEOUT if a wait inside a kernel gave up (a quarter of a second; the result is not complete).
  */
 int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32_t q_heads,
                        const shn_kv_cache* cache, const int32_t* d_block_table, uint32_t max_blocks,
@@ -155,11 +154,13 @@ int shn_kv_attn_prompt(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens
  *  d_work          shn_kv_attn_shared_workspace_bytes, 256-byte aligned; what holds n_reqs requests holds fewer too
  *                  (same cache shape and q_heads)
  * Other arguments and device errors as shn_kv_attn_prompt; *d_prefix_len that the pages cannot hold is taken as what they
- * hold (SHN_ERR_INVALID_ARG). Arithmetic: as there for a large prefix (many query rows, many tokens); for a
- * smaller one and for the requests' own tokens values enter exactly too, their scales with the
- * weights (which are rounded to fp16 once), and parts of a query below 2^-25 of its largest are lost. The parts of a row meet
- * in float32 before they are divided by the sum of the weights: a sum of weights times values above 3.4e38 is infinite. A
- * token whose value scale is not finite makes the rows that see it NaN or infinite.
+ * hold (SHN_ERR_INVALID_ARG). Arithmetic: as there for a large prefix (many query rows, room for many tokens in d_prefix_pages); for a
+ * smaller one and for the requests' own tokens only the product of weight and value scale is rounded to fp16 (2^-11, and
+ * n 2^-30 127 s), and parts of a query below 2^-25 of its largest are lost. The parts of a row meet in float32 before they are divided
+ * by the sum of the weights: a sum of weights times values above 3.4e38 is infinite. A token whose value scale is not finite makes
+ * the rows that see it NaN or infinite.
+ * Which kernel a call takes is chosen by the sizes on the host, n_reqs, n_prefix_pages and max_blocks: a captured step with room for
+ * far more tokens than it has takes what suits the room.
  */
 size_t shn_kv_attn_shared_workspace_bytes(const shn_kv_cache* cache, uint32_t n_reqs, uint32_t q_heads);
 int shn_kv_attn_shared(const uint16_t* d_q, uint64_t q_stride, uint32_t n_reqs, uint32_t q_heads,
