@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if (ok) half_tile(std::true_type{}, j, 1, info, grows);
       if (ok) end_tile();
     }
+    wait_st();  // (weights that a wait which gave up left on their way: TMEM goes back behind them)
     // the rows' sums, through shared memory to the threads that write the rows: warps of the same 32 rows take half of the
     // columns each (the barrier comes first: no warp may miss it)
     const uint32_t rows32 = (warp & 3) * 32;
@@ -956,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if (!ok) {
         // gave up: let the products in flight end (again with a limit) before TMEM goes back
         commit(bars + kDrain + 8 * i, lead);
-        for (uint32_t n = 0; n < kWaitTries && !bar_try(bars + kDrain + 8 * i, 0); ++n) {
+        for (uint32_t n = 0; n < kDrainTries && !bar_try(bars + kDrain + 8 * i, 0); ++n) {
         }
       }
     }

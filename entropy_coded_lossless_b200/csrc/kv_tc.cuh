@@ -28,10 +28,14 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 // Waits for the phase of this parity, at most kWaitTries tries of 2000 ns each: a quarter of a second, where a legitimate
-// wait here is microseconds. False: gave up, or another warp of the block did, which *stop tells.
-constexpr uint32_t kWaitTries = 1u << 17;
+// wait here is microseconds. False: gave up, or another warp of the block did, which *stop tells. (A build for tests may set
+// fewer tries; the products that a block has in flight are waited for with the full limit all the same.)
+#ifndef SHN_KV_WAIT_TRIES
+#define SHN_KV_WAIT_TRIES (1u << 17)
+#endif
+constexpr uint32_t kWaitTries = SHN_KV_WAIT_TRIES, kDrainTries = 1u << 17;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t stop) {
-  for (uint32_t i = 0; i < kWaitTries; ++i) {
+  for (uint32_t i = 0; i != kWaitTries; ++i) {
     if (bar_try(bar, parity)) return true;
     if ((i & 63u) == 63u && lds32(stop) != 0) return false;
   }
