@@ -1,11 +1,12 @@
 """Build libshn.so (the CUDA kernels + C ABI) in-tree for sm_100a with nvcc, and _kv.so (the Python calls of the paged
-KV cache over it) with g++.
+KV cache over it) with g++ and torch's headers. Only the module ``kv`` needs the latter: where it cannot be built, build() warns.
 
     python -m entropy_coded_lossless_b200.build [--force]
 """
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -18,6 +19,7 @@ HEADERS = [os.path.join(CSRC, "shn_internal.cuh"), os.path.join(ROOT, "include",
 KV_HEADERS = [os.path.join(CSRC, "kv_internal.cuh"), os.path.join(CSRC, "kv_tc.cuh"),
               os.path.join(CSRC, "kv_decode.cuh"), os.path.join(ROOT, "include", "shn_kv.h")]
 BINDING = os.path.join(HERE, "_kv.so")
+BINDING_TORCH = os.path.join(HERE, "_build", "_kv.torch")  # the torch it was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
@@ -32,14 +34,28 @@ def _stale(target, deps):
 
 def build(force: bool = False, verbose: bool = False) -> str:
     lib = build_lib(force, verbose)
-    build_binding(force, verbose)
+    try:
+        build_binding(force, verbose)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"_kv.so not built, so entropy_coded_lossless_b200.kv does not import ({e}); the codec does without it", RuntimeWarning,
+                      stacklevel=2)
     return lib
+
+
+def _torch_version():
+    from importlib import metadata
+
+    return metadata.version("torch")
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     src = os.path.join(CSRC, "kv_binding.cpp")
+    version = _torch_version()
     if not force and not _stale(BINDING, [src, os.path.join(ROOT, "include", "shn_kv.h"), os.path.join(ROOT, "include", "shn.h")]):
-        return BINDING
+        if os.path.exists(BINDING_TORCH) and open(BINDING_TORCH).read() == version:
+            return BINDING
+    if os.path.exists(BINDING):  # one that no longer fits is not left to be imported
+        os.remove(BINDING)
     import sysconfig
 
     import torch
@@ -53,6 +69,9 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)
+    os.makedirs(os.path.dirname(BINDING_TORCH), exist_ok=True)
+    with open(BINDING_TORCH, "w") as f:
+        f.write(version)
     return BINDING
 
 
