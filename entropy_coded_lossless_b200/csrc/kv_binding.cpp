@@ -88,7 +88,8 @@ struct Args {
   };
   Table table(int i, int64_t reqs) const {
     const Tensor& t = tensor(i, "block_table");
-    if (t.dim() != 2 || t.size(0) != reqs) throw std::invalid_argument("block_table must be [" + std::to_string(reqs) + ", max_blocks]");
+    if (t.dim() != 2 || t.size(0) != reqs || t.size(1) > UINT32_MAX)
+      throw std::invalid_argument("block_table must be [" + std::to_string(reqs) + ", max_blocks]");
     return {i32(i, "block_table"), (uint32_t)t.size(1)};
   }
   void* work(int i, size_t& bytes) const {
@@ -103,19 +104,20 @@ struct Args {
   }
 };
 
-// The call's device made current around it, and its stream: the caller's, or the device's current one.
+// The call's device made current around it, and its stream: the caller's, or the device's current one. What may be refused is
+// asked first, so that a refusal leaves the device as it was; and putting it back raises nothing, whatever the call met.
 struct On {
+  void* stream;
   int before;
   bool changed;
-  void* stream;
-  On(const Args& a, int i) {
-    before = c10::cuda::current_device();
-    changed = before != a.device;
+  On(const Args& a, int i)
+      : stream(a.none(i) ? static_cast<void*>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)a.device).stream()) : reinterpret_cast<void*>((uintptr_t)a.u(i))),
+        before(c10::cuda::current_device()),
+        changed(before != a.device) {
     if (changed) c10::cuda::set_device((c10::DeviceIndex)a.device);
-    stream = a.none(i) ? static_cast<void*>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)a.device).stream()) : reinterpret_cast<void*>((uintptr_t)a.u(i));
   }
   ~On() {
-    if (changed) c10::cuda::set_device((c10::DeviceIndex)before);
+    if (changed) (void)c10::cuda::SetDevice((c10::DeviceIndex)before);
   }
 };
 
@@ -148,7 +150,7 @@ PyObject* plan(PyObject*, PyObject* const* v, Py_ssize_t n) {
     int32_t *next = a.i32(6, "free_next", 1), *cu = a.i32(7, "cu_new", reqs + 1), *len = a.i32(8, "kv_len", reqs),
             *pos = a.i32(9, "positions", tokens), *slots = a.i32(10, "slots", tokens);
     const int64_t n_free = THPVariable_Unpack(a.v[4]).numel();
-    if (n_free > UINT32_MAX || tokens > UINT32_MAX) throw std::invalid_argument("a buffer is too long");
+    if (n_free > UINT32_MAX || tokens > UINT32_MAX || reqs > UINT32_MAX) throw std::invalid_argument("a buffer is too long");
     const uint64_t pt = a.u(2);
     if (pt > 1024) return (int)SHN_ERR_INVALID_ARG;
     const On on(a, 12);

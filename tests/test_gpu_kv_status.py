@@ -85,3 +85,22 @@ def test_prompts_report_the_first_bad_request(n, new):
             for _ in range(3):
                 kv.shn_kv_attn_prompt(q, cache, t, ints(cu), ints(lens), 0.1, out, w)
                 assert status(w) == (BAD, min(bad)), (what, bad)
+
+
+def test_refusals_of_arguments_that_are_no_tensors():
+    """A stream that is none, an epsilon that is no number: refused, and the current device stays."""
+    cache, w = base.filled_cache(2, 1, 16, 64), work()
+    k, slots = base.bf16(2, 1, 64), ints([0, 1])
+    was, before = cache.k.clone(), torch.cuda.current_device()
+
+    class NoStream:
+        cuda_stream = "x"
+
+    with pytest.raises(ValueError):
+        kv.shn_kv_load(cache, slots, k, None, w, stream=NoStream())
+    with pytest.raises(ValueError):
+        kv.shn_kv_store(None, k, k, None, slots, cache, None, w, stream=NoStream())
+    with pytest.raises(ValueError):
+        kv.shn_kv_store(None, k, k, None, slots, cache, None, w, eps="small")
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k, was) and torch.cuda.current_device() == before
