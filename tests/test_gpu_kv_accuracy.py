@@ -203,3 +203,29 @@ def test_tokens_of_a_prefix_that_a_request_does_not_see(h, hk, n, prefix, d, sma
     for s in base.spec.token_slots(table[0], pt, cut).tolist():
         cache.v_scale[s // pt, :, s % pt] *= small
     shared(cache, table, lens, prefix, h, d, 7, 1 / math.sqrt(d), None, *bounds(h, hk, n))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_error_in_the_mean(d, monkeypatch):
+    """Over many results the error is the result's own rounding to bfloat16 and the roundings to fp16, at most three for each token.
+    These are independent of each other and across tokens, uniform within half a step of 2^-10 or less: at most 2^-11 / sqrt(3) of a
+    token's part each, so that their squares add up to at most 2^-22 of the sum of the parts' squares, which for values of random
+    signs is the result's. (Weights in bfloat16 would add 64 times that; 1.05: the sample's spread.)"""
+    seen = []
+
+    def mean(out, ref, tol):
+        own = (ref.to(torch.bfloat16).double() - ref).norm() / ref.norm()
+        seen.append((((out.double() - ref).norm() / ref.norm()).item(), own.item()))
+
+    monkeypatch.setitem(globals(), "check", mean)
+    pt, hk, h = 32, 16, 16
+    for new, kv_lens in (([300, 40], [1500, 300]), ([900, 700], [900, 1000])):
+        table, pages = base.tables(kv_lens, pt, 5)
+        prompt(base.filled_cache(pages, hk, pt, d, seed=6), table, new, kv_lens, h, d, 7, 1 / math.sqrt(d))
+    for h, hk, n, prefix in ((32, 8, 9, 700), (32, 2, 70, 1500)):
+        lens = [prefix + 1 + r * 53 % 400 for r in range(n)]
+        table, pages = base.tables(lens, pt, 5)
+        shared(base.filled_cache(pages, hk, pt, d, seed=6), table, lens, prefix, h, d, 7, 1 / math.sqrt(d))
+    assert len(seen) == 4
+    for err, own in seen:
+        assert err <= 1.05 * math.sqrt(own**2 + 2.0**-22), seen
