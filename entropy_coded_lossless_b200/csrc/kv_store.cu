@@ -10,11 +10,13 @@ __global__ void kv_begin_kernel(DeviceStatus* st) {
   if (threadIdx.x == 0) st->status = 0, st->detail = 0;
 }
 
-// The status of a call whose errors its indexes alone show. Up to kOneTokens tokens (kOne) one block looks at all of them
-// and is the only one to write the status, so no kernel has to clear it first: 64 tokens stored and loaded again 4.97 us
-// against 5.99 with one in front of each, 8000 53.5 against 54.8. With more tokens that block would be the last to end (65,536
-// tokens of one head of 64 loaded in 21.2 us against 7.8): then the kernel in front clears the status and every block
-// reports what it finds.
+// The status of a call whose errors its indexes alone show: one block looks at all of them and is the only one to write the
+// status, so no kernel has to clear it first (64 tokens stored and loaded again 4.97 us against 5.99 with one in front of each).
+// A store always does so, since its tokens take longer than their indexes (one key head of 64: 8192 tokens 7.5 us, with a kernel
+// in front and every block reporting 8.4; 262,144 tokens 196 and 205; 32 query and 8 key heads of 128, 65,536 tokens 262 and 279).
+// In a load of many small rows that block would be the last to end, so it does up to kOneTokens tokens (kOne); with more the kernel
+// in front clears the status and every block reports. Measured, the one block / the kernel in front: one head of 64, 4096 tokens
+// 2.65 / 2.91 us, 8192 3.80 / 3.30, 65,536 21.3 / 8.0; 8 heads of 128, 8192 tokens 10.2 / 10.8, 12,288 14.7 / 14.8, 16,384 18.8 / 18.4.
 constexpr uint32_t kOneTokens = 8192;
 constexpr int kAhead = 8;  // 16-byte loads of a thread on their way together
 // The first of the n indexes that is outside [0, end); negative ones are fine where kNone.
@@ -117,17 +119,17 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-template <int D, bool kOne>
+template <int D>
 __global__ void __launch_bounds__(kStoreThreads, kStoreBlocks) kv_store_kernel(KvPages c, KvStoreArgs a) {
   using namespace tc;
   constexpr uint32_t kLanes = D / 8, kGroups = kStoreThreads / kLanes;
-  if (kOne && blockIdx.x == 0) {
+  if (blockIdx.x == 0) {
     if (blockIdx.y) return;
     uint32_t first = first_outside<true, kStoreThreads>(a.slots, a.n_tokens, c.n_pages << c.log2_pt);
     if (a.rot) first = min(first, first_outside<false, kStoreThreads>(a.positions, a.n_tokens, a.n_positions));
     return write_status<kStoreThreads>(a.st, first);
   }
-  const uint32_t block = blockIdx.x - kOne, blocks = gridDim.x - kOne;
+  const uint32_t block = blockIdx.x - 1, blocks = gridDim.x - 1;
   const uint32_t lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   // The block's share of the query rows, and of the key and value rows (keys first); all lanes of a warp run the same
   // number of turns (the shuffles are full).
@@ -182,7 +184,6 @@ __global__ void __launch_bounds__(kStoreThreads, kStoreBlocks) kv_store_kernel(K
   };
   // a block's tokens one after another; the next one's slot and position are read a turn ahead
   int32_t slot = a.slots[block], pos = a.rot ? a.positions[block] : 0;
-  if constexpr (!kOne) after_previous();
   for (uint32_t token = block; token < a.n_tokens; token += blocks) {
     q_src = a.q + (uint64_t)token * a.q_stride + d_lo;
     k_src = a.k + (uint64_t)token * a.k_stride + d_lo, v_src = a.v + (uint64_t)token * a.v_stride + d_lo;
@@ -193,10 +194,7 @@ __global__ void __launch_bounds__(kStoreThreads, kStoreBlocks) kv_store_kernel(K
       slot = a.slots[token + blocks];
       if (a.rot) pos = a.positions[token + blocks];
     }
-    if ((slot_now >= 0 && ((uint32_t)slot_now >> c.log2_pt) >= c.n_pages) || (a.rot && (uint32_t)pos_now >= a.n_positions)) {
-      if (!kOne && threadIdx.x == 0 && blockIdx.y == 0) report_first(a.st, SHN_ERR_INVALID_ARG, token);
-      continue;
-    }
+    if ((slot_now >= 0 && ((uint32_t)slot_now >> c.log2_pt) >= c.n_pages) || (a.rot && (uint32_t)pos_now >= a.n_positions)) continue;
     Turn turn = {};
     if (turns) {
       const float *cp = a.cos_sin + (uint64_t)pos_now * a.rot, *sp = cp + a.rot / 2;
@@ -344,18 +342,9 @@ cudaError_t launch_kv_store(const KvPages& c, uint32_t head_dim, const KvStoreAr
   uint32_t parts = 1;
   while ((uint64_t)parts * a.n_tokens < 8ull * sm_count && parts * groups < rows) ++parts;
   // as many blocks as the SMs have places, each with its tokens (or the status)
-  if (a.n_tokens > kOneTokens) {
-    const cudaError_t e = launch_kv_begin(a.st, s);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(a.n_tokens < kStoreBlocks * (uint32_t)sm_count ? a.n_tokens : kStoreBlocks * (uint32_t)sm_count, parts);
-    return head_dim == 128 ? launch_behind(kv_store_kernel<128, false>, grid, kStoreThreads, 0, s, c, a)
-                           : launch_behind(kv_store_kernel<64, false>, grid, kStoreThreads, 0, s, c, a);
-  }
   const uint32_t most = kStoreBlocks * (uint32_t)sm_count - 1;
   const dim3 grid(1 + (a.n_tokens < most ? a.n_tokens : most), parts);
-  if (head_dim == 128) kv_store_kernel<128, true><<<grid, kStoreThreads, 0, s>>>(c, a);
-  else kv_store_kernel<64, true><<<grid, kStoreThreads, 0, s>>>(c, a);
-  return cudaGetLastError();
+  return head_dim == 128 ? launch_first(kv_store_kernel<128>, grid, kStoreThreads, 0, s, c, a) : launch_first(kv_store_kernel<64>, grid, kStoreThreads, 0, s, c, a);
 }
 
 cudaError_t launch_kv_load(const KvPages& c, uint32_t head_dim, const KvLoadArgs& a, cudaStream_t s) {
