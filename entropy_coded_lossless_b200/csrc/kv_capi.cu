@@ -69,6 +69,8 @@ int check_attn(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32
 // 18.4 / 26.6, 8192 tokens 28.7 / 34.8; 16 requests 1024 tokens 20.5 / 26.7, 8192 tokens 41.0 / 36.8. So tensor cores from
 // kPrefixUnits units on, and for more row groups than the workspace keeps places for.
 constexpr uint64_t kPrefixUnits = 12288, kPrefixGroups = 64;
+// As many parts as give each of a B200's SMs a block: a number and not a question to the device, since the size query is for any device
+// and makes no CUDA call. (Fewer or more SMs get the same parts, and right results.)
 constexpr uint64_t kSplitBlocks = 148;
 
 // How shn_kv_attn_shared is cut up, and its workspace: [status 256][pieces' sums][pieces' (mt, ms, l)][the same of the prefix's

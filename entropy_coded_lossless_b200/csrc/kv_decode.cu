@@ -11,10 +11,11 @@
 // is scaled by a power of two into fp16, exactly but for parts 2^-25 of its largest. Scales meet the float32 scores: with
 // x = s k_scale softmax_scale log2(e),
 //   p = 2^(x - m),   l += p,   P = fp16(p v_scale 2^-E)   (2^-11, the one rounding before the sums)
-// The reference m is raised only when a score passes it by 8, and E, the exponent a row's sums are held in, when a value
-// scale that the row sees is 2^7 above it (2^15 together, within fp16); then E is 5 below that scale's. Almost every step does
-// without a reduction across lanes. What fp16 cannot hold of a token's part is 2^-25 of the row's range, so the sums are exact
-// to n 2^-30 of the largest value of the n tokens that the row sees.
+// The reference m is raised only when a score passes it by 8, and E, the exponent the sums are held in, when a value scale
+// is 2^7 above it (2^15 together, within fp16); then E is 5 below that scale's. Almost every step does without a reduction
+// across lanes. What fp16 cannot hold of a token's part is 2^-25 of that range, so the sums are exact to n 2^-30 of the largest
+// value of the n tokens that the row sees: in a shared prefix a step that holds the end of what some row sees is taken in parts
+// that end there, so that a row's own tokens are summed before larger ones that it does not see raise E.
 //
 // Measured (32 query and 8 key heads of 128, 128 requests with 1024 own tokens each): 53 us for 282 MB, 5.3 TB/s, 81 % of
 // the measured copy rate. The join then reads what the parts of the prefix and the pieces left for each row: 15 us.
@@ -216,28 +217,29 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
     const int32_t full_to = min((int32_t)t_last, __reduce_min_sync(~0u, least));
 
     float o[NT][D / 16][4], l[NT][2], m[NT][2], above[NT][2];  // above: m + 8
-    float held[NT][2], unit[NT][2], ceiling = 0.f;             // E, 2^-E; the least 2^(E + 7) of the rows that see more tokens
+    float held = -200.f, ceiling = 0.f, unit = 0.f;            // E, 2^(E + 7), 2^-E
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[nt][i] = m[nt][i] = 0.f, above[nt][i] = -INFINITY;  // (a reference of 0 until there is one)
-        held[nt][i] = -200.f, unit[nt][i] = 0.f;
-      }
+      for (int i = 0; i < 2; ++i) l[nt][i] = m[nt][i] = 0.f, above[nt][i] = -INFINITY;  // (a reference of 0 until there is one)
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[nt][k][i] = 0.f;
     }
 
+    int32_t from = t_from;  // the first token that is not summed yet
+    bool again = false;     // the rest of a step
 #pragma unroll 1
-    for (uint32_t t = t_first; t < t_last; t += 16) {
-      // the step kStages - 1 ahead into the stage that the last step left
-      const uint32_t ahead = t + 16 * (kStages - 1);
-      fetch((stage + kStages - 1) % kStages, row_of(ahead, page_next));
-      page_next = page_of(ahead + 16);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      __syncwarp();
+    for (uint32_t t = t_first; t < t_last;) {
+      if (!again) {
+        // the step kStages - 1 ahead into the stage that the last step left
+        const uint32_t ahead = t + 16 * (kStages - 1);
+        fetch((stage + kStages - 1) % kStages, row_of(ahead, page_next));
+        page_next = page_of(ahead + 16);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
+      }
       const uint32_t at = ring + stage * kStage;
       float s[NT][4];
 #pragma unroll
@@ -272,12 +274,24 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[nt][i] *= ks[i >> 1] * mul[nt][i & 1];
-      const bool edge = (int32_t)t < t_from || (int32_t)t + 16 > full_to;
+      const bool edge = (int32_t)t < from || (int32_t)t + 16 > full_to;
+      again = false;
       if (edge) {
+        const int32_t begin = max(from, (int32_t)t);
+        int32_t end = min((int32_t)t_last, (int32_t)t + 16);
+        const int32_t step_end = end;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (limit_at[nt][e] > begin) end = min(end, limit_at[nt][e]);
+        end = __reduce_min_sync(~0u, end);
+        again = end < step_end;
+        from = end;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int32_t tok = (int32_t)(t + g + 8 * i);
-          const bool in = tok >= t_from && tok < (int32_t)t_last;
+          const bool in = tok >= begin && tok < end;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -294,33 +308,20 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
 #pragma unroll
         for (int e = 0; e < 2; ++e) rise |= fmaxf(s[nt][e], s[nt][2 + e]) > above[nt][e];
       if (__any_sync(~0u, rise)) {
-        uint32_t big[2];  // value scales that are finite
+        uint32_t big = 0;  // the largest finite value scale of the step
 #pragma unroll
-        for (int i = 0; i < 2; ++i) big[i] = fabsf(vs_now[i]) < INFINITY ? __float_as_uint(fabsf(vs_now[i])) : 0u;
-        const bool larger = __uint_as_float(__reduce_max_sync(~0u, max(big[0], big[1]))) > ceiling;
-        float lower[NT][2], least = INFINITY;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            lower[nt][e] = 1.f;
-            if (!larger) continue;
-            // the largest that the row sees
-            uint32_t most = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if ((int32_t)(t + g + 8 * i) < limit_at[nt][e]) most = max(most, big[i]);
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) most = max(most, __shfl_xor_sync(~0u, most, d));
-            if (most && (float)(int32_t)(most >> 23) - 127.f > held[nt][e] + 6.f) {
-              const float to = (float)max(-126, min(121, (int32_t)(most >> 23) - 132));
-              lower[nt][e] = held[nt][e] < -150.f ? 0.f : pow2(fmaxf(held[nt][e] - to, -126.f));
-              held[nt][e] = to;
-              unit[nt][e] = pow2(-to);
-            }
-            if (limit_at[nt][e] > (int32_t)t + 16) least = fminf(least, held[nt][e] < -150.f ? 0.f : pow2(held[nt][e] + 7.f));
-          }
-        if (larger) ceiling = __uint_as_float(__reduce_min_sync(~0u, __float_as_uint(least)));
+        for (int i = 0; i < 2; ++i)
+          if (fabsf(vs_now[i]) < INFINITY) big = max(big, __float_as_uint(fabsf(vs_now[i])));
+        big = __reduce_max_sync(~0u, big);
+        float lower = 1.f;
+        if (__uint_as_float(big) > ceiling) {
+          const float to = (float)max(-126, min(121, (int32_t)(big >> 23) - 132));
+          const float down = held - to;  // (in two steps: what a row has summed stays right even where it is not normal any more)
+          lower = held < -150.f ? 0.f : pow2(fmaxf(down, -126.f)) * pow2(fmaxf(fminf(down + 126.f, 0.f), -126.f));
+          held = to;
+          ceiling = pow2(held + 7.f);
+          unit = pow2(-held);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -335,12 +336,13 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
               above[nt][e] = x + 8.f;
             }
             l[nt][e] *= keep;
-            keep *= lower[nt][e];
+            keep *= lower;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) o[nt][k][e] *= keep, o[nt][k][2 + e] *= keep;
           }
       }
       uint32_t pb[NT][2];
+      const float f[2] = {vs_now[0] * unit, vs_now[1] * unit};
       auto weights = [&](auto edge_tag) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
               const float x = s[nt][2 * i + e];
               p[e] = exp2_approx(x - m[nt][e]);
               l[nt][e] += p[e];
-              p[e] *= vs_now[i] * unit[nt][e];
+              p[e] *= f[i];
               if constexpr (decltype(edge_tag)::value) p[e] = x == -INFINITY ? 0.f : p[e];  // (a scale may be infinite)
             }
             pb[nt][i] = transposed8x8(fp16_pack(p[0], p[1]));
@@ -390,8 +392,10 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][k], af, pb[nt][0], pb[nt][1]);
       }
+      if (again) continue;
       __syncwarp();  // the stage is read: the next turn may fill it
       stage = (stage + 1) % kStages;
+      t += 16;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");  // (what was fetched ahead of the end is nothing)
     __syncwarp();
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 2 : 1) kv_decode_ker
 #pragma unroll
         for (int k = 0; k < D / 16; k += 2)
           *reinterpret_cast<float4*>(dst + 2 * k) = make_float4(o[nt][k][e], o[nt][k][2 + e], o[nt][k + 1][e], o[nt][k + 1][2 + e]);
-        if (g == 0) pl.ml[q] = make_float4(held[nt][e] < -150.f ? -INFINITY : m[nt][e] + held[nt][e], above[nt][e] == -INFINITY ? -INFINITY : m[nt][e], x, 0.f);
+        if (g == 0) pl.ml[q] = make_float4(held < -150.f ? -INFINITY : m[nt][e] + held, above[nt][e] == -INFINITY ? -INFINITY : m[nt][e], x, 0.f);
       }
 
     // ---- on to the next segment ----

@@ -15,7 +15,7 @@ namespace shn {
 
 constexpr uint32_t kUnit = 32;           // tokens
 constexpr uint32_t kDecodeThreads = 256;
-constexpr uint32_t kDecodeMaxWarps = 148 * 16;  // two blocks on each SM; the workspace has room for their pieces
+constexpr uint32_t kDecodeMaxWarps = 148 * 16;  // two blocks on each of a B200's SMs; the workspace has room for their pieces
 
 struct DecodePlan {
   uint32_t rows;           // query rows of a segment: 8 or 16
