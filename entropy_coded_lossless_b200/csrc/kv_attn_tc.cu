@@ -17,7 +17,7 @@
 // Tokens that a row does not see are nothing to it, whatever their size. So a tile that some row of the block does not see whole
 // has the integers as values and the scales on the float32 weights, P = fp16(p * v_scale 2^-E), and each row's E is of what it sees.
 // (All tiles that way would round once for three times: the mean error stays 0.0017, 8192 tokens take 761 us a call instead
-// of 696.)
+// of 663.)
 //
 // Softmax in one pass over the scores, without a search for the maximum: m is the maximum of a row's first 64 scores, and a
 // thread's sum of 16 weights shows whether one of the later ones is above it by 2^8; only then m is raised, and what is
@@ -32,14 +32,14 @@
 // Where a call has too few rows to fill the SMs, up to 8 blocks of a cluster share a row tile's tokens and join their sums in
 // each other's shared memory (join_parts): no workspace, no second launch.
 //
-// What bounds it. 8192 causal tokens, 32 query and 8 key heads of 128: 700 us in a run of calls, 785 TFLOP/s, 48 % of the
-// measured bf16 rate (630 us and 53 % for the call alone in a graph). A tile of 256 x 128 scores costs a block about 4400
+// What bounds it. 8192 causal tokens, 32 query and 8 key heads of 128: 663 us in a run of calls, 829 TFLOP/s, 50 % of the
+// measured bf16 rate (598 us and 56 % for the call alone in a graph). A tile of 256 x 128 scores costs a block about 4400
 // cycles; the products would take 2048 of them (1024 at D = 64) and so would the exponentials, at 16 a cycle; issuing the
 // instructions of softmax, conversion and waits takes some 3000 of each scheduler. So the softmax sets the pace, by its
 // instructions and their latency, and products and fetches run behind it.
 // The steps, same case: a thread per row with its 128 scores in registers 1458 us; a row shared by four threads, so that a
 // column's scale is read for two rows, 1193; 16 softmax warps 759; two issuing warps, halves with scores formed ahead and no
-// search for the maximum 716; whole lines out and a shorter block start 700. Tried and not kept: 8 softmax warps of 32
+// search for the maximum 716; whole lines out and a shorter block start 690; tiles in front of the edge in a loop of their own 663. Tried and not kept: 8 softmax warps of 32
 // rows, and blocks of all requests in the order of their lengths.
 #include <type_traits>
 
@@ -391,12 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       qx[i] = make_uint4(0, 0, 0, 0);
       if (row < rows_here) qx[i] = *reinterpret_cast<const uint4*>(q_src + (uint64_t)query * a.q_stride + head * D + piece * 8);
     }
-    int32_t seen[2];  // (rows behind the last one: all tokens)
+    int32_t seen[2];  // (rows behind the last one: all tokens); from here to the edge's tiles in shared memory
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const uint32_t row = half * 128 + lanes + quad + 8 * r;
       seen[r] = row < rows_here ? seen_by(row) : 0x7FFFFFFF;
     }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if ((lane & 3) == 0) sts32(base + L::row_sum + 4 * (half * 128 + lanes + quad + 8 * r), (uint32_t)seen[r]);
     const int32_t least_seen = __reduce_min_sync(~0u, min(seen[0], seen[1]));
     if (lane == 0) atomicMin(reinterpret_cast<int32_t*>(smem + L::misc + 12), least_seen);
     // One power of two brings the block's largest query value just below 2^15; fp16 then holds every bf16 down to 2^-32
@@ -437,8 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     fence_smem();
     bar_arrive(bars + kQFull);
 
-    // Tiles that all rows of the block see whole come first: all rows hold their sums in the same range, and no column's place is
-    // looked at. In the others a row has its own.
+    // Tiles that all rows of the block see whole come first: all rows hold their sums in the same range (held[0]), and no column's
+    // place is looked at. In the others a row has its own. What only those need is kept out of the first ones' registers (8192
+    // tokens 640 -> 598 us).
     const uint32_t whole = min(tiles, lds32(base + L::misc + 12) / kTile);
     float m[2], l[2];
     float neg[2];    // minus the reference (0 while there is none)
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
     // A warp whose rows are all behind the last one keeps step and does no more: its places in TMEM hold anything, and so do
     // these rows' sums, which nobody reads (one query after 5102 tokens 29.6 -> 25.8 us, 24 short requests 14.4 -> 12.8). Not for
     // full grids, whose blocks have few such rows: there the question alone costs 7 % (8192 tokens 627 -> 673 us).
-    if (kSplit && half * 128 + lanes >= rows_here) seen[0] = -1;
+    const bool skip = kSplit && half * 128 + lanes >= rows_here;
     bool ok = true;
     // Half a tile (64 tokens) at a time. The first half's scores lie in the 64 columns `here`, the second's in the other 64; both
     // halves' weights go into `here` (32 columns each). So the columns of the second half are free as soon as its scores
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       const uint32_t here = s_at + (j & 1) * 64;
       ok = __all_sync(~0u, bar_wait(bars + kSFull + 16 * half + 8 * h, j & 1, stop));
       if (!ok) return;
-      if (kSplit && seen[0] < 0) {  // (see above)
+      if (skip) {  // (see above)
         if (lane == 0 && h == 1) bar_arrive(bars + kPFull + 16 * half);
         return;
       }
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
         }
         bool raised = false;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < (kEdge ? 2 : 1); ++r) {
           if (!(top[r] > held[r] + kValueRise)) continue;
           const float to = fmaxf(top[r] - kValueRise, -126.f);
           lower[r] = pow2(fmaxf(held[r] - to, -126.f));
@@ -517,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
           held2[r] = pow2(to);
           raised = true;
         }
+        if constexpr (!kEdge) lower[1] = lower[0];
         rise |= __any_sync(~0u, raised);
       }
       float sum[2];
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
           float by[2], unby[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int of = kMask ? r : 0;
+            const int of = kMask ? r : 0;  // (no mask: the warp's rows have the same range)
             by[r] = fmaxf(size - held[of], kValueFall);
             unby[r] = fminf(held2[of] * inverse, kValueFall2);
             if constexpr (kMask) by[r] = fminf(by[r], kValueClimb), unby[r] = fmaxf(unby[r], kValueClimb2);
@@ -652,6 +657,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(KvPages c, KvAtt
       if (ok) half_tile(std::false_type{}, j, 1, info, false);
       if (ok) end_tile();
     }
+    held[1] = held[0], held2[1] = held2[0];
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      seen[r] = (int32_t)lds32(base + L::row_sum + 4 * (half * 128 + lanes + quad + 8 * r));
 #pragma unroll 1
     for (; j < tiles && ok; ++j) {
       uint32_t info;
