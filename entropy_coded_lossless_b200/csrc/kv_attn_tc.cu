@@ -39,8 +39,8 @@
 // instructions and their latency, and products and fetches run behind it.
 // The steps, same case: a thread per row with its 128 scores in registers 1458 us; a row shared by four threads, so that a
 // column's scale is read for two rows, 1193; 16 softmax warps 759; two issuing warps, halves with scores formed ahead and no
-// search for the maximum 716; whole lines out and a shorter block start 690; tiles in front of the edge in a loop of their own 663. Tried and not kept: 8 softmax warps of 32
-// rows, and blocks of all requests in the order of their lengths.
+// search for the maximum 716; whole lines out and a shorter block start 690; tiles in front of the edge in a loop of their
+// own 663. Tried and not kept: 8 softmax warps of 32 rows, and blocks of all requests in the order of their lengths.
 #include <type_traits>
 
 #include "kv_decode.cuh"
@@ -1007,8 +1007,8 @@ cudaError_t launch_kv_prompt(const KvPages& c, uint32_t head_dim, const KvAttnAr
   DecodePlan pl = {};
   pl.splits = 1;
   // Few blocks, and requests that may be long: several blocks to the same rows, as many as the SMs have places and the longest
-  // sequence tiles. Measured, with and without: one query after 5102 tokens (8 heads on one) 25.9 / 118.8 us, 700 after 2551 (8 on
-  // 2) 34.4 / 74.6, 40 after 5102 (32 on 8, of 64) 26.6 / 102.1. With 4 blocks to a row at most they take 42.4, 34.2 and
+  // sequence tiles. Measured, with and without: one query after 5102 tokens (8 heads on one) 25.5 / 118.8 us, 700 after 2551 (8 on
+  // 2) 33.8 / 74.6, 40 after 5102 (32 on 8, of 64) 27.5 / 102.1. With 4 blocks to a row at most they take 42.4, 34.2 and
   // 37.8, with up to twice the blocks that have places 29.7, 49.1 and 27.0.
   const uint64_t tokens = (uint64_t)a.max_blocks << c.log2_pt;  // what a request can have
   kv_prompt_begin_kernel<<<1, a.n_reqs < 1024 ? (a.n_reqs + 31) / 32 * 32 : 1024, 0, s>>>(c, a);

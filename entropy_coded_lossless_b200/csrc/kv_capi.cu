@@ -65,8 +65,8 @@ int check_attn(const uint16_t* d_q, uint64_t q_stride, uint32_t n_tokens, uint32
 
 // Which kernel the prefix goes to. The single-token kernel reads it once for each 8 (16) query rows, about 1.5 ns a unit of 32
 // tokens; the tensor core kernel serves 256 rows at once but takes some 12 us to start and end. Measured (32 query and 8
-// key heads of 128, microseconds of a call with 16 own tokens each, single-token kernel / tensor cores): 8 requests 1024 tokens
-// 18.4 / 26.6, 8192 tokens 28.7 / 34.8; 16 requests 1024 tokens 20.5 / 26.7, 8192 tokens 41.0 / 36.8. So tensor cores from
+// key heads of 128, microseconds of GPU time with 16 own tokens each, single-token kernel / tensor cores): 8 requests 1024 tokens
+// 13.3 / 18.0, 8192 tokens 22.8 / 26.6; 16 requests 1024 tokens 15.8 / 19.3, 8192 tokens 33.2 / 28.0. So tensor cores from
 // kPrefixUnits units on, and for more row groups than the workspace keeps places for.
 constexpr uint64_t kPrefixUnits = 12288, kPrefixGroups = 64;
 // As many parts as give each of a B200's SMs a block: a number and not a question to the device, since the size query is for any device
