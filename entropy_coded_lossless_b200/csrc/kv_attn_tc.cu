@@ -215,9 +215,9 @@ __device__ __forceinline__ void find_part(const KvPages& c, const KvAttnArgs& a,
 __device__ __forceinline__ uint32_t parts_of(uint32_t tiles, uint32_t most) { return tiles > 3 ? min(most, tiles) : 1; }
 __device__ __forceinline__ uint32_t first_tile(uint32_t tiles, uint32_t parts, uint32_t rank) { return min(rank, parts) * tiles / parts; }
 
-// The parts' sums, sums of weights l, references m and exponents E of their rows lie in their blocks' shared memory. Each block of the cluster
-// joins 256 / ranks rows, a warp 16 / ranks of them, half of these at a time: 8 loads of 32 lanes (a row of a block each) are on
-// their way together.
+// The parts' sums, sums of weights l, references m and exponents E of their rows lie in their blocks' shared memory. Each block of
+// the cluster joins 256 / ranks rows, a warp 16 / ranks of them, half of these at a time: 8 loads of 32 lanes (a row of a block
+// each) are on their way together.
 //   out = sum O_i 2^(m_i - m + E_i - E) 2^E / sum l_i 2^(m_i - m)
 template <int D, typename F>
 __device__ __forceinline__ void join_parts(uint32_t base, uint32_t ranks, uint32_t parts, uint32_t tiles, uint32_t rank, uint32_t warp,
