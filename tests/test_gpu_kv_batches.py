@@ -72,3 +72,58 @@ def test_a_shrinking_batch_keeps_its_workspace(h, hk, prefix):
             kv.shn_kv_attn_shared(q[:n], cache, front, base.ints([prefix]), table[:n], lens, 0.1, o, x)
             assert base.status(x) == (0, 0)
         assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_captured_step_with_room_for_a_long_prefix(d):
+    """Which kernel the prefix takes is the room's: with room for a long one every length of it gives what a call without that room gives,
+    no prefix at all among them, and lengths that the room cannot hold are reported."""
+    pt, hk, h, n, room = 32, 2, 32, 70, 3200
+    own = [r * 37 % 90 for r in range(n)]
+    table, pages = base.shared_tables([room + x for x in own], 0, pt, 3)
+    cache = base.filled_cache(pages, hk, pt, d, seed=4)
+    q, plen, lens = base.bf16(n, h, d, seed=5), base.ints([0]), base.ints([0] * n)
+    front, out = table[0, :room // pt].contiguous(), rows(n, h, d)
+    shared = table.clone()
+    shared[:, :room // pt] = front
+    w = base.work(kv.attn_shared_workspace_bytes(cache, n, h))
+    args = (q, cache, front, plen, shared, lens, 0.1, out, w)
+    kv.shn_kv_attn_shared(*args)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv.shn_kv_attn_shared(*args)
+    for prefix in (0, 1, 31, 128, 1000, room):
+        lens.copy_(base.ints([prefix + x for x in own])), plen.copy_(base.ints([prefix])), out.fill_(7.0)
+        graph.replay()
+        assert base.status(w) == (0, 0)
+        ref, tol = base.spec.cache_attention(q, cache, lambda r: shared[r], [prefix + x for x in own], list(range(n + 1)), 0.1)
+        assert ((out.double() - ref).abs() <= tol).all()
+        assert (out[[r for r in range(n) if prefix + own[r] == 0]] == 0).all()
+    for prefix, held in ((-1, 0), (room + 1, room)):
+        plen.copy_(base.ints([prefix])), lens.copy_(base.ints([held + x for x in own]))
+        graph.replay()
+        assert base.status(w)[0] == shn.SHN_ERR_INVALID_ARG
+        ref, tol = base.spec.cache_attention(q, cache, lambda r: shared[r], [held + x for x in own], list(range(n + 1)), 0.1)
+        assert ((out.double() - ref).abs() <= tol).all()
+
+
+def test_many_single_tokens():
+    """Thousands of requests, more than any kernel has threads for, most of them short."""
+    n, hk, h, d, pt = 5000, 2, 4, 64, 16
+    lens = [r * 7 % 23 for r in range(n)]
+    lens[4321] = 3000
+    table, pages = base.tables(lens, pt, 1)
+    cache = base.filled_cache(pages, hk, pt, d, seed=2)
+    q, out, w = base.bf16(n, h, d, seed=3), rows(n, h, d), base.work(kv.attn_shared_workspace_bytes(cache, n, h))
+    kv.shn_kv_attn_shared(q, cache, None, base.ints([0]), table, base.ints(lens), 0.1, out, w)
+    assert base.status(w) == (0, 0)
+    again = rows(n, h, d)
+    kv.shn_kv_attn_prompt(q, cache, table, torch.arange(n + 1, dtype=torch.int32, device=DEV), base.ints(lens), 0.1, again, w)
+    assert base.status(w) == (0, 0)
+    some = [r for r in range(0, n, 250)] + [4321]
+    ref, tol = base.spec.cache_attention(q[some], cache, lambda i: table[some[i]], [lens[r] for r in some], list(range(len(some) + 1)), 0.1)
+    for o in (out, again):
+        assert ((o[some].double() - ref).abs() <= tol).all()
+        assert (o[[r for r in range(n) if lens[r] == 0]] == 0).all()
+    # both hold each result to 2^-11 of its parts and half a step of bfloat16: together below 2^-6 of the largest value
+    assert (out.double() - again.double()).abs().max() <= 2.0**-6 * out.double().abs().max()
